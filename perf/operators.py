@@ -347,8 +347,8 @@ def _own_conv(s):
         y = iga.causal_conv_step(s["x"], s["state"], s["w"], s["b"], silu=True, slots=s["slots"], state_out=s["state_out"])
         return {"y": y, "state": s["state_out"]}
     if s["mode"] == "prompt":
-        y, state = iga.causal_conv(s["x"], s["w"], s["b"], silu=True, offsets=s["offsets"], max_len=s["max_len"],
-                                   state=s["state"], state_out=s["state_out"])
+        y, state = iga.causal_conv(s["x"], s["w"], s["b"], silu=True, offsets=s["offsets"], state=s["state"],
+                                   state_out=s["state_out"])
         return {"y": y, "state": state}
     x = s["x"].unflatten(0, (s["S"], -1))
     y, _ = iga.causal_conv(x, s["w"], s["b"], silu=True)
