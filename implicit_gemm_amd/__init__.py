@@ -440,3 +440,16 @@ def wgrad(x, dy, R, S, pad=0, stride=1, dilation=1, groups=1, split_k=-1, dw=Non
     conv_wgrad2(d, x.data_ptr(), dy.data_ptr(), dw.data_ptr(), db.data_ptr() if bias else 0, ws_ptr, ws_len,
                 stream.cuda_stream)
     return (dw, db) if bias else dw
+
+
+_SEQUENCE = ("rms_norm", "rms_norm_e4m3", "rms_norm_grad", "causal_conv", "causal_conv_step", "causal_conv_grad",
+             "selective_scan", "selective_scan_step", "selective_scan_grad", "ScanGrads")
+
+
+def __getattr__(name):
+    # The sequence operators import torch, which this module leaves to the calls that need it.
+    if name in _SEQUENCE:
+        from . import sequence
+        globals().update({n: getattr(sequence, n) for n in _SEQUENCE})
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -1,0 +1,88 @@
+// What the forward scan and its gradient share: how the work is cut, and the carry between pieces.
+#pragma once
+
+#include "seq_common.h"
+
+namespace cw {
+
+// A sequence longer than one piece is scanned in three launches: every piece from a zero state (its end state and its
+// sum of D, as the product of its decays is e^(A sum D)), the carries of each sequence in order, and every piece again
+// from its carry with the outputs.  The gradient runs the same three over the reversed recurrence.
+struct ScanArgs {
+  seq_scan_args_t a;
+  seq_view_t dy;           // gradient only
+  const float* last;       // gradient only: dense gradient of the final states, or nullptr
+  SeqMap m;
+  int32_t pieces;
+  int32_t dblocks;         // blocks of 64 channels in a group
+  int32_t split;           // the carries are in `carry`
+  float* carry;            // [pieces][states][channels]
+  float* sums;             // [pieces][channels]: sum of D
+};
+
+constexpr int kWholeShift = 30;   // one piece a sequence
+
+struct ScanCut {
+  int shift;
+  bool split;
+};
+// Long sequences are split so that pieces x channel blocks come to about kScanWaves waves; a piece keeps 64 tokens.
+constexpr int64_t kScanWaves = 2048;
+ScanCut scan_cut(const seq_scan_args_t& a);
+inline int scan_dblocks(const seq_scan_args_t& a) { return (int)((a.channels / a.groups + 63) / 64); }
+inline int64_t scan_round(int64_t floats) { return (floats + 63) / 64 * 64; }
+
+// Pieces' aggregates and their combination; backward: over the reversed recurrence.
+hipError_t launch_scan_carry(const ScanArgs& k, bool backward, hipStream_t stream);
+
+// Tokens whose loads are issued together, and their elements of B (or C) a lane stages.
+constexpr int kScanTile = 8;
+
+// Rows [t, t + kScanTile) of one channel (a lane's own), clamped to the piece.
+template <typename T>
+struct ChannelTile {
+  T v[kScanTile];
+  __device__ __forceinline__ void load(const seq_view_t& view, const Piece& p, int t, int d) {
+#pragma unroll
+    for (int i = 0; i < kScanTile; ++i)
+      v[i] = row_at<const T>(view, p, min(max(t + i, p.t0), p.end - 1))[d];
+  }
+};
+
+// Rows [t, t + kScanTile) of B or C, widened, through registers into LDS ([token][NP]); zeros where there is none.
+template <typename T, int NP>
+struct StateTile {
+  static constexpr int kEach = kScanTile * NP / 64;
+  float v[kEach];
+  __device__ __forceinline__ void load(const seq_view_t& view, int64_t group_off, const Piece& p, int t, int N) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int e = i * 64 + ((int)threadIdx.x & 63), tok = t + e / NP, n = e % NP;
+      v[i] = 0.f;
+      if (n < N && tok >= p.t0 && tok < p.end) v[i] = to_f32(row_at<const T>(view, p, tok)[group_off + n]);
+    }
+  }
+  __device__ __forceinline__ void put(float* lds) const {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) lds[i * 64 + ((int)threadIdx.x & 63)] = v[i];
+  }
+};
+
+__device__ __forceinline__ float step_size(float delta, float bias, int32_t with_softplus) {
+  const float v = delta + bias;
+  return with_softplus ? softplus(v) : v;
+}
+
+// The element type and padded state count of a call as template arguments; FULL: no padded states.
+#define SCAN_DISPATCH_N(call, T, n)                                                               \
+  ((n) <= 8 ? ((n) == 8 ? call(T, 8, true) : call(T, 8, false))                                   \
+            : (n) <= 16 ? ((n) == 16 ? call(T, 16, true) : call(T, 16, false))                    \
+                        : ((n) == 32 ? call(T, 32, true) : call(T, 32, false)))
+#define SCAN_DISPATCH(call, dtype, n)                                                             \
+  switch (dtype) {                                                                                \
+    case CONV_WGRAD_F32: return SCAN_DISPATCH_N(call, float, n);                                  \
+    case CONV_WGRAD_BF16: return SCAN_DISPATCH_N(call, Bf16, n);                                  \
+    default: return SCAN_DISPATCH_N(call, F16, n);                                                \
+  }
+
+}  // namespace cw

@@ -1,0 +1,399 @@
+// Selective state space scan for prompts and for one token of each sequence (gfx950).
+//
+//   D = softplus(delta + bias),  h[t] = e^(D A) h[t - 1] + D u B[t],  y = (sum_n h C[t] + skip u) z sigmoid(z)
+//
+// Bound by the vector ALU: every (token, channel, state) costs one exponential (a quarter-rate instruction) and four
+// multiply-adds, 16 states to the 8 bytes that a token and channel move.  A lane owns one channel with all its states
+// in registers, so the sum over states stays in the lane; a wave owns 64 channels and one piece of a sequence, with
+// B and C of its tokens broadcast from LDS in fp32.  Channels alone give a long prompt too few waves, so its tokens
+// are split as well (seq_scan.h).
+#include "seq_scan.h"
+
+namespace cw {
+
+namespace {
+
+// Channel of this lane within its group's blocks; lanes past the group's end repeat its last channel.
+struct Lane {
+  int d;
+  int g;
+  bool on;
+};
+__device__ __forceinline__ Lane lane_channel(const ScanArgs& k, int block) {
+  const int Dg = (int)(k.a.channels / k.a.groups);
+  const int c = (block % k.dblocks) * 64 + ((int)threadIdx.x & 63);
+  const int g = block / k.dblocks;
+  return Lane{g * Dg + min(c, Dg - 1), g, c < Dg};
+}
+
+template <int NP>
+__device__ __forceinline__ void load_decay(const seq_scan_args_t& a, int d, float (&A2)[NP]) {
+#pragma unroll
+  for (int n = 0; n < NP; ++n) A2[n] = n < a.states ? a.A[(int64_t)d * a.states + n] * kLog2e : 0.f;
+}
+
+template <typename T, int NP, bool FULL>
+__global__ __launch_bounds__(64) void scan_kernel(ScanArgs k) {
+  __shared__ __align__(16) float lb[2][kScanTile * NP], lc[2][kScanTile * NP];
+  const seq_scan_args_t& a = k.a;
+  const int blocks = k.dblocks * (int)a.groups;
+  const int piece = (int)blockIdx.x / blocks;
+  const Lane l = lane_channel(k, (int)blockIdx.x % blocks);
+  Piece p;
+  if (!find_piece(k.m, piece, p)) return;
+  if (p.seq >= k.m.S) {
+    T zero;
+    from_f32(0.f, zero);
+    for (int t = p.t0; t < p.end; ++t)
+      if (l.on) row_at<T>(a.y, p, t)[l.d] = zero;
+    return;
+  }
+  const int N = a.states, D = (int)a.channels;
+  const int64_t slot = pool_slot(a.tokens.slots, a.tokens.pool, p.seq);
+  float A2[NP], h[NP];
+  load_decay<NP>(a, l.d, A2);
+  const float bias = a.delta_bias ? a.delta_bias[l.d] : 0.f;
+  const float skip = a.skip ? a.skip[l.d] : 0.f;
+#pragma unroll
+  for (int n = 0; n < NP; ++n) {
+    h[n] = 0.f;
+    if (FULL || n < N) {
+      if (k.split) h[n] = k.carry[((int64_t)piece * N + n) * D + l.d];
+      else if (a.state && slot >= 0) h[n] = a.state[slot * a.state_stride + (int64_t)l.d * N + n];
+    }
+  }
+  // Where the states of this sequence's 16-token tiles are saved.
+  const int64_t tile0 = k.m.offsets ? (p.first >> kSaveShift) + p.seq
+                                    : (int64_t)p.seq * (((k.m.rows - 1) >> kSaveShift) + 1);
+  if (p.end > p.t0) {
+    const int64_t gb = l.g * a.B_group, gc = l.g * a.C_group;
+    ChannelTile<T> u, dl, z, nu, ndl, nz;
+    StateTile<T, NP> sb, sc;
+    nu.load(a.u, p, p.t0, l.d);
+    ndl.load(a.delta, p, p.t0, l.d);
+    if (a.z.ptr) nz.load(a.z, p, p.t0, l.d);
+    sb.load(a.B, gb, p, p.t0, N);
+    sc.load(a.C, gc, p, p.t0, N);
+    int buf = 0;
+    for (int t = p.t0; t < p.end; t += kScanTile, buf ^= 1) {
+      sb.put(lb[buf]);
+      sc.put(lc[buf]);
+      u = nu;
+      dl = ndl;
+      z = nz;
+      __syncthreads();
+      nu.load(a.u, p, t + kScanTile, l.d);
+      ndl.load(a.delta, p, t + kScanTile, l.d);
+      if (a.z.ptr) nz.load(a.z, p, t + kScanTile, l.d);
+      sb.load(a.B, gb, p, t + kScanTile, N);
+      sc.load(a.C, gc, p, t + kScanTile, N);
+      if (a.save && (t & ((1 << kSaveShift) - 1)) == 0 && l.on) {
+        float* s = a.save + ((tile0 + (t >> kSaveShift)) * D + l.d) * N;
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+          if (FULL || n < N) s[n] = h[n];
+      }
+#pragma unroll
+      for (int i = 0; i < kScanTile; ++i) {
+        if (t + i < p.end) {
+          const float uv = to_f32(u.v[i]);
+          const float dt = step_size(to_f32(dl.v[i]), bias, a.softplus);
+          const float x = dt * uv;
+          float o[2] = {0.f, 0.f};
+#pragma unroll
+          for (int n = 0; n < NP; ++n)
+            if (FULL || n < N) {
+              const float e = __builtin_amdgcn_exp2f(dt * A2[n]);
+              h[n] = __builtin_fmaf(e, h[n], x * lb[buf][i * NP + n]);
+              o[n & 1] = __builtin_fmaf(h[n], lc[buf][i * NP + n], o[n & 1]);
+            }
+          float y = __builtin_fmaf(skip, uv, o[0] + o[1]);
+          if (a.z.ptr) {
+            const float zv = to_f32(z.v[i]);
+            y *= zv * sigmoid(zv);
+          }
+          if (l.on) from_f32(y, row_at<T>(a.y, p, t + i)[l.d]);
+        }
+      }
+    }
+  }
+  if (a.state_out && p.end == p.len && slot >= 0 && l.on) {
+    float* s = a.state_out + slot * a.state_out_stride + (int64_t)l.d * N;
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+      if (FULL || n < N) s[n] = h[n];
+  }
+}
+
+// A piece from a zero carry.  Forward: its end state.  Backward: what its first token passes to the token before,
+// from g[t] = dy z sigmoid(z) C[t] + c, c = e^(D A) g[t].  The last (first) piece of a sequence passes nothing on.
+template <typename T, int NP, bool FULL, bool BACK>
+__global__ __launch_bounds__(64) void scan_carry_kernel(ScanArgs k) {
+  __shared__ __align__(16) float lds[2][kScanTile * NP];
+  const seq_scan_args_t& a = k.a;
+  const int blocks = k.dblocks * (int)a.groups;
+  const int piece = (int)blockIdx.x / blocks;
+  const Lane l = lane_channel(k, (int)blockIdx.x % blocks);
+  Piece p;
+  if (!find_piece(k.m, piece, p) || p.seq >= k.m.S) return;
+  if (p.end == p.t0 || (BACK ? p.t0 == 0 : p.end == p.len)) return;
+  const int N = a.states, D = (int)a.channels;
+  float A2[NP], c[NP], sum = 0.f;
+  load_decay<NP>(a, l.d, A2);
+  const float bias = a.delta_bias ? a.delta_bias[l.d] : 0.f;
+#pragma unroll
+  for (int n = 0; n < NP; ++n) c[n] = 0.f;
+  const seq_view_t in = BACK ? k.dy : a.u, side = BACK ? a.C : a.B;
+  const int64_t goff = l.g * (BACK ? a.C_group : a.B_group);
+  const int tiles = (p.end - p.t0 + kScanTile - 1) / kScanTile;
+  ChannelTile<T> u, dl, z, nu, ndl, nz;
+  StateTile<T, NP> s;
+  const int t1 = BACK ? p.t0 + (tiles - 1) * kScanTile : p.t0;
+  nu.load(in, p, t1, l.d);
+  ndl.load(a.delta, p, t1, l.d);
+  if (BACK && a.z.ptr) nz.load(a.z, p, t1, l.d);
+  s.load(side, goff, p, t1, N);
+  for (int j = 0; j < tiles; ++j) {
+    const int t = BACK ? t1 - j * kScanTile : t1 + j * kScanTile;
+    const int next = BACK ? t - kScanTile : t + kScanTile;
+    s.put(lds[j & 1]);
+    u = nu;
+    dl = ndl;
+    z = nz;
+    __syncthreads();
+    nu.load(in, p, next, l.d);
+    ndl.load(a.delta, p, next, l.d);
+    if (BACK && a.z.ptr) nz.load(a.z, p, next, l.d);
+    s.load(side, goff, p, next, N);
+#pragma unroll
+    for (int q = 0; q < kScanTile; ++q) {
+      const int i = BACK ? kScanTile - 1 - q : q;
+      if (t + i < p.end) {
+        const float dt = step_size(to_f32(dl.v[i]), bias, a.softplus);
+        float x = to_f32(u.v[i]);
+        sum += dt;
+        if constexpr (BACK) {
+          if (a.z.ptr) {
+            const float zv = to_f32(z.v[i]);
+            x *= zv * sigmoid(zv);
+          }
+        } else {
+          x *= dt;
+        }
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+          if (FULL || n < N) {
+            const float e = __builtin_amdgcn_exp2f(dt * A2[n]);
+            const float b = x * lds[j & 1][i * NP + n];
+            c[n] = BACK ? e * (c[n] + b) : __builtin_fmaf(e, c[n], b);
+          }
+      }
+    }
+  }
+  if (l.on) {
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+      if (FULL || n < N) k.carry[((int64_t)piece * N + n) * D + l.d] = c[n];
+    k.sums[(int64_t)piece * D + l.d] = sum;
+  }
+}
+
+// The carry into every piece of a sequence, in place of the pieces' aggregates; a lane owns one channel and state.
+template <bool BACK>
+__global__ __launch_bounds__(64) void scan_join_kernel(ScanArgs k) {
+  constexpr int kAhead = 8;   // pieces whose aggregates are loaded together
+  const seq_scan_args_t& a = k.a;
+  const int N = a.states, D = (int)a.channels;
+  const int dblocks = (D + 63) / 64;
+  const int db = (int)blockIdx.x % dblocks, n = (int)blockIdx.x / dblocks % N, s = (int)blockIdx.x / dblocks / N;
+  const int d = db * 64 + (int)threadIdx.x;
+  if (d >= D) return;
+  int first, len;
+  if (k.m.offsets) {
+    const int start = seq_start(k.m, s);
+    first = (start >> k.m.shift) + s;
+    len = max(seq_start(k.m, s + 1) - start, 0);
+  } else {
+    first = s * k.m.per;
+    len = k.m.rows;
+  }
+  const int count = max(1, ((len - 1) >> k.m.shift) + 1);   // len 0: one piece
+  const float A2 = a.A[(int64_t)d * N + n] * kLog2e;
+  float h = 0.f;
+  if (BACK) {
+    if (k.last) h = k.last[((int64_t)s * D + d) * N + n];
+  } else {
+    const int64_t slot = pool_slot(a.tokens.slots, a.tokens.pool, s);
+    if (a.state && slot >= 0) h = a.state[slot * a.state_stride + (int64_t)d * N + n];
+  }
+  for (int j0 = 0; j0 < count; j0 += kAhead) {
+    float e[kAhead], sum[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i;
+      if (j < count - 1) {   // the last one's aggregate is not needed
+        const int64_t q = first + (BACK ? count - 1 - j : j);
+        e[i] = k.carry[(q * N + n) * D + d];
+        sum[i] = k.sums[q * D + d];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i;
+      if (j < count) {
+        const int64_t q = first + (BACK ? count - 1 - j : j);
+        k.carry[(q * N + n) * D + d] = h;
+        if (j < count - 1) h = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * sum[i]), h, e[i]);
+      }
+    }
+  }
+}
+
+// One token of each sequence: NP / 4 lanes a channel with four states each, so that the states of a wave's channels
+// are one contiguous read and write of 16 bytes a lane.  Bound by those bytes.
+template <typename T, int NP, bool FULL>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs k) {
+  constexpr int NG = NP / 4, kChannels = 256 / NG;
+  const seq_scan_args_t& a = k.a;
+  const int N = a.states, D = (int)a.channels;
+  const int blocks = (D + kChannels - 1) / kChannels;
+  const int s = (int)blockIdx.x / blocks;
+  const int c = ((int)blockIdx.x % blocks) * kChannels + (int)threadIdx.x / NG;
+  const int n0 = ((int)threadIdx.x % NG) * 4;
+  const bool on = c < D;
+  const int d = min(c, D - 1);
+  const int g = d / (D / (int)a.groups);
+  const int64_t slot = pool_slot(a.tokens.slots, a.tokens.pool, s);
+  const int nv = N - n0;   // states of this lane, <= 0: none
+  Raw<float, 4> A, h;
+  Raw<T, 4> B, C;
+  A.clear();
+  h.clear();
+  B.clear();
+  C.clear();
+  if (FULL || nv > 0) {
+    const int v = FULL ? 4 : nv;
+    if (a.state && slot >= 0) h.load_n(a.state + slot * a.state_stride + (int64_t)d * N + n0, v);
+    A.load_n(a.A + (int64_t)d * N + n0, v);
+    B.load_n(static_cast<const T*>(a.B.ptr) + s * a.B.batch + g * a.B_group + n0, v);
+    C.load_n(static_cast<const T*>(a.C.ptr) + s * a.C.batch + g * a.C_group + n0, v);
+  }
+  const float u = to_f32(static_cast<const T*>(a.u.ptr)[s * a.u.batch + d]);
+  const float delta = to_f32(static_cast<const T*>(a.delta.ptr)[s * a.delta.batch + d]);
+  const float dt = step_size(delta, a.delta_bias ? a.delta_bias[d] : 0.f, a.softplus);
+  const float x = dt * u;
+  float o = 0.f, out[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    out[i] = 0.f;
+    if (FULL || i < nv) {
+      out[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * (A.get(i) * kLog2e)), h.get(i), x * B.get(i));
+      o = __builtin_fmaf(out[i], C.get(i), o);
+    }
+  }
+  o = lanes_reduce<AddOp>(o, NG);
+  if (!on) return;
+  if (a.state_out && slot >= 0 && (FULL || nv > 0)) {
+    h.pack(out);
+    h.store_n(a.state_out + slot * a.state_out_stride + (int64_t)d * N + n0, FULL ? 4 : nv);
+  }
+  if (n0 == 0) {
+    float y = __builtin_fmaf(a.skip ? a.skip[d] : 0.f, u, o);
+    if (a.z.ptr) {
+      const float zv = to_f32(static_cast<const T*>(a.z.ptr)[s * a.z.batch + d]);
+      y *= zv * sigmoid(zv);
+    }
+    from_f32(y, static_cast<T*>(a.y.ptr)[s * a.y.batch + d]);
+  }
+}
+
+template <typename T, int NP, bool FULL>
+hipError_t scan_t(const ScanArgs& k, hipStream_t stream) {
+  const int64_t grid = (int64_t)k.pieces * k.dblocks * k.a.groups;
+  return launch_kernel(scan_kernel<T, NP, FULL>, dim3((unsigned)grid), dim3(64), k, stream);
+}
+
+template <typename T, int NP, bool FULL>
+hipError_t carry_t(const ScanArgs& k, bool back, hipStream_t stream) {
+  const int64_t grid = (int64_t)k.pieces * k.dblocks * k.a.groups;
+  if (back) return launch_kernel(scan_carry_kernel<T, NP, FULL, true>, dim3((unsigned)grid), dim3(64), k, stream);
+  return launch_kernel(scan_carry_kernel<T, NP, FULL, false>, dim3((unsigned)grid), dim3(64), k, stream);
+}
+
+template <typename T, int NP, bool FULL>
+hipError_t step_t(const ScanArgs& k, hipStream_t stream) {
+  constexpr int kChannels = 256 / (NP / 4);
+  const int64_t grid = (k.a.channels + kChannels - 1) / kChannels * k.a.tokens.sequences;
+  return launch_kernel(scan_step_kernel<T, NP, FULL>, dim3((unsigned)grid), dim3(256), k, stream);
+}
+
+hipError_t scan_any(const ScanArgs& k, hipStream_t stream) {
+#define CALL(T, NP, FULL) scan_t<T, NP, FULL>(k, stream)
+  SCAN_DISPATCH(CALL, k.a.dtype, k.a.states)
+#undef CALL
+}
+
+hipError_t carry_any(const ScanArgs& k, bool back, hipStream_t stream) {
+#define CALL(T, NP, FULL) carry_t<T, NP, FULL>(k, back, stream)
+  SCAN_DISPATCH(CALL, k.a.dtype, k.a.states)
+#undef CALL
+}
+
+}  // namespace
+
+ScanCut scan_cut(const seq_scan_args_t& a) {
+  const int64_t waves = (int64_t)scan_dblocks(a) * a.groups;
+  const int64_t rows = seq_rows(a.tokens);
+  int64_t longest = a.tokens.rows;
+  if (a.tokens.offsets && a.longest > 0 && a.longest < longest) longest = a.longest;
+  int shift = 6;
+  while (shift < kWholeShift && (rows >> shift) * waves > kScanWaves) ++shift;
+  if (longest <= ((int64_t)1 << shift)) return ScanCut{kWholeShift, false};
+  return ScanCut{shift, true};
+}
+
+int64_t scan_save_floats(const seq_scan_args_t& a) {
+  return seq_pieces(seq_map(a.tokens, kSaveShift)) * a.channels * a.states;
+}
+
+int64_t scan_ws_floats(const seq_scan_args_t& a) {
+  const ScanCut cut = scan_cut(a);
+  if (!cut.split) return 0;
+  const int64_t pieces = seq_pieces(seq_map(a.tokens, cut.shift));
+  return scan_round(pieces * a.channels * a.states) + scan_round(pieces * a.channels);
+}
+
+hipError_t launch_scan_carry(const ScanArgs& k, bool backward, hipStream_t stream) {
+  const hipError_t err = carry_any(k, backward, stream);
+  if (err != hipSuccess) return err;
+  const int64_t grid = (k.a.channels + 63) / 64 * k.a.states * k.a.tokens.sequences;
+  if (backward) return launch_kernel(scan_join_kernel<true>, dim3((unsigned)grid), dim3(64), k, stream);
+  return launch_kernel(scan_join_kernel<false>, dim3((unsigned)grid), dim3(64), k, stream);
+}
+
+hipError_t launch_scan(const seq_scan_args_t& a, float* ws, hipStream_t stream) {
+  const ScanCut cut = scan_cut(a);
+  ScanArgs k{};
+  k.a = a;
+  k.m = seq_map(a.tokens, cut.shift);
+  k.pieces = (int32_t)seq_pieces(k.m);
+  k.dblocks = scan_dblocks(a);
+  k.split = cut.split;
+  if (cut.split) {
+    k.carry = ws;
+    k.sums = ws + scan_round((int64_t)k.pieces * a.channels * a.states);
+    const hipError_t err = launch_scan_carry(k, false, stream);
+    if (err != hipSuccess) return err;
+  }
+  return scan_any(k, stream);
+}
+
+hipError_t launch_scan_step(const seq_scan_args_t& a, hipStream_t stream) {
+  ScanArgs k{};
+  k.a = a;
+#define CALL(T, NP, FULL) step_t<T, NP, FULL>(k, stream)
+  SCAN_DISPATCH(CALL, a.dtype, a.states)
+#undef CALL
+}
+
+}  // namespace cw

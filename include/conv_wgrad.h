@@ -408,6 +408,200 @@ conv_wgrad_status_t conv_igemm_call_timed(const conv_wgrad_desc2_t* desc, int32_
 conv_wgrad_status_t conv_wgrad_noalloc(const conv_wgrad_desc_t* desc, const void* x, const void* dy,
                                        float* dw, float* db, void* stream);
 
+/* ------------------------------------------------------------------------------------------------------------------
+ * Sequence operators: the root-mean-square norm, the short causal (depthwise) convolution over tokens and the selective
+ * state space scan, which together with two matrix products make a layer of a sequence model.  Tokens are rows,
+ * channels the contiguous axis; element types as above (desc dtype), arithmetic and every sum in fp32.
+ *
+ * Execution is as for the convolutions: validation is synchronous and comes before anything is enqueued, the kernels
+ * go to `stream`, nothing is allocated, and results are bit-identical from run to run.  The one thing validation
+ * cannot see is the content of device arrays: any offsets and slots are memory-safe (see seq_tokens_t).
+ */
+
+/* A tensor of rows: element (b, t, c) is at ptr + b * batch + t * row + c, strides in elements, >= 0 (0: the same row
+ * for all).  Element alignment suffices. */
+typedef struct seq_view {
+  void* ptr;
+  int64_t batch, row;
+} seq_view_t;
+
+/*
+ * How rows make up sequences.
+ *   offsets NULL : `sequences` sequences of `rows` tokens each; sequence s is batch index s.
+ *   offsets      : device int32 [sequences + 1], offsets[0] = 0, not decreasing: sequence s is rows offsets[s] ..
+ *                  offsets[s + 1] - 1 of `rows` in all (batch index 0).  Rows from offsets[sequences] on are padding:
+ *                  their outputs are zero.  Offsets that break these rules give outputs without meaning, in bounds.
+ *   slots        : device int32 [sequences] or NULL (s itself): where sequence s has its state in a pool of `pool`
+ *                  states.  A slot outside [0, pool) stands for no state: it reads as zeros and is not written.
+ *                  Two sequences with one slot race on it.
+ */
+typedef struct seq_tokens {
+  int64_t sequences, rows;
+  const int32_t* offsets;
+  const int32_t* slots;
+  int64_t pool;
+} seq_tokens_t;
+
+/*
+ * y = h r w,  h = x + residual rounded to the element type,  r = 1 / sqrt(mean(h^2) + eps), per row.
+ *   x, residual : rows x channels (residual NULL: h = x); row strides in elements
+ *   w           : fp32 [channels]
+ *   y, h, rstd  : dense outputs; h may be NULL (not needed), rstd fp32 [rows] or NULL.
+ * 1 <= channels <= 16384, rows >= 0.
+ */
+typedef struct seq_norm_args {
+  int64_t rows, channels;
+  int32_t dtype;
+  int32_t group;          /* seq_rms_norm_e4m3: channels per scale (0: the row; 32, 64, 128, 256) */
+  float eps;
+  int32_t reserved;
+  const void* x;
+  int64_t x_row;
+  const void* residual;
+  int64_t residual_row;
+  const float* w;
+  void* y;                /* seq_rms_norm_e4m3: 8-bit [rows][channels] */
+  void* h;
+  float* rstd;
+  float* scale;           /* seq_rms_norm_e4m3: [rows][ceil(channels / group)] */
+} seq_norm_args_t;
+
+conv_wgrad_status_t seq_rms_norm(const seq_norm_args_t* args, void* stream);
+
+/* The norm with an 8-bit output (OCP e4m3, largest value 448): per group of channels scale = max|h r w| / 448 (1 where
+ * that is zero) and y = e4m3(h r w / scale), rounded to nearest even. */
+conv_wgrad_status_t seq_rms_norm_e4m3(const seq_norm_args_t* args, void* stream);
+
+/*
+ * Gradients of seq_rms_norm:  dx = r (dy w - h r^2 mean(dy w h)) + dh  (also the residual's gradient) and
+ * dw = sum over rows of dy h r.  h and rstd are the forward's (h = x without a residual).
+ *   dh : gradient that reaches h by another way, or NULL
+ *   workspace : 16-byte aligned, seq_rms_norm_grad_workspace bytes
+ */
+typedef struct seq_norm_grad_args {
+  int64_t rows, channels;
+  int32_t dtype;
+  int32_t reserved;
+  const void* dy;
+  int64_t dy_row;
+  const void* h;
+  int64_t h_row;
+  const void* dh;
+  int64_t dh_row;
+  const float* w;
+  const float* rstd;
+  void* dx;               /* [rows][channels] */
+  float* dw;              /* [channels] */
+} seq_norm_grad_args_t;
+
+conv_wgrad_status_t seq_rms_norm_grad_workspace(const seq_norm_grad_args_t* args, size_t* bytes);
+conv_wgrad_status_t seq_rms_norm_grad(const seq_norm_grad_args_t* args, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Short causal convolution, one filter of `width` taps per channel:
+ *   p[t, d] = bias[d] + sum_k w[d, k] x[t - (width - 1) + k, d],   y = p  or, with silu, p / (1 + e^-p).
+ * Before a sequence's first token x is its state: [pool][width - 1][channels], the last width - 1 inputs, oldest first
+ * (NULL: zeros).  state_out receives the window after the last token (NULL: not needed); it is `state` itself or does
+ * not overlap it.  State strides are elements between two states of a pool.
+ * 2 <= width <= 4; w fp32 [channels][width], bias fp32 [channels] or NULL.
+ */
+typedef struct seq_conv_args {
+  seq_tokens_t tokens;
+  int64_t channels;
+  int32_t width, dtype, silu, reserved;
+  seq_view_t x;
+  const float* w;
+  const float* bias;
+  const void* state;
+  int64_t state_stride;
+  void* state_out;
+  int64_t state_out_stride;
+  seq_view_t y;
+} seq_conv_args_t;
+
+conv_wgrad_status_t seq_causal_conv(const seq_conv_args_t* args, void* stream);
+
+/* The same for one token of each sequence (tokens.offsets NULL, tokens.rows 1); the window of a slot is read and
+ * written by the same lane, so state_out may be state. */
+conv_wgrad_status_t seq_causal_conv_step(const seq_conv_args_t* args, void* stream);
+
+/* Gradients: dx, dw, dbias (NULL: not needed) and dstate (dense [sequences][width - 1][channels], NULL: not needed)
+ * from dy and dstate_out (the same shape; gradient of the outgoing windows, NULL: zero).  fwd.y, fwd.state_out and
+ * their strides are not read. */
+typedef struct seq_conv_grad_args {
+  seq_conv_args_t fwd;
+  seq_view_t dy;
+  const void* dstate_out;
+  seq_view_t dx;
+  float* dw;
+  float* dbias;
+  void* dstate;
+} seq_conv_grad_args_t;
+
+conv_wgrad_status_t seq_causal_conv_grad_workspace(const seq_conv_grad_args_t* args, size_t* bytes);
+conv_wgrad_status_t seq_causal_conv_grad(const seq_conv_grad_args_t* args, void* workspace, size_t ws_bytes,
+                                         void* stream);
+
+/*
+ * Selective state space scan.  Per sequence, channel d and state n, with g = d / (channels / groups):
+ *   D[t, d] = delta[t, d] + delta_bias[d], with softplus: log(1 + e^that)
+ *   h[t, d, n] = e^(D A[d, n]) h[t - 1, d, n] + D u[t, d] B[t, g, n]
+ *   y[t, d] = (sum_n h[t, d, n] C[t, g, n] + skip[d] u[t, d]) * (z / (1 + e^-z), z = z[t, d])
+ * A fp32 [channels][states]; skip, delta_bias fp32 [channels] or NULL; z.ptr NULL: no gate.  B and C: element
+ * (b, t, g, n) at ptr + b * batch + t * row + g * group_stride + n.
+ * state, state_out: fp32 [pool][channels][states] (stride elements apart), NULL: zeros / not needed; they may be the
+ * same.  save: NULL, or what seq_selective_scan_grad needs, seq_selective_scan_save bytes.
+ * longest: no sequence is longer (<= 0: not known); a hint for the split of long sequences, results do not depend on
+ * its being right.  1 <= states <= 32.
+ */
+typedef struct seq_scan_args {
+  seq_tokens_t tokens;
+  int64_t channels, groups;
+  int32_t states, dtype, softplus, reserved;
+  int64_t longest;
+  seq_view_t u, delta, z, B, C;
+  int64_t B_group, C_group;
+  const float* A;
+  const float* skip;
+  const float* delta_bias;
+  const float* state;
+  int64_t state_stride;
+  float* state_out;
+  int64_t state_out_stride;
+  float* save;
+  seq_view_t y;
+} seq_scan_args_t;
+
+conv_wgrad_status_t seq_selective_scan_save(const seq_scan_args_t* args, size_t* bytes);
+conv_wgrad_status_t seq_selective_scan_workspace(const seq_scan_args_t* args, size_t* bytes);
+conv_wgrad_status_t seq_selective_scan(const seq_scan_args_t* args, void* workspace, size_t ws_bytes, void* stream);
+
+/* The same for one token of each sequence (tokens.offsets NULL, tokens.rows 1). */
+conv_wgrad_status_t seq_selective_scan_step(const seq_scan_args_t* args, void* stream);
+
+/* Gradients, from dy, dstate_out (dense fp32 [sequences][channels][states], gradient of the final states, NULL: zero)
+ * and fwd.save as the forward filled it.  Outputs dense: du, ddelta, dz (NULL without a gate) rows x channels, dB and
+ * dC rows x groups x states, dA, dskip and ddelta_bias fp32 (the last two may be NULL), dstate fp32 [sequences]
+ * [channels][states] or NULL.  fwd.y, fwd.state and fwd.state_out are not read. */
+typedef struct seq_scan_grad_args {
+  seq_scan_args_t fwd;
+  seq_view_t dy;
+  const float* dstate_out;
+  void* du;
+  void* ddelta;
+  void* dz;
+  void* dB;
+  void* dC;
+  float* dA;
+  float* dskip;
+  float* ddelta_bias;
+  float* dstate;
+} seq_scan_grad_args_t;
+
+conv_wgrad_status_t seq_selective_scan_grad_workspace(const seq_scan_grad_args_t* args, size_t* bytes);
+conv_wgrad_status_t seq_selective_scan_grad(const seq_scan_grad_args_t* args, void* workspace, size_t ws_bytes,
+                                            void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,508 @@
+"""Sequence operators on the GPU against their 64-bit definitions (sequence_ref).
+
+Tolerances: one rounding of the output type plus c roundings in 32 bits of the largest magnitude.  A norm's row sums
+pass through at most 64 additions a lane and 8 between lanes, a gradient's dw through at most 64 rows a chain and 32
+joins; a scan's state after t tokens has t roundings of its product, t of its sums, and the exponentials' (about 8
+roundings each, the step size's among them), so c = 16 + 12 t, t at most the sequence's length; its gradients pass
+through two such chains and a sum over tokens and channels."""
+import random
+
+import pytest
+import torch
+
+import sequence_ref as ref
+from gpu_util import log
+from sequence_ref import DT, close, leaf
+
+pytestmark = pytest.mark.gpu
+TYPES = ["f32", "bf16", "f16"]
+
+
+@pytest.fixture(scope="module")
+def iga():
+    import implicit_gemm_amd
+    return implicit_gemm_amd
+
+
+def gen(seed):
+    g = torch.Generator().manual_seed(seed)
+
+    def rand(*shape, std=1.0, dtype=torch.float32):
+        return (torch.randn(*shape, generator=g) * std).to(dtype)
+
+    return rand
+
+
+def strided(t, pad):
+    """The same values as a part of wider rows."""
+    wide = torch.full(t.shape[:-1] + (t.shape[-1] + pad,), 7.0, dtype=t.dtype)
+    wide[..., pad:] = t
+    return wide.cuda()[..., pad:]
+
+
+# ---------------------------------------------------------------------------------------------------------- norm
+
+NORM_SHAPES = [(1, 1), (3, 7), (5, 64), (1, 257), (1100, 300), (1030, 1024), (2, 1537), (1025, 2048), (2, 4100), (3, 8192),
+               (2, 16384), (0, 64), (1, 16383)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,C", NORM_SHAPES)
+def test_norm_and_gradient(iga, rows, C, dtype):
+    log("norm", rows, C, dtype)
+    rand, dt = gen(rows * 31 + C), DT[dtype]
+    x, res, dy, dh = (rand(rows, C, dtype=dt) for _ in range(4))
+    w = rand(C)
+    if rows > 1:
+        x[1] = 0
+        res[1] = 0                      # a row of zeros: r = eps^-1/2
+    with_res = C % 2 == 0
+    xd = strided(x, 3) if C < 5000 else x.cuda()
+    y, h, r = iga.rms_norm(xd, w.cuda(), residual=res.cuda() if with_res else None, eps=1e-5)
+    hr = ref.norm(x, res if with_res else None, w, 1e-5)[1]
+    assert torch.equal(h.cpu(), hr)
+    if not with_res:
+        assert h is xd
+    hl, wl = leaf(hr), leaf(w)
+    yr, _, rr = ref.norm(hl, None, wl, 1e-5)
+    close(y, yr, dt, 96, "y")
+    close(r, rr, torch.float32, 96, "r", scale=rr.detach())
+    for dhx in (None, dh):
+        dx, dw = iga.rms_norm_grad(strided(dy, 5), h, w.cuda(), r, dh=dhx.cuda() if dhx is not None else None)
+        dxr, dwr = ref.grads((yr,), (dy.double(),), (hl, wl)) if rows else (hl, torch.zeros(C))
+        if dhx is not None:
+            dxr = dxr + dhx.double()
+        # the rows of zeros have r = 316, so each row is measured against its own largest terms
+        top = ((dy.double() * w.double()).abs().amax(1, keepdim=True) * rr.detach()[:, None] * 2 + 4) if rows else None
+        close(dx, dxr, dt, 160, "dx", scale=top)
+        close(dw, dwr, torch.float32, 256 + rows, "dw")
+        yr, _, rr = ref.norm(hl, None, wl, 1e-5)
+
+
+def e4m3_expected(y, group):
+    """Scales and the values q stands for, before their rounding."""
+    M, C = y.shape
+    g = group or C
+    scale = torch.stack([p.abs().amax(1) / 448 for p in y.split(g, 1)], 1)
+    scale = torch.where(scale == 0, torch.ones_like(scale), scale)
+    return scale, y / scale.repeat_interleave(g, 1)[:, :C]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,C,group", [(3, 300, 0), (2, 300, 32), (5, 300, 64), (1, 2048, 128), (1100, 520, 256),
+                                          (1027, 1537, 128), (2, 7, 32), (1, 16384, 256), (2, 5000, 0), (0, 128, 128)])
+def test_norm_e4m3(iga, rows, C, group, dtype):
+    log("norm e4m3", rows, C, group, dtype)
+    rand, dt = gen(rows + C + group), DT[dtype]
+    x, res, w = rand(rows, C, dtype=dt), rand(rows, C, dtype=dt, std=2.0), rand(C)
+    if rows > 1:
+        x[1] = 0
+        res[1] = 0
+    q, scale, h = iga.rms_norm_e4m3(strided(x, 1), w.cuda(), residual=res.cuda(), group=group)
+    y, hr, _ = ref.norm(x, res, w, 1e-5)
+    assert torch.equal(h.cpu(), hr) and q.dtype == torch.float8_e4m3fn
+    if rows == 0:
+        assert q.shape == (0, C) and scale.shape == (0, -(-C // (group or C)))
+        return
+    sr, qr = e4m3_expected(y, group)
+    close(scale, sr, torch.float32, 100, "scale", scale=sr)
+    # half a step of e4m3: 2^-4 of the value, 2^-10 below the smallest normal number (2^-6); and the scale's error
+    err = (q.cpu().double() - qr).abs()
+    assert (err <= qr.abs() * (2.0 ** -4 + 200 * ref.EPS32) + 2.0 ** -10).all()
+    assert q.cpu().float().abs().max() <= 448
+
+
+def test_norm_keeps_nan_and_infinity_in_their_row(iga):
+    x = torch.ones(3, 256)
+    x[0, 5] = float("nan")
+    x[1, 7] = float("inf")
+    y, h, r = iga.rms_norm(x.cuda(), torch.ones(256).cuda())
+    assert y[0].isnan().all() and y[1, 7].isnan() and bool((y[1, :7] == 0).all()) and bool(torch.isfinite(y[2]).all())
+    q, scale, _ = iga.rms_norm_e4m3(x.cuda(), torch.ones(256).cuda(), group=128)
+    assert scale[0].isnan().all() and scale[1, 0].isnan() and bool(torch.isfinite(scale[2]).all())
+
+
+def test_norm_of_higher_rank_and_its_refusals(iga):
+    rand = gen(1)
+    x = rand(2, 3, 5, 64).cuda()
+    w = rand(64).cuda()
+    y, _, r = iga.rms_norm(x, w)
+    assert y.shape == x.shape and r.shape == (2, 3, 5)
+    assert torch.equal(y.view(-1, 64), iga.rms_norm(x.view(-1, 64), w)[0])
+    assert torch.equal(iga.rms_norm(x[0, 0, 0], w)[0], y[0, 0, 0])
+    for bad in (lambda: iga.rms_norm(x.transpose(0, 1), w), lambda: iga.rms_norm(x.transpose(2, 3), w),
+                lambda: iga.rms_norm(x, w.bfloat16()), lambda: iga.rms_norm(x, w[:32]),
+                lambda: iga.rms_norm(x, w, residual=x[0]), lambda: iga.rms_norm(x.double(), w),
+                lambda: iga.rms_norm_e4m3(x, w, group=100), lambda: iga.rms_norm(x, w.cpu()),
+                lambda: iga.rms_norm_grad(x, x, w, r[0])):
+        with pytest.raises((ValueError, TypeError, iga.ConvWgradError)):
+            bad()
+
+
+# --------------------------------------------------------------------------------------------------- convolution
+
+PACKED = [[0, 1, 1, 3, 40, 41], [0, 0, 16, 48, 113], [0, 0], [0, 200]]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("W,D,act,offsets,tail", [
+    (4, 64, True, None, 0), (2, 5, False, None, 0), (3, 130, True, None, 0), (4, 1, True, PACKED[0], 0),
+    (4, 600, True, PACKED[0], 7), (3, 67, False, PACKED[1], 33), (2, 256, True, PACKED[2], 20), (4, 12, True, PACKED[3], 0),
+    (4, 8, True, PACKED[2], 0)])
+@pytest.mark.parametrize("carried", [False, True])
+def test_conv_and_gradient(iga, W, D, act, offsets, tail, carried, dtype):
+    log("conv", W, D, act, offsets, tail, carried, dtype)
+    rand, dt = gen(W * 100 + D), DT[dtype]
+    shape = (3, 37) if offsets is None else (offsets[-1] + tail,)
+    S = 3 if offsets is None else len(offsets) - 1
+    x, dy = rand(*shape, D, dtype=dt), rand(*shape, D, dtype=dt)
+    w, b = rand(D, W, std=0.5), rand(D) if D != 5 else None
+    P = S + 2
+    slots = torch.randperm(P, generator=torch.Generator().manual_seed(D))[:S].int()
+    pool = rand(P, W - 1, D, dtype=dt)
+    state = pool[slots.long()] if carried else None
+    dlast = rand(S, W - 1, D, dtype=dt) if carried else None
+    off = torch.tensor(offsets, dtype=torch.int32).cuda() if offsets is not None else None
+    xd = strided(x, 3)
+    kw = dict(silu=act, offsets=off)
+    if carried:
+        kw.update(state=pool.cuda(), slots=slots.cuda())
+    out = torch.full((P, W - 1, D), 5.0, dtype=dt).cuda() if carried else None
+    wd, bd = w.cuda(), b.cuda() if b is not None else None
+    y, last = iga.causal_conv(xd, wd, bd, state_out=out, **kw)
+    xl, wl, bl, sl = leaf(x), leaf(w), leaf(b), leaf(state)
+    yr, lr = ref.conv(xl, wl, bl, act, offsets, sl)
+    c = 16
+    close(y, yr, dt, c, "y")
+    if carried:
+        want = torch.full((P, W - 1, D), 5.0, dtype=dt)
+        want[slots.long()] = lr.detach().to(dt)
+        assert torch.equal(last.cpu(), want)
+        inplace = pool.cuda()
+        y2, last2 = iga.causal_conv(xd, wd, bd, silu=act, offsets=off, state=inplace, slots=slots.cuda())
+        assert last2 is inplace and torch.equal(y2, y)
+        want = pool.clone()
+        want[slots.long()] = lr.detach().to(dt)
+        assert torch.equal(inplace.cpu(), want)
+    else:
+        assert torch.equal(last.cpu(), lr.detach().to(dt))
+    got = iga.causal_conv_grad(strided(dy, 1), xd, wd, bd, dstate_out=dlast.cuda() if carried else None, **kw)
+    inside = dy.double()
+    if tail:
+        inside[offsets[-1]:] = 0
+    exp = ref.grads((yr, lr), (inside, dlast.double() if carried else None), (xl, wl, bl, sl))
+    n = x.numel() // D
+    close(got[0], exp[0], dt, 64, "dx")
+    close(got[1], exp[1], torch.float32, 64 + n, "dw")
+    if b is not None:
+        close(got[2], exp[2], torch.float32, 64 + n, "db")
+    else:
+        assert got[2] is None
+    if carried:
+        close(got[3], exp[3], dt, 64, "dstate")
+    else:
+        assert got[3] is None
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_conv_long_has_many_pieces_a_workgroup(iga, dtype):
+    """More pieces than partial sums: each workgroup of the gradient walks along several."""
+    rand, dt = gen(3), DT[dtype]
+    x, dy, w, b = rand(2, 20000, 8, dtype=dt), rand(2, 20000, 8, dtype=dt), rand(8, 4, std=0.5), rand(8)
+    y, _ = iga.causal_conv(x.cuda(), w.cuda(), b.cuda(), silu=True)
+    dx, dw, db, _ = iga.causal_conv_grad(dy.cuda(), x.cuda(), w.cuda(), b.cuda(), silu=True)
+    xl, wl, bl = leaf(x), leaf(w), leaf(b)
+    yr, _ = ref.conv(xl, wl, bl, True, None, None)
+    exp = ref.grads((yr,), (dy.double(),), (xl, wl, bl))
+    close(y, yr, dt, 16, "y")
+    close(dx, exp[0], dt, 64, "dx")
+    close(dw, exp[1], torch.float32, 2000, "dw")
+    close(db, exp[2], torch.float32, 2000, "db")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("W,D,S", [(4, 300, 1), (4, 1030, 5), (2, 3, 4), (3, 64, 2)])
+def test_conv_step_matches_prompt(iga, W, D, S, dtype):
+    """Tokens one at a time give the prompt's outputs bit for bit (the same sums in the same order) and its window."""
+    rand, dt = gen(D), DT[dtype]
+    T = 6
+    x, w, b = strided(rand(S, T, D, dtype=dt), 2), rand(D, W, std=0.5).cuda(), rand(D).cuda()
+    pool = rand(S + 1, W - 1, D, dtype=dt).cuda()
+    slots = torch.arange(S, 0, -1, dtype=torch.int32).cuda()
+    whole = pool.clone()
+    y, _ = iga.causal_conv(x, w, b, silu=True, state=whole, slots=slots)
+    steps = [iga.causal_conv_step(x[:, t], pool, w, b, silu=True, slots=slots) for t in range(T)]
+    assert torch.equal(torch.stack(steps, 1), y) and torch.equal(pool, whole)
+
+
+def test_slots_outside_the_pool_have_no_state(iga):
+    rand = gen(9)
+    pool, w, x = rand(4, 3, 64).cuda(), rand(64, 4).cuda(), rand(3, 64).cuda()
+    slots = torch.tensor([-1, 2, 4], dtype=torch.int32).cuda()
+    before = pool.clone()
+    y = iga.causal_conv_step(x, pool, w, slots=slots)
+    assert torch.equal(pool[[0, 1, 3]], before[[0, 1, 3]])
+    assert torch.equal(pool[2], torch.cat([before[2, 1:], x[1:2]]))
+    zero = iga.causal_conv_step(x, torch.zeros(3, 3, 64).cuda(), w)
+    assert torch.equal(y[[0, 2]], zero[[0, 2]])
+    A, Bc = -torch.rand(64, 16).cuda() - 0.1, rand(3, 1, 16).cuda()
+    states = rand(4, 64, 16).cuda()
+    before = states.clone()
+    y = iga.selective_scan_step(x, x, A, Bc, Bc, states, softplus=True, slots=slots)
+    assert torch.equal(states[[0, 1, 3]], before[[0, 1, 3]]) and not torch.equal(states[2], before[2])
+    zero = iga.selective_scan_step(x, x, A, Bc, Bc, torch.zeros(3, 64, 16).cuda(), softplus=True)
+    assert torch.equal(y[[0, 2]], zero[[0, 2]])
+    y2, _, _ = iga.selective_scan(x, x, A, Bc, Bc, softplus=True, state=before.clone(), slots=slots,
+                                  offsets=torch.arange(4, dtype=torch.int32).cuda())
+    close(y2, y.double(), torch.float32, 64, "prompt of one token")
+
+
+# ---------------------------------------------------------------------------------------------------------- scan
+
+def scan_case(D, N, G, offsets, tail, dtype, opts, seed, L=37, S=2):
+    rand, dt = gen(seed), DT[dtype]
+    shape = (S, L) if offsets is None else (offsets[-1] + tail,)
+    S = S if offsets is None else len(offsets) - 1
+    case = dict(u=rand(*shape, D, dtype=dt), delta=rand(*shape, D, std=0.5, dtype=dt),
+                A=-(torch.arange(1, N + 1).float() * (0.8 + 0.4 * torch.rand(D, N, generator=torch.Generator().manual_seed(seed)))),
+                B=rand(*shape, G, N, dtype=dt), C=rand(*shape, G, N, dtype=dt),
+                skip=rand(D) if "skip" in opts else None, z=rand(*shape, D, dtype=dt) if "z" in opts else None,
+                bias=rand(D) - 2 if "bias" in opts else None, softplus="softplus" in opts,
+                state=rand(S, D, N) if "state" in opts else None, dy=rand(*shape, D, dtype=dt),
+                dlast=rand(S, D, N) if "last" in opts else None, offsets=offsets, S=S, dt=dt)
+    if not case["softplus"]:
+        case["delta"] = (case["delta"].float().abs() * 0.2 + 0.01).to(dt)
+        if case["bias"] is not None:
+            case["bias"] = case["bias"].abs() * 0.05
+    return case
+
+
+def run_scan(iga, c, max_len=None, grad=True, stream=None):
+    def dev(t):
+        return t.cuda() if t is not None else None
+
+    off = torch.tensor(c["offsets"], dtype=torch.int32).cuda() if c["offsets"] is not None else None
+    A = c["A"].cuda()
+    kw = dict(skip=dev(c["skip"]), z=strided(c["z"], 4) if c["z"] is not None else None, delta_bias=dev(c["bias"]),
+              softplus=c["softplus"], offsets=off, max_len=max_len, state=dev(c["state"]), stream=stream)
+    B, C = strided(c["B"], 5), strided(c["C"], 3)
+    u, delta = c["u"].cuda(), strided(c["delta"], 1)
+    y, last, saved = iga.selective_scan(u, delta, A, B, C, save=grad, **kw)
+    if not grad:
+        return y, last
+    return y, last, iga.selective_scan_grad(strided(c["dy"], 2), u, delta, A, B, C, saved, dstate_out=dev(c["dlast"]), **kw)
+
+
+ALL = ("skip", "z", "bias", "softplus", "state", "last")
+SCAN = [
+    # D, N, G, offsets, tail, options, L
+    (64, 16, 1, None, 0, ALL, 37), (1, 1, 1, None, 0, (), 1), (37, 11, 1, None, 0, ALL, 17), (130, 32, 1, None, 0, ALL, 16),
+    (66, 8, 2, None, 0, ("softplus", "state"), 65), (200, 24, 2, None, 0, ("z", "bias", "softplus", "last"), 33),
+    (70, 4, 1, None, 0, ("skip",), 15), (64, 16, 1, None, 0, ALL, 0), (96, 16, 1, None, 0, ALL, 150), (33, 20, 3, None, 0, ALL, 130),
+    (64, 16, 1, PACKED[0], 0, ALL, 0), (65, 9, 1, PACKED[1], 33, ALL, 0), (8, 16, 2, PACKED[2], 20, ALL, 0),
+    (48, 16, 1, PACKED[3], 0, ("softplus",), 0), (40, 8, 1, PACKED[1], 1, ("z", "state"), 0), (64, 16, 1, PACKED[2], 0, ALL, 0),
+    (24, 3, 1, None, 0, ("z", "softplus", "bias"), 64),
+]
+
+
+def check_scan(c, got, L):
+    y, last, g = got if len(got) == 3 else (*got, None)
+    names = ("u", "delta", "A", "B", "C", "skip", "z", "bias", "state")
+    leaves = [leaf(c[n]) for n in names]
+    yr, hr = ref.scan(*leaves[:5], leaves[5], leaves[6], leaves[7], c["softplus"], c["offsets"], leaves[8])
+    cc = 16 + 12 * L
+    dt = c["dt"]
+    close(y, yr, dt, cc, "y")
+    close(last, hr, torch.float32, cc, "state")
+    if g is None:
+        return
+    inside = c["dy"].double()
+    if c["offsets"] is not None:
+        inside[c["offsets"][-1]:] = 0
+    exp = ref.grads((yr, hr), (inside, c["dlast"].double() if c["dlast"] is not None else None), leaves)
+    rows = c["u"].numel() // c["u"].shape[-1]
+    for name, e, t, extra in zip(("du", "ddelta", "dA", "dB", "dC", "dskip", "dz", "ddelta_bias", "dstate"), exp,
+                                 (dt, dt, torch.float32, dt, dt, torch.float32, dt, torch.float32, torch.float32),
+                                 (0, 0, rows, 64, 64, rows, 0, rows, 0)):
+        if e is None:
+            assert getattr(g, name) is None, name
+        else:
+            close(getattr(g, name), e, t, 4 * cc + extra, name)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D,N,G,offsets,tail,opts,L", SCAN)
+def test_scan_and_gradient(iga, D, N, G, offsets, tail, opts, L, dtype):
+    log("scan", D, N, G, offsets, tail, opts, L, dtype)
+    c = scan_case(D, N, G, offsets, tail, dtype, opts, D + N + L, L=L)
+    longest = L if offsets is None else max(b - a for a, b in zip(offsets, offsets[1:]))
+    check_scan(c, run_scan(iga, c), longest)
+    if offsets is not None:
+        # told the longest length: the short ones go in one launch, with the same results to rounding
+        check_scan(c, run_scan(iga, c, max_len=max(longest, 1)), longest)
+        y, _ = run_scan(iga, c, max_len=1, grad=False)      # a hint that is wrong changes nothing either
+        check_scan(c, (y, run_scan(iga, c, grad=False)[1]), longest)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scan_of_many_short_sequences(iga, dtype):
+    rng = random.Random(3)
+    offsets = [0]
+    for _ in range(150):
+        offsets.append(offsets[-1] + rng.choice([0, 1, 1, 2, 3, 9]))
+    c = scan_case(24, 16, 1, offsets, 5, dtype, ALL, 77)
+    check_scan(c, run_scan(iga, c), 9)
+    check_scan(c, run_scan(iga, c, max_len=9), 9)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scan_with_more_pieces_than_workgroups(iga, dtype):
+    """A narrow layer over many sequences: the gradient's workgroups walk along several pieces each."""
+    c = scan_case(3, 2, 1, None, 0, dtype, ALL, 78, L=18, S=4500)
+    check_scan(c, run_scan(iga, c), 18)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D,N,G,S", [(64, 16, 1, 3), (37, 11, 1, 1), (66, 32, 2, 5), (300, 8, 3, 2), (5, 1, 1, 2)])
+def test_scan_step_matches_prompt(iga, D, N, G, S, dtype):
+    T = 5
+    c = scan_case(D, N, G, None, 0, dtype, ALL, D, L=T, S=S)
+    y, last, _ = run_scan(iga, c)
+    pool = torch.zeros(S + 2, D, N).cuda()
+    slots = torch.arange(S + 1, 1, -1, dtype=torch.int32).cuda()
+    pool[slots.long()] = c["state"].cuda()
+    u, delta, z, B, C = (strided(c[k], 4) for k in ("u", "delta", "z", "B", "C"))
+    args = dict(skip=c["skip"].cuda(), delta_bias=c["bias"].cuda(), softplus=True, slots=slots)
+    outs = [iga.selective_scan_step(u[:, t], delta[:, t], c["A"].cuda(), B[:, t], C[:, t], pool, z=z[:, t], **args)
+            for t in range(T)]
+    check_scan(c, (torch.stack(outs, 1), pool[slots.long()]), T)
+    assert bool((pool[:2] == 0).all())
+    other = torch.full_like(pool, 3.0)
+    iga.selective_scan_step(u[:, 0], delta[:, 0], c["A"].cuda(), B[:, 0], C[:, 0], pool, z=z[:, 0], state_out=other, **args)
+    assert bool((other[:2] == 3).all())
+
+
+@pytest.mark.parametrize("split", [False, True])
+def test_scan_in_place_and_in_two_halves(iga, split):
+    """A prompt in two calls, its state carried in place, gives the states of one call; sums are split elsewhere, so
+    equal to rounding."""
+    L = 160 if split else 40
+    c = scan_case(50, 16, 1, None, 0, "f32", ALL, 21, L=L)
+    y, last = run_scan(iga, c, grad=False)
+    state = c["state"].cuda()
+    k = L // 2 + 3
+    kw = dict(skip=c["skip"].cuda(), delta_bias=c["bias"].cuda(), softplus=True, state=state, state_out=state)
+    parts = []
+    for lo, hi in ((0, k), (k, L)):
+        u, d, z, B, C = (c[n].cuda()[:, lo:hi] for n in ("u", "delta", "z", "B", "C"))
+        parts.append(iga.selective_scan(u, d, c["A"].cuda(), B, C, z=z, **kw)[0])
+    close(torch.cat(parts, 1), y.double(), torch.float32, 16 + 12 * L, "y")
+    close(state, last.double(), torch.float32, 16 + 12 * L, "state")
+
+
+def test_scan_gradient_against_differences(iga):
+    """The directional derivative from the GPU's gradients against central differences of the 64-bit definition."""
+    c = scan_case(20, 16, 1, None, 0, "f32", ALL, 8, L=70)
+    _, _, g = run_scan(iga, c)
+    names = ("u", "delta", "A", "B", "C", "skip", "z", "bias", "state")
+    got = (g.du, g.ddelta, g.dA, g.dB, g.dC, g.dskip, g.dz, g.ddelta_bias, g.dstate)
+    ins = [c[n].double() for n in names]
+    direction = [torch.randn(t.shape, dtype=torch.float64, generator=torch.Generator().manual_seed(i)) for i, t in enumerate(ins)]
+
+    def loss(e):
+        v = [t + e * d for t, d in zip(ins, direction)]
+        y, h = ref.scan(*v[:5], v[5], v[6], v[7], True, None, v[8])
+        return (y * c["dy"].double()).sum() + (h * c["dlast"].double()).sum()
+
+    want = (loss(1e-5) - loss(-1e-5)) / 2e-5
+    terms = [(a.double().cpu() * d) for a, d in zip(got, direction)]
+    have, mass = sum(t.sum() for t in terms), sum(t.abs().sum() for t in terms)
+    assert abs(have - want) <= (4 * (16 + 12 * 70) * ref.EPS32) * mass + 1e-6 * abs(want)
+
+
+def test_results_do_not_change_from_run_to_run(iga):
+    c = scan_case(130, 16, 1, None, 0, "bf16", ALL, 4, L=300)
+    first, second = run_scan(iga, c), run_scan(iga, c)
+    assert torch.equal(first[0], second[0]) and torch.equal(first[1], second[1])
+    assert all(torch.equal(a, b) for a, b in zip(first[2], second[2]))
+
+
+def test_scan_refusals(iga):
+    rand = gen(2)
+    u, A, B = rand(2, 5, 8).cuda(), -torch.ones(8, 4).cuda(), rand(2, 5, 1, 4).cuda()
+    off = torch.tensor([0, 5], dtype=torch.int32).cuda()
+    y, last, saved = iga.selective_scan(u, u, A, B, B, save=True)
+    for bad in (lambda: iga.selective_scan(u, u[:1], A, B, B), lambda: iga.selective_scan(u, u, A.half(), B, B),
+                lambda: iga.selective_scan(u, u, A, B, B.half()), lambda: iga.selective_scan(u, u, A[:4], B, B),
+                lambda: iga.selective_scan(u, u, A, B[:, :, :, :3], B), lambda: iga.selective_scan(u, u, A, B, B, offsets=off),
+                lambda: iga.selective_scan(u[0], u[0], A, B[0], B[0], offsets=off.long()),
+                lambda: iga.selective_scan(u, u, A, B, B, state=last[:1]),
+                lambda: iga.selective_scan(u, u, A, B, B, state=last.half()),
+                lambda: iga.selective_scan(u, u, A, B, B, skip=torch.ones(7).cuda()),
+                lambda: iga.selective_scan(u.transpose(1, 2), u, A, B, B),
+                lambda: iga.selective_scan(u, u, -torch.ones(8, 40).cuda(), rand(2, 5, 1, 40).cuda(), rand(2, 5, 1, 40).cuda()),
+                lambda: iga.selective_scan_step(u, u, A, B, B, last),
+                lambda: iga.selective_scan_grad(u, u, u, A, B, B, saved[:-1]),
+                lambda: iga.causal_conv(u, rand(8, 5).cuda()), lambda: iga.causal_conv(u, rand(7, 4).cuda()),
+                lambda: iga.causal_conv(u, rand(8, 4).cuda(), state=u)):
+        with pytest.raises((ValueError, TypeError, iga.ConvWgradError)):
+            bad()
+
+
+# ------------------------------------------------------------------------------------------------ streams, graphs
+
+def test_on_another_stream(iga):
+    c = scan_case(64, 16, 1, None, 0, "bf16", ALL, 6, L=200)
+    want = run_scan(iga, c)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = run_scan(iga, c, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and all(torch.equal(a, b) for a, b in zip(got[2], want[2]))
+    x, w = torch.randn(4, 256).cuda(), torch.ones(256).cuda()
+    side.wait_stream(torch.cuda.current_stream())
+    y = iga.rms_norm(x, w, stream=side)[0]
+    side.synchronize()
+    assert torch.equal(y, iga.rms_norm(x, w)[0])
+
+
+def test_captured_into_a_graph(iga):
+    """Norm, convolution and scan with their gradients in one graph: every replay, on new inputs and with eager work
+    in between, gives the eager results."""
+    rand = gen(12)
+    S, L, D, N = 2, 130, 64, 16
+    x, dy = rand(S, L, D).cuda(), rand(S, L, D).cuda()
+    w, cw, cb = rand(D).cuda(), rand(D, 4).cuda(), rand(D).cuda()
+    A, bias = -torch.rand(D, N).cuda() - 0.2, rand(D).cuda()
+    B = rand(S, L, 1, N).cuda()
+    pool, states = rand(S, 3, D).cuda(), rand(S, D, N).cuda()
+
+    def work(pool, states):
+        y, h, r = iga.rms_norm(x, w)
+        v, _ = iga.causal_conv(y, cw, cb, silu=True)
+        o, last, saved = iga.selective_scan(v, y, A, B, B, z=x, delta_bias=bias, softplus=True, save=True)
+        g = iga.selective_scan_grad(dy, v, y, A, B, B, saved, z=x, delta_bias=bias, softplus=True)
+        dv = iga.causal_conv_grad(g.du, y, cw, cb, silu=True)
+        dx, dw = iga.rms_norm_grad(dv[0], h, w, r)
+        t = iga.causal_conv_step(x[:, 0], pool, cw, cb, silu=True)
+        t = iga.selective_scan_step(t, x[:, 1], A, B[:, 0], B[:, 1], states, delta_bias=bias, softplus=True)
+        return [o, last, dx, dw, dv[1], g.dA, g.dB, t]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        work(pool.clone(), states.clone())
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = work(pool, states)
+    for i in range(4):
+        x.copy_(torch.randn(S, L, D, generator=torch.Generator().manual_seed(i)))
+        p, s = pool.clone(), states.clone()
+        want = work(p, s)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+        assert torch.equal(pool, p) and torch.equal(states, s)
