@@ -125,7 +125,7 @@ Status check_scan_shape(const seq_scan_args_t& a, bool step) {
   const int64_t blocks = (int64_t)cw::scan_blocks(a);
   const int64_t pieces = seq_pieces(cw::seq_map(a.tokens, 6));
   const int64_t padded = a.states <= 8 ? 8 : a.states <= 16 ? 16 : 32;
-  if (!fits(pieces, 64 * blocks) || !fits(a.tokens.sequences, 64 * a.states * ((a.channels + 63) / 64)) ||
+  if (!fits(pieces, 64 * blocks) || !fits(a.tokens.sequences, 256 * a.states * ((a.channels + 63) / 64)) ||
       !fits(a.tokens.sequences, 256 * ((a.channels * padded / 4 + 255) / 256)))
     return CONV_WGRAD_ERR_UNSUPPORTED;
   return CONV_WGRAD_OK;
@@ -161,6 +161,9 @@ Status check_scan_grad(const seq_scan_grad_args_t* g) {
   const Status st = check_scan_shape(a, false);
   if (st != CONV_WGRAD_OK) return st;
   if (negative(g->dy)) return CONV_WGRAD_ERR_BAD_SHAPE;
+  // a lane's part of an address, up to 15 rows, is 32 bits
+  for (const seq_view_t* v : {&a.u, &a.delta, &a.z, &a.B, &a.C, &g->dy})
+    if (v->row >= (int64_t)1 << 26) return CONV_WGRAD_ERR_UNSUPPORTED;
   // the fold's lanes over dB: at most 32 an output
   if (!fits(seq_rows(a.tokens), 32 * a.groups * a.states)) return CONV_WGRAD_ERR_UNSUPPORTED;
   return CONV_WGRAD_OK;

@@ -26,8 +26,11 @@ struct ScanCut {
   int shift;
   bool split;
 };
-// Long sequences are split so that pieces x channel blocks come to about kScanWaves waves; a piece keeps 64 tokens.
-constexpr int64_t kScanWaves = 2048;
+// Long sequences are cut so that pieces x channel blocks come to about kScanWaves waves, four to a SIMD; a piece has at
+// least 16 tokens.  8192 tokens x 2048 channels: 2048 waves 181 us for the three launches, 4096 175, 8192 189 (a piece
+// of 32 tokens, whose carries are then as many bytes as the inputs); 1551 x 387 in fp32: pieces of 64 tokens 104 us, of
+// 16 tokens 26.  Up to kScanWhole tokens one launch is as quick as three.
+constexpr int64_t kScanWaves = 4096, kScanWhole = 64;
 ScanCut scan_cut(const seq_scan_args_t& a);
 inline int scan_dblocks(const seq_scan_args_t& a) { return (int)((a.channels / a.groups + 63) / 64); }
 inline int64_t scan_round(int64_t floats) { return (floats + 63) / 64 * 64; }
@@ -45,44 +48,74 @@ struct ChannelTile {
   __device__ __forceinline__ void load(const seq_view_t& view, const Piece& p, int t, int d) {
 #pragma unroll
     for (int i = 0; i < kScanTile; ++i)
-      v[i] = row_at<const T>(view, p, min(max(t + i, p.t0), p.end - 1))[d];
+      v[i] = at_lane(row_at<const T>(view, p, min(max(t + i, p.t0), p.end - 1)), d);
   }
 };
 
 // Rows [t, t + kScanTile) of B or C, widened, through registers into LDS ([token][NP]); zeros where there is none.
 template <typename T, int NP>
 struct StateTile {
-  static constexpr int kEach = kScanTile * NP / 64;
+  static constexpr int kAll = kScanTile * NP, kEach = (kAll + 63) / 64;
   float v[kEach];
   __device__ __forceinline__ void load(const seq_view_t& view, int64_t group_off, const Piece& p, int t, int N) {
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int e = i * 64 + ((int)threadIdx.x & 63), tok = t + e / NP, n = e % NP;
       v[i] = 0.f;
-      if (n < N && tok >= p.t0 && tok < p.end) v[i] = to_f32(row_at<const T>(view, p, tok)[group_off + n]);
+      if (e < kAll && n < N && tok >= p.t0 && tok < p.end)
+        v[i] = to_f32(row_at<const T>(view, p, tok)[group_off + n]);
     }
   }
   __device__ __forceinline__ void put(float* lds) const {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) lds[i * 64 + ((int)threadIdx.x & 63)] = v[i];
+    for (int i = 0; i < kEach; ++i) {
+      const int e = i * 64 + ((int)threadIdx.x & 63);
+      if (e < kAll) lds[e] = v[i];
+    }
   }
 };
+
+// D of a tile's tokens, zero past token n: such a token leaves the state as it is.
+template <typename T>
+__device__ __forceinline__ void step_sizes(float (&dt)[kScanTile], const ChannelTile<T>& delta, float bias,
+                                           int32_t with_softplus, int n) {
+#pragma unroll
+  for (int i = 0; i < kScanTile; ++i) dt[i] = to_f32(delta.v[i]) + bias;
+  if (with_softplus) {
+#pragma unroll
+    for (int i = 0; i < kScanTile; ++i) dt[i] = softplus(dt[i]);
+  }
+  if (n < kScanTile) {
+#pragma unroll
+    for (int i = 0; i < kScanTile; ++i) dt[i] = i < n ? dt[i] : 0.f;
+  }
+}
 
 __device__ __forceinline__ float step_size(float delta, float bias, int32_t with_softplus) {
   const float v = delta + bias;
   return with_softplus ? softplus(v) : v;
 }
 
-// The element type and padded state count of a call as template arguments; FULL: no padded states.
-#define SCAN_DISPATCH_N(call, T, n)                                                               \
-  ((n) <= 8 ? ((n) == 8 ? call(T, 8, true) : call(T, 8, false))                                   \
-            : (n) <= 16 ? ((n) == 16 ? call(T, 16, true) : call(T, 16, false))                    \
-                        : ((n) == 32 ? call(T, 32, true) : call(T, 32, false)))
-#define SCAN_DISPATCH(call, dtype, n)                                                             \
-  switch (dtype) {                                                                                \
-    case CONV_WGRAD_F32: return SCAN_DISPATCH_N(call, float, n);                                  \
-    case CONV_WGRAD_BF16: return SCAN_DISPATCH_N(call, Bf16, n);                                  \
-    default: return SCAN_DISPATCH_N(call, F16, n);                                                \
+// The element type and state count of a call as template arguments; the count is rounded up, and the states past the
+// call's own have A = B = C = 0.
+#define SCAN_DISPATCH_N(call, T, n) \
+  ((n) <= 8 ? call(T, 8) : (n) <= 12 ? call(T, 12) : (n) <= 16 ? call(T, 16) : (n) <= 24 ? call(T, 24) : call(T, 32))
+#define SCAN_DISPATCH(call, dtype, n)                            \
+  switch (dtype) {                                               \
+    case CONV_WGRAD_F32: return SCAN_DISPATCH_N(call, float, n); \
+    case CONV_WGRAD_BF16: return SCAN_DISPATCH_N(call, Bf16, n); \
+    default: return SCAN_DISPATCH_N(call, F16, n);               \
+  }
+// Kernels that share a channel's states out in fours, and know which states are their own (FULL: all).
+#define SCAN_DISPATCH4_N(call, T, n, full)                                                        \
+  ((n) <= 8 ? ((full) && (n) == 8 ? call(T, 8, true) : call(T, 8, false))                         \
+            : (n) <= 16 ? ((full) && (n) == 16 ? call(T, 16, true) : call(T, 16, false))          \
+                        : ((full) && (n) == 32 ? call(T, 32, true) : call(T, 32, false)))
+#define SCAN_DISPATCH4(call, dtype, n, full)                            \
+  switch (dtype) {                                                      \
+    case CONV_WGRAD_F32: return SCAN_DISPATCH4_N(call, float, n, full); \
+    case CONV_WGRAD_BF16: return SCAN_DISPATCH4_N(call, Bf16, n, full); \
+    default: return SCAN_DISPATCH4_N(call, F16, n, full);               \
   }
 
 }  // namespace cw

@@ -13,6 +13,10 @@ namespace cw {
 
 namespace {
 
+// Waves of a workgroup, each with a piece and channels of its own: workgroups of one wave are not spread evenly over
+// the four SIMDs of a CU.
+constexpr int kScanGroup = 4;
+
 // Channel of this lane within its group's blocks; lanes past the group's end repeat its last channel.
 struct Lane {
   int d;
@@ -32,15 +36,18 @@ __device__ __forceinline__ void load_decay(const seq_scan_args_t& a, int d, floa
   for (int n = 0; n < NP; ++n) A2[n] = n < a.states ? a.A[(int64_t)d * a.states + n] * kLog2e : 0.f;
 }
 
-template <typename T, int NP, bool FULL>
-__global__ __launch_bounds__(64) void scan_kernel(ScanArgs k) {
-  __shared__ __align__(16) float lb[2][kScanTile * NP], lc[2][kScanTile * NP];
+template <typename T, int NP>
+__global__ __launch_bounds__(64 * kScanGroup) void scan_kernel(ScanArgs k) {
+  typedef StateTile<T, NP> Tile;
+  __shared__ __align__(16) float l_B[kScanGroup][2][Tile::kAll], l_C[kScanGroup][2][Tile::kAll];
   const seq_scan_args_t& a = k.a;
-  const int blocks = k.dblocks * (int)a.groups;
-  const int piece = (int)blockIdx.x / blocks;
-  const Lane l = lane_channel(k, (int)blockIdx.x % blocks);
+  const int blocks = k.dblocks * (int)a.groups, wave = uniform((int)threadIdx.x >> 6);
+  const int job = (int)blockIdx.x * kScanGroup + wave, piece = job / blocks;
+  const Lane l = lane_channel(k, job % blocks);
   Piece p;
-  if (!find_piece(k.m, piece, p)) return;
+  if (piece >= k.pieces || !find_piece(k.m, piece, p)) return;
+  auto& lb = l_B[wave];
+  auto& lc = l_C[wave];
   if (p.seq >= k.m.S) {
     T zero;
     from_f32(0.f, zero);
@@ -57,7 +64,7 @@ __global__ __launch_bounds__(64) void scan_kernel(ScanArgs k) {
 #pragma unroll
   for (int n = 0; n < NP; ++n) {
     h[n] = 0.f;
-    if (FULL || n < N) {
+    if (n < N) {
       if (k.split) h[n] = k.carry[((int64_t)piece * N + n) * D + l.d];
       else if (a.state && slot >= 0) h[n] = a.state[slot * a.state_stride + (int64_t)l.d * N + n];
     }
@@ -67,8 +74,8 @@ __global__ __launch_bounds__(64) void scan_kernel(ScanArgs k) {
                                     : (int64_t)p.seq * (((k.m.rows - 1) >> kSaveShift) + 1);
   if (p.end > p.t0) {
     const int64_t gb = l.g * a.B_group, gc = l.g * a.C_group;
-    ChannelTile<T> u, dl, z, nu, ndl, nz;
-    StateTile<T, NP> sb, sc;
+    ChannelTile<T> u, z, nu, ndl, nz;
+    Tile sb, sc;
     nu.load(a.u, p, p.t0, l.d);
     ndl.load(a.delta, p, p.t0, l.d);
     if (a.z.ptr) nz.load(a.z, p, p.t0, l.d);
@@ -76,44 +83,49 @@ __global__ __launch_bounds__(64) void scan_kernel(ScanArgs k) {
     sc.load(a.C, gc, p, p.t0, N);
     int buf = 0;
     for (int t = p.t0; t < p.end; t += kScanTile, buf ^= 1) {
+      const int valid = p.end - t;
       sb.put(lb[buf]);
       sc.put(lc[buf]);
       u = nu;
-      dl = ndl;
       z = nz;
-      __syncthreads();
+      float dt[kScanTile], o[kScanTile];
+      step_sizes<T>(dt, ndl, bias, a.softplus, valid);
+      wave_sync();
       nu.load(a.u, p, t + kScanTile, l.d);
       ndl.load(a.delta, p, t + kScanTile, l.d);
       if (a.z.ptr) nz.load(a.z, p, t + kScanTile, l.d);
       sb.load(a.B, gb, p, t + kScanTile, N);
       sc.load(a.C, gc, p, t + kScanTile, N);
       if (a.save && (t & ((1 << kSaveShift) - 1)) == 0 && l.on) {
-        float* s = a.save + ((tile0 + (t >> kSaveShift)) * D + l.d) * N;
+        float* s = a.save + (tile0 + (t >> kSaveShift)) * D * N + l.d;   // [tile][state][channel]
 #pragma unroll
         for (int n = 0; n < NP; ++n)
-          if (FULL || n < N) s[n] = h[n];
+          if (n < N) s[(int64_t)n * D] = h[n];
       }
+      // No branch from here to the outputs: the tokens' loads from LDS, exponentials and sums overlap.
 #pragma unroll
       for (int i = 0; i < kScanTile; ++i) {
-        if (t + i < p.end) {
-          const float uv = to_f32(u.v[i]);
-          const float dt = step_size(to_f32(dl.v[i]), bias, a.softplus);
-          const float x = dt * uv;
-          float o[2] = {0.f, 0.f};
+        const float uv = to_f32(u.v[i]), x = dt[i] * uv;
+        float part[2] = {skip * uv, 0.f};
 #pragma unroll
-          for (int n = 0; n < NP; ++n)
-            if (FULL || n < N) {
-              const float e = __builtin_amdgcn_exp2f(dt * A2[n]);
-              h[n] = __builtin_fmaf(e, h[n], x * lb[buf][i * NP + n]);
-              o[n & 1] = __builtin_fmaf(h[n], lc[buf][i * NP + n], o[n & 1]);
-            }
-          float y = __builtin_fmaf(skip, uv, o[0] + o[1]);
-          if (a.z.ptr) {
-            const float zv = to_f32(z.v[i]);
-            y *= zv * sigmoid(zv);
-          }
-          if (l.on) from_f32(y, row_at<T>(a.y, p, t + i)[l.d]);
+        for (int n = 0; n < NP; ++n) {
+          const float e = __builtin_amdgcn_exp2f(dt[i] * A2[n]);
+          h[n] = __builtin_fmaf(e, h[n], x * lb[buf][i * NP + n]);
+          part[n & 1] = __builtin_fmaf(h[n], lc[buf][i * NP + n], part[n & 1]);
         }
+        o[i] = part[0] + part[1];
+      }
+      if (a.z.ptr) {
+#pragma unroll
+        for (int i = 0; i < kScanTile; ++i) {
+          const float zv = to_f32(z.v[i]);
+          o[i] *= zv * sigmoid(zv);
+        }
+      }
+      if (l.on) {
+#pragma unroll
+        for (int i = 0; i < kScanTile; ++i)
+          if (i < valid) from_f32(o[i], at_lane(row_at<T>(a.y, p, t + i), l.d));
       }
     }
   }
@@ -121,21 +133,23 @@ __global__ __launch_bounds__(64) void scan_kernel(ScanArgs k) {
     float* s = a.state_out + slot * a.state_out_stride + (int64_t)l.d * N;
 #pragma unroll
     for (int n = 0; n < NP; ++n)
-      if (FULL || n < N) s[n] = h[n];
+      if (n < N) s[n] = h[n];
   }
 }
 
 // A piece from a zero carry.  Forward: its end state.  Backward: what its first token passes to the token before,
 // from g[t] = dy z sigmoid(z) C[t] + c, c = e^(D A) g[t].  The last (first) piece of a sequence passes nothing on.
-template <typename T, int NP, bool FULL, bool BACK>
-__global__ __launch_bounds__(64) void scan_carry_kernel(ScanArgs k) {
-  __shared__ __align__(16) float lds[2][kScanTile * NP];
+template <typename T, int NP, bool BACK>
+__global__ __launch_bounds__(64 * kScanGroup) void scan_carry_kernel(ScanArgs k) {
+  typedef StateTile<T, NP> Tile;
+  __shared__ __align__(16) float l_side[kScanGroup][2][Tile::kAll];
   const seq_scan_args_t& a = k.a;
-  const int blocks = k.dblocks * (int)a.groups;
-  const int piece = (int)blockIdx.x / blocks;
-  const Lane l = lane_channel(k, (int)blockIdx.x % blocks);
+  const int blocks = k.dblocks * (int)a.groups, wave = uniform((int)threadIdx.x >> 6);
+  const int job = (int)blockIdx.x * kScanGroup + wave, piece = job / blocks;
+  const Lane l = lane_channel(k, job % blocks);
   Piece p;
-  if (!find_piece(k.m, piece, p) || p.seq >= k.m.S) return;
+  if (piece >= k.pieces || !find_piece(k.m, piece, p) || p.seq >= k.m.S) return;
+  auto& lds = l_side[wave];
   if (p.end == p.t0 || (BACK ? p.t0 == 0 : p.end == p.len)) return;
   const int N = a.states, D = (int)a.channels;
   float A2[NP], c[NP], sum = 0.f;
@@ -146,8 +160,8 @@ __global__ __launch_bounds__(64) void scan_carry_kernel(ScanArgs k) {
   const seq_view_t in = BACK ? k.dy : a.u, side = BACK ? a.C : a.B;
   const int64_t goff = l.g * (BACK ? a.C_group : a.B_group);
   const int tiles = (p.end - p.t0 + kScanTile - 1) / kScanTile;
-  ChannelTile<T> u, dl, z, nu, ndl, nz;
-  StateTile<T, NP> s;
+  ChannelTile<T> nu, ndl, nz;
+  Tile s;
   const int t1 = BACK ? p.t0 + (tiles - 1) * kScanTile : p.t0;
   nu.load(in, p, t1, l.d);
   ndl.load(a.delta, p, t1, l.d);
@@ -157,10 +171,23 @@ __global__ __launch_bounds__(64) void scan_carry_kernel(ScanArgs k) {
     const int t = BACK ? t1 - j * kScanTile : t1 + j * kScanTile;
     const int next = BACK ? t - kScanTile : t + kScanTile;
     s.put(lds[j & 1]);
-    u = nu;
-    dl = ndl;
-    z = nz;
-    __syncthreads();
+    float dt[kScanTile], x[kScanTile];
+    step_sizes<T>(dt, ndl, bias, a.softplus, p.end - t);
+#pragma unroll
+    for (int i = 0; i < kScanTile; ++i) x[i] = to_f32(nu.v[i]);
+    if constexpr (BACK) {
+      if (a.z.ptr) {
+#pragma unroll
+        for (int i = 0; i < kScanTile; ++i) {
+          const float zv = to_f32(nz.v[i]);
+          x[i] *= zv * sigmoid(zv);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kScanTile; ++i) x[i] *= dt[i];
+    }
+    wave_sync();
     nu.load(in, p, next, l.d);
     ndl.load(a.delta, p, next, l.d);
     if (BACK && a.z.ptr) nz.load(a.z, p, next, l.d);
@@ -168,46 +195,37 @@ __global__ __launch_bounds__(64) void scan_carry_kernel(ScanArgs k) {
 #pragma unroll
     for (int q = 0; q < kScanTile; ++q) {
       const int i = BACK ? kScanTile - 1 - q : q;
-      if (t + i < p.end) {
-        const float dt = step_size(to_f32(dl.v[i]), bias, a.softplus);
-        float x = to_f32(u.v[i]);
-        sum += dt;
-        if constexpr (BACK) {
-          if (a.z.ptr) {
-            const float zv = to_f32(z.v[i]);
-            x *= zv * sigmoid(zv);
-          }
-        } else {
-          x *= dt;
-        }
+      sum += dt[i];
 #pragma unroll
-        for (int n = 0; n < NP; ++n)
-          if (FULL || n < N) {
-            const float e = __builtin_amdgcn_exp2f(dt * A2[n]);
-            const float b = x * lds[j & 1][i * NP + n];
-            c[n] = BACK ? e * (c[n] + b) : __builtin_fmaf(e, c[n], b);
-          }
+      for (int n = 0; n < NP; ++n) {
+        const float e = __builtin_amdgcn_exp2f(dt[i] * A2[n]);
+        const float b = lds[j & 1][i * NP + n];   // zero for a token past the end
+        c[n] = BACK ? e * __builtin_fmaf(x[i], b, c[n]) : __builtin_fmaf(e, c[n], x[i] * b);
       }
     }
   }
   if (l.on) {
 #pragma unroll
     for (int n = 0; n < NP; ++n)
-      if (FULL || n < N) k.carry[((int64_t)piece * N + n) * D + l.d] = c[n];
+      if (n < N) k.carry[((int64_t)piece * N + n) * D + l.d] = c[n];
     k.sums[(int64_t)piece * D + l.d] = sum;
   }
 }
 
 // The carry into every piece of a sequence, in place of the pieces' aggregates; a lane owns one channel and state.
+// Four waves take 16 consecutive pieces each, all their aggregates in registers after one wait for memory; what the
+// waves before pass on comes through LDS.
+constexpr int kJoinWaves = 4, kJoinEach = 16;
 template <bool BACK>
-__global__ __launch_bounds__(64) void scan_join_kernel(ScanArgs k) {
-  constexpr int kAhead = 8;   // pieces whose aggregates are loaded together
+__global__ __launch_bounds__(64 * kJoinWaves) void scan_join_kernel(ScanArgs k) {
+  __shared__ float l_end[kJoinWaves][64], l_sum[kJoinWaves][64];
   const seq_scan_args_t& a = k.a;
   const int N = a.states, D = (int)a.channels;
   const int dblocks = (D + 63) / 64;
   const int db = (int)blockIdx.x % dblocks, n = (int)blockIdx.x / dblocks % N, s = (int)blockIdx.x / dblocks / N;
-  const int d = db * 64 + (int)threadIdx.x;
-  if (d >= D) return;
+  const int lane = (int)threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
+  const int d = min(db * 64 + lane, D - 1);
+  const bool on = db * 64 + lane < D;
   int first, len;
   if (k.m.offsets) {
     const int start = seq_start(k.m, s);
@@ -226,26 +244,42 @@ __global__ __launch_bounds__(64) void scan_join_kernel(ScanArgs k) {
     const int64_t slot = pool_slot(a.tokens.slots, a.tokens.pool, s);
     if (a.state && slot >= 0) h = a.state[slot * a.state_stride + (int64_t)d * N + n];
   }
-  for (int j0 = 0; j0 < count; j0 += kAhead) {
-    float e[kAhead], sum[kAhead];
+  for (int j0 = 0; j0 < count; j0 += kJoinWaves * kJoinEach) {
+    const int mine = j0 + wave * kJoinEach;
+    float e[kJoinEach], q[kJoinEach];   // end state, sum of D: zeros (which change nothing) where no piece follows
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i;
-      if (j < count - 1) {   // the last one's aggregate is not needed
-        const int64_t q = first + (BACK ? count - 1 - j : j);
-        e[i] = k.carry[(q * N + n) * D + d];
-        sum[i] = k.sums[q * D + d];
+    for (int i = 0; i < kJoinEach; ++i) {
+      const int j = mine + i;
+      e[i] = q[i] = 0.f;
+      if (j < count - 1) {
+        const int64_t at = first + (BACK ? count - 1 - j : j);
+        e[i] = k.carry[(at * N + n) * D + d];
+        q[i] = k.sums[at * D + d];
       }
     }
+    float end = 0.f, sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i;
-      if (j < count) {
-        const int64_t q = first + (BACK ? count - 1 - j : j);
-        k.carry[(q * N + n) * D + d] = h;
-        if (j < count - 1) h = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * sum[i]), h, e[i]);
-      }
+    for (int i = 0; i < kJoinEach; ++i) {
+      sum += q[i];
+      q[i] = __builtin_amdgcn_exp2f(A2 * q[i]);
+      end = __builtin_fmaf(q[i], end, e[i]);
     }
+    l_end[wave][lane] = end;
+    l_sum[wave][lane] = sum;
+    __syncthreads();
+    float c = h;
+#pragma unroll
+    for (int w = 0; w < kJoinWaves; ++w) {
+      if (w == wave) c = h;
+      h = __builtin_fmaf(__builtin_amdgcn_exp2f(A2 * l_sum[w][lane]), h, l_end[w][lane]);
+    }
+#pragma unroll
+    for (int i = 0; i < kJoinEach; ++i) {
+      const int j = mine + i;
+      if (j < count && on) k.carry[((int64_t)(first + (BACK ? count - 1 - j : j)) * N + n) * D + d] = c;
+      c = __builtin_fmaf(q[i], c, e[i]);
+    }
+    __syncthreads();
   }
 }
 
@@ -307,17 +341,20 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs k) {
   }
 }
 
-template <typename T, int NP, bool FULL>
-hipError_t scan_t(const ScanArgs& k, hipStream_t stream) {
-  const int64_t grid = (int64_t)k.pieces * k.dblocks * k.a.groups;
-  return launch_kernel(scan_kernel<T, NP, FULL>, dim3((unsigned)grid), dim3(64), k, stream);
+unsigned scan_grid(const ScanArgs& k) {
+  return (unsigned)(((int64_t)k.pieces * k.dblocks * k.a.groups + kScanGroup - 1) / kScanGroup);
 }
 
-template <typename T, int NP, bool FULL>
+template <typename T, int NP>
+hipError_t scan_t(const ScanArgs& k, hipStream_t stream) {
+  return launch_kernel(scan_kernel<T, NP>, dim3(scan_grid(k)), dim3(64 * kScanGroup), k, stream);
+}
+
+template <typename T, int NP>
 hipError_t carry_t(const ScanArgs& k, bool back, hipStream_t stream) {
-  const int64_t grid = (int64_t)k.pieces * k.dblocks * k.a.groups;
-  if (back) return launch_kernel(scan_carry_kernel<T, NP, FULL, true>, dim3((unsigned)grid), dim3(64), k, stream);
-  return launch_kernel(scan_carry_kernel<T, NP, FULL, false>, dim3((unsigned)grid), dim3(64), k, stream);
+  const dim3 grid(scan_grid(k)), block(64 * kScanGroup);
+  if (back) return launch_kernel(scan_carry_kernel<T, NP, true>, grid, block, k, stream);
+  return launch_kernel(scan_carry_kernel<T, NP, false>, grid, block, k, stream);
 }
 
 template <typename T, int NP, bool FULL>
@@ -328,13 +365,13 @@ hipError_t step_t(const ScanArgs& k, hipStream_t stream) {
 }
 
 hipError_t scan_any(const ScanArgs& k, hipStream_t stream) {
-#define CALL(T, NP, FULL) scan_t<T, NP, FULL>(k, stream)
+#define CALL(T, NP) scan_t<T, NP>(k, stream)
   SCAN_DISPATCH(CALL, k.a.dtype, k.a.states)
 #undef CALL
 }
 
 hipError_t carry_any(const ScanArgs& k, bool back, hipStream_t stream) {
-#define CALL(T, NP, FULL) carry_t<T, NP, FULL>(k, back, stream)
+#define CALL(T, NP) carry_t<T, NP>(k, back, stream)
   SCAN_DISPATCH(CALL, k.a.dtype, k.a.states)
 #undef CALL
 }
@@ -342,13 +379,13 @@ hipError_t carry_any(const ScanArgs& k, bool back, hipStream_t stream) {
 }  // namespace
 
 ScanCut scan_cut(const seq_scan_args_t& a) {
-  const int64_t waves = (int64_t)scan_dblocks(a) * a.groups;
-  const int64_t rows = seq_rows(a.tokens);
+  const int64_t waves = scan_blocks(a), rows = seq_rows(a.tokens);
   int64_t longest = a.tokens.rows;
   if (a.tokens.offsets && a.longest > 0 && a.longest < longest) longest = a.longest;
-  int shift = 6;
+  int shift = kSaveShift;
   while (shift < kWholeShift && (rows >> shift) * waves > kScanWaves) ++shift;
-  if (longest <= ((int64_t)1 << shift)) return ScanCut{kWholeShift, false};
+  const int64_t piece = (int64_t)1 << shift;
+  if (longest <= (piece > kScanWhole ? piece : kScanWhole)) return ScanCut{kWholeShift, false};
   return ScanCut{shift, true};
 }
 
@@ -366,9 +403,9 @@ int64_t scan_ws_floats(const seq_scan_args_t& a) {
 hipError_t launch_scan_carry(const ScanArgs& k, bool backward, hipStream_t stream) {
   const hipError_t err = carry_any(k, backward, stream);
   if (err != hipSuccess) return err;
-  const int64_t grid = (k.a.channels + 63) / 64 * k.a.states * k.a.tokens.sequences;
-  if (backward) return launch_kernel(scan_join_kernel<true>, dim3((unsigned)grid), dim3(64), k, stream);
-  return launch_kernel(scan_join_kernel<false>, dim3((unsigned)grid), dim3(64), k, stream);
+  const dim3 grid((unsigned)((k.a.channels + 63) / 64 * k.a.states * k.a.tokens.sequences)), block(64 * kJoinWaves);
+  if (backward) return launch_kernel(scan_join_kernel<true>, grid, block, k, stream);
+  return launch_kernel(scan_join_kernel<false>, grid, block, k, stream);
 }
 
 hipError_t launch_scan(const seq_scan_args_t& a, float* ws, hipStream_t stream) {
@@ -392,7 +429,7 @@ hipError_t launch_scan_step(const seq_scan_args_t& a, hipStream_t stream) {
   ScanArgs k{};
   k.a = a;
 #define CALL(T, NP, FULL) step_t<T, NP, FULL>(k, stream)
-  SCAN_DISPATCH(CALL, a.dtype, a.states)
+  SCAN_DISPATCH4(CALL, a.dtype, a.states, true)
 #undef CALL
 }
 

@@ -5,14 +5,16 @@
 //   dD = sum_n A c[t - 1] h[t - 1] + u sum_n g B,  ddelta = dD sigmoid(delta + bias),  dA = sum_t D c[t - 1] h[t - 1]
 // and dz from o = sum_n h C + skip u.  All of it needs the states again: the forward saved one state of every 16 tokens
 // (4 bytes a token and channel for 16 states; scanning forward once more to find them would cost as much as the first
-// of the three forward launches, about twice what writing and reading them does).
+// of the three forward launches, 67 us where writing and reading them costs 13 and 14).
 //
 // Bound by the vector ALU.  A workgroup takes a piece of a sequence and 64 channels, 16 tokens at a time from the last:
 // what a token and channel need (D, D u, do) is computed once by the lane that loads it and passed through LDS; then
-// NG lanes share a channel, four states each, and keep e^(D A) and h of the 16 tokens in registers (128 of them), so
-// the reversed sweep recomputes nothing.  Sums over states are taken inside a group of NG lanes, sums over channels by
-// exchanging halves of the wave (each step halves the values a lane holds), then over the waves through LDS and over
-// the channel blocks by a fold, in a fixed order.
+// NG lanes share a channel, four states each, and keep h of the 16 tokens in 64 registers for the reversed sweep.
+// Keeping e^(D A) too would save the second exponential (3 of about 28 instructions a state) but 64 registers more leave
+// one wave a SIMD: 519 us against 341 on 8192 tokens x 2048 channels x 16 states in bf16.  Sums over states are taken
+// inside a group of NG lanes, each of which keeps one of NG tokens' results; sums over channels by exchanging halves of
+// the wave (each step halves the values a lane holds), then over the waves through LDS and over the channel blocks by a
+// fold, all in a fixed order.  Those 8192 tokens take 286 us; the vector ALU is busy 73 % of them.
 #include "seq_scan.h"
 
 namespace cw {
@@ -39,9 +41,14 @@ __device__ __forceinline__ float xor4(float v) {
 }
 constexpr int kXor8 = 0x128;   // row_ror:8
 
-// Sums v[0 .. 7] over the lanes that differ in bits 3 .. 5 and, for NG < 8, 2 (and 1); lane l gets value
-// 4 b5 + 2 b4 + b3 of its bits.
-template <int NG>
+// One step of a sum over lanes that shares its results out: of values a and b, lanes whose bit is clear get the sum of
+// a over themselves and their partner, the others that of b; `from` brings the partner's value.
+template <class From>
+__device__ __forceinline__ float halve(bool bit, float a, float b, From from) {
+  return (bit ? b : a) + from(bit ? a : b);
+}
+
+// Sums v[0 .. 7] over the lanes that differ in bits 3 .. 5; lane l gets value 4 b5 + 2 b4 + b3 of its bits.
 __device__ __forceinline__ float channels_reduce(const float (&v)[8]) {
   float r4[4], r2[2];
 #pragma unroll
@@ -54,47 +61,89 @@ __device__ __forceinline__ float channels_reduce(const float (&v)[8]) {
     const u32x2 p = __builtin_amdgcn_permlane16_swap(__float_as_uint(r4[i]), __float_as_uint(r4[i + 2]), false, false);
     r2[i] = __uint_as_float(p[0]) + __uint_as_float(p[1]);
   }
-  const bool b3 = threadIdx.x & 8;
-  float r = (b3 ? r2[1] : r2[0]) + dpp<kXor8>(b3 ? r2[0] : r2[1]);
-  if constexpr (NG < 8) r += xor4(r);
-  if constexpr (NG < 4) r += dpp<kXor2>(r);
-  return r;
+  return halve(threadIdx.x & 8, r2[0], r2[1], [](float f) { return dpp<kXor8>(f); });
+}
+
+// The rest of that sum, over bits 2 (NG = 4) or 2 and 1 (NG = 2) that name channels too, shared out over 8 / NG tokens:
+// lane l gets token bit 2 (+ 2 bit 1).
+template <int NG>
+__device__ __forceinline__ float tokens_reduce(const float (&r)[8 / NG]) {
+  const bool b2 = threadIdx.x & 4;
+  auto four = [](float f) { return xor4(f); };
+  if constexpr (NG == 8) {
+    return r[0];
+  } else if constexpr (NG == 4) {
+    return halve(b2, r[0], r[1], four);
+  } else {
+    const float lo = halve(b2, r[0], r[1], four), hi = halve(b2, r[2], r[3], four);
+    return halve(threadIdx.x & 2, lo, hi, [](float f) { return dpp<kXor2>(f); });
+  }
 }
 
 // What the lanes of a workgroup pass each other of one tile.
 template <int NG>
 struct GradTile {
   alignas(16) float dt[kTile][64], x[kTile][64], dov[kTile][64];   // D, D u, do
-  float o[kTile][64], gb[kTile][64], da[kTile][64];                // sums over states: h C, g B, A c[t - 1] h[t - 1]
+  // Sums over states: h C, g B, A c[t - 1] h[t - 1].  NG lanes write NG rows of 64 / NG channels: no two in one bank.
+  alignas(16) float o[kTile][64 + 64 / NG], gb[kTile][64 + 64 / NG], da[kTile][64 + 64 / NG];
   alignas(16) float B[kTile][4 * NG], C[kTile][4 * NG];
   float bias[64], skip[64];
   float bc[NG][kTile][8 * NG];                                     // each wave's sums over its channels: dB, dC
 };
 
+// Rows of a tensor from the first token of a piece on: an address that is the same in the whole wave and the distance of
+// two rows, both in bytes.  A lane's own part of an address is a 32-bit offset.
+struct Rows {
+  const char* at;
+  uint32_t row;
+};
+template <typename T>
+__device__ __forceinline__ Rows rows_from(const seq_view_t& v, const Piece& p, int64_t offset) {
+  return Rows{reinterpret_cast<const char*>(row_at<const T>(v, p, p.t0) + offset), (uint32_t)v.row * (uint32_t)sizeof(T)};
+}
+template <typename T>
+__device__ __forceinline__ const T* lane_of(const Rows& r, int tile, uint32_t offset) {
+  return reinterpret_cast<const T*>(r.at + (int64_t)tile * kTile * r.row + offset);
+}
+
+// The kernel's arguments, to be loaded where they are used: held through the sweeps they need more scalar registers than
+// there are, and the compiler would keep them in vector lanes, an instruction for each use.
+typedef const __attribute__((address_space(4))) GradArgs* ArgsPtr;
+__device__ __forceinline__ ArgsPtr args_again() {
+  ArgsPtr p = (ArgsPtr)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return p;
+}
+__device__ __forceinline__ seq_view_t view_of(const __attribute__((address_space(4))) seq_view_t& v) {
+  return seq_view_t{v.ptr, v.batch, v.row};
+}
+
+// FULL: every lane has a channel and four states (channels of a group a multiple of 64, states of 4 NG).
 template <typename T, int NG, bool FULL>
-__global__ __launch_bounds__(64 * NG) void scan_grad_kernel(GradArgs k) {
-  constexpr int NP = 4 * NG, kWaveCh = 64 / NG, V = 16 / NG;
+__global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
+  constexpr int NP = 4 * NG, kWaveCh = 64 / NG, V = 16 / NG, kShare = 8 / NG;
+  constexpr bool kEarly = V * sizeof(T) < 32;   // the next tile's inputs fit the registers
   __shared__ GradTile<NG> m;
   const seq_scan_args_t& a = k.s.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int N = a.states, D = (int)a.channels, Dg = D / (int)a.groups;
+  const int N = FULL ? NP : a.states, D = (int)a.channels, Dg = D / (int)a.groups;
   const int blocks = k.s.dblocks * (int)a.groups;
   const int part = (int)blockIdx.x / blocks, block = (int)blockIdx.x % blocks;
   const int g = block / k.s.dblocks, cblock = block % k.s.dblocks;
-  const int c0 = cblock * 64;               // first channel of the block in its group
-  const int nch = min(64, Dg - c0);         // channels of the block
-  const int d0 = g * Dg + c0;
+  const int nch = FULL ? 64 : min(64, Dg - cblock * 64);   // channels of the block
+  const int d0 = g * Dg + cblock * 64;                     // the first
   // As a lane of the sweeps: one channel, four states.
-  const int ch = wave * kWaveCh + lane / NG, n0 = (lane % NG) * 4, nv = N - n0;
-  const bool on = ch < nch;
-  const int d = d0 + min(ch, nch - 1);
-  // As a lane of the loads and outputs: one token, V channels.
+  const int ch = wave * kWaveCh + lane / NG, ng = lane % NG, n0 = ng * 4, nv = N - n0;
+  const bool on = FULL || ch < nch;
+  const int chc = FULL ? ch : min(ch, nch - 1);
+  // As a lane of the loads and outputs: one token, V channels; and one element of B and C.
   const int it = tid / (64 / V), ic = tid % (64 / V) * V, iv = nch - ic;   // iv <= 0: none
-  const bool gated = a.z.ptr != nullptr;
+  const int eT = tid / NP, eN = tid % NP;
+  const bool gated = a.z.ptr != nullptr, with_softplus = a.softplus != 0;
 
   float A2[4], dA[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] = FULL || i < nv ? a.A[(int64_t)d * N + n0 + i] * kLog2e : 0.f;
+  for (int i = 0; i < 4; ++i) A2[i] = FULL || i < nv ? a.A[(int64_t)(d0 + chc) * N + n0 + i] * kLog2e : 0.f;
   float dskip[V], dbias[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) dskip[j] = dbias[j] = 0.f;
@@ -105,177 +154,244 @@ __global__ __launch_bounds__(64 * NG) void scan_grad_kernel(GradArgs k) {
   __syncthreads();
   const int64_t all_rows = k.s.m.offsets ? k.s.m.rows : (int64_t)k.s.m.S * k.s.m.rows;
   const int64_t bc = all_rows * a.groups * N;   // floats of dB
+  const uint32_t bc_row = (uint32_t)a.groups * (uint32_t)N;
 
   for (int piece = part; piece < k.s.pieces; piece += k.parts) {
     Piece p;
     if (!find_piece(k.s.m, piece, p)) continue;
-    const int64_t row0 = k.s.m.offsets ? p.first : (int64_t)p.seq * k.s.m.rows;   // dense row of the first token
-    const bool real = p.seq < k.s.m.S;
     const int tiles = (p.end - p.t0 + kTile - 1) / kTile;
-    const int64_t tile0 = k.s.m.offsets ? (p.first >> kSaveShift) + p.seq
-                                        : (int64_t)p.seq * (((k.s.m.rows - 1) >> kSaveShift) + 1);
+    // Dense row of the piece's first token, and where this lane writes in it.
+    const int64_t row0 = (k.s.m.offsets ? p.first : (int64_t)p.seq * k.s.m.rows) + p.t0;
+    float* const bc0 = k.part_bc + (int64_t)cblock * 2 * bc + (row0 * a.groups + g) * N;
+    if (p.seq >= k.s.m.S) {   // padding behind the last sequence
+      for (int j = 0; j < tiles; ++j) {
+        const int nt = min(kTile, p.end - p.t0 - j * kTile);
+        if (it < nt && iv > 0) {
+          Raw<T, V> zero;
+          zero.clear();
+          const int64_t at = (row0 + j * kTile + it) * D + d0 + ic;
+          zero.store_n(static_cast<T*>(k.g.du) + at, iv);
+          zero.store_n(static_cast<T*>(k.g.ddelta) + at, iv);
+          if (gated) zero.store_n(static_cast<T*>(k.g.dz) + at, iv);
+        }
+        if (eT < nt && eN < N) {
+          float* const to = bc0 + (int64_t)(j * kTile + eT) * bc_row + eN;
+          to[0] = to[bc] = 0.f;
+        }
+      }
+      continue;
+    }
+    const int64_t tile0 = (k.s.m.offsets ? (p.first >> kSaveShift) + p.seq
+                                         : (int64_t)p.seq * (((k.s.m.rows - 1) >> kSaveShift) + 1)) +
+                          (p.t0 >> kSaveShift);
+    const uint32_t state_off = (uint32_t)(n0 * D + chc);   // of this lane's first state in [states][channels]
     float c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       c[i] = 0.f;
-      if (real && (FULL || i < nv)) {
-        if (k.s.split) c[i] = k.s.carry[((int64_t)piece * N + n0 + i) * D + d];
-        else if (k.s.last) c[i] = k.s.last[((int64_t)p.seq * D + d) * N + n0 + i];
+      if (FULL || i < nv) {
+        if (k.s.split) c[i] = (k.s.carry + (int64_t)piece * N * D + d0)[state_off + i * D];
+        else if (k.s.last) c[i] = k.s.last[((int64_t)p.seq * D + d0 + chc) * N + n0 + i];
       }
     }
     Raw<T, V> u, dl, z, dy;
-    float h0[4], eB, eC;
-    const int eT = tid / NP, eN = tid % NP;   // the element of B and C that this lane stages
-    auto fetch = [&](int j) {                 // the inputs of tile j
-      const int t = p.t0 + j * kTile;
-      u.clear();
-      dl.clear();
-      z.clear();
-      dy.clear();
-      eB = eC = 0.f;
-      if (j < 0 || !real) return;
-      if (t + it < p.end && iv > 0) {
-        u.load_n(row_at<const T>(a.u, p, t + it) + d0 + ic, iv);
-        dl.load_n(row_at<const T>(a.delta, p, t + it) + d0 + ic, iv);
-        dy.load_n(row_at<const T>(k.s.dy, p, t + it) + d0 + ic, iv);
-        if (gated) z.load_n(row_at<const T>(a.z, p, t + it) + d0 + ic, iv);
+    float h0[4];
+    T eB, eC;
+    from_f32(0.f, eB);
+    from_f32(0.f, eC);
+    u.clear();
+    dl.clear();
+    z.clear();
+    dy.clear();
+    // This lane's token and channels of tile j; rows past the end repeat the last one.
+    auto fetch_items = [&](int j, Raw<T, V>& u, Raw<T, V>& dl, Raw<T, V>& z, Raw<T, V>& dy) {
+      const uint32_t r = (uint32_t)min(it, min(kTile, p.end - p.t0 - j * kTile) - 1), off = (uint32_t)ic * sizeof(T);
+      const ArgsPtr q = args_again();
+      if (FULL || iv > 0) {
+        const int nvec = FULL ? V : iv;
+        const Rows ru = rows_from<T>(view_of(q->s.a.u), p, d0), rdl = rows_from<T>(view_of(q->s.a.delta), p, d0);
+        u.load_n(lane_of<T>(ru, j, r * ru.row + off), nvec);
+        dl.load_n(lane_of<T>(rdl, j, r * rdl.row + off), nvec);
+        const Rows rdy = rows_from<T>(view_of(q->s.dy), p, d0);
+        dy.load_n(lane_of<T>(rdy, j, r * rdy.row + off), nvec);
+        if (gated) {
+          const Rows rz = rows_from<T>(view_of(q->s.a.z), p, d0);
+          z.load_n(lane_of<T>(rz, j, r * rz.row + off), nvec);
+        }
       }
-      if (t + eT < p.end && eN < N) {
-        eB = to_f32(row_at<const T>(a.B, p, t + eT)[g * a.B_group + eN]);
-        eC = to_f32(row_at<const T>(a.C, p, t + eT)[g * a.C_group + eN]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        h0[i] = FULL || i < nv ? a.save[((tile0 + (t >> kSaveShift)) * D + d) * N + n0 + i] : 0.f;
     };
+    // The inputs of tile j.
+    auto fetch = [&](int j) {
+      fetch_items(j, u, dl, z, dy);
+      const uint32_t e = (uint32_t)min(eT, min(kTile, p.end - p.t0 - j * kTile) - 1);
+      const ArgsPtr q = args_again();
+      if (FULL || eN < N) {
+        const Rows rB = rows_from<T>(view_of(q->s.a.B), p, g * q->s.a.B_group);
+        const Rows rC = rows_from<T>(view_of(q->s.a.C), p, g * q->s.a.C_group);
+        eB = *lane_of<T>(rB, j, e * rB.row + (uint32_t)eN * (uint32_t)sizeof(T));
+        eC = *lane_of<T>(rC, j, e * rC.row + (uint32_t)eN * (uint32_t)sizeof(T));
+      }
+      const float* const from = q->s.a.save + (tile0 + j) * D * N + d0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) h0[i] = 0.f;
-    fetch(tiles - 1);
+      for (int i = 0; i < 4; ++i) h0[i] = FULL || i < nv ? from[state_off + i * D] : 0.f;
+    };
+    if (kEarly && tiles) fetch(tiles - 1);
     for (int j = tiles - 1; j >= 0; --j) {
-      const int t = p.t0 + j * kTile;
-      const int nt = min(kTile, p.end - t);
-      // What the sweeps need of this lane's own token and channels; its raw inputs are kept for its outputs.
-      const Raw<T, V> cu = u, cdl = dl, cz = z, cdy = dy;
+      if constexpr (!kEarly) fetch(j);
+      const int nt = min(kTile, p.end - p.t0 - j * kTile);
+      // What the sweeps need of this lane's own token and channels; its raw inputs are kept for its outputs (eight
+      // channels a lane do not fit the registers: read again).  Tokens past the piece's end pass state and gradient on
+      // unchanged.
+      Raw<T, V> cu = u, cdl = dl, cz = z, cdy = dy;
+      const bool valid = it < nt;
+      float pdt[V], pdo[V];
 #pragma unroll
       for (int q = 0; q < V; ++q) {
-        const float raw = cdl.get(q) + m.bias[ic + q];
-        // Tokens past the piece's end pass state and gradient on unchanged.
-        const float dt = it >= nt ? 0.f : a.softplus ? softplus(raw) : raw;
-        float dov = cdy.get(q);
-        if (gated) dov *= cz.get(q) * sigmoid(cz.get(q));
-        m.dt[it][ic + q] = dt;
-        m.x[it][ic + q] = dt * cu.get(q);
-        m.dov[it][ic + q] = dov;
+        pdt[q] = cdl.get(q) + m.bias[ic + q];
+        pdo[q] = cdy.get(q);
       }
-      m.B[eT][eN] = eB;
-      m.C[eT][eN] = eC;
+      if (with_softplus) {
+#pragma unroll
+        for (int q = 0; q < V; ++q) pdt[q] = softplus(pdt[q]);
+      }
+      if (gated) {
+#pragma unroll
+        for (int q = 0; q < V; ++q) pdo[q] *= cz.get(q) * sigmoid(cz.get(q));
+      }
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        m.dt[it][ic + q] = valid ? pdt[q] : 0.f;
+        m.x[it][ic + q] = valid ? pdt[q] * cu.get(q) : 0.f;
+        m.dov[it][ic + q] = valid ? pdo[q] : 0.f;
+      }
+      m.B[eT][eN] = to_f32(eB);
+      m.C[eT][eN] = to_f32(eC);
       float hs[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) hs[i] = h0[i];
       __syncthreads();
-      fetch(j - 1);
+      if (kEarly && j > 0) fetch(j - 1);
 
-      float e[kTile][4], h[kTile][4];
+      float h[kTile][4];
+      float keep = 0.f;
 #pragma unroll
       for (int q = 0; q < kTile; ++q) {
-          const float dt = m.dt[q][ch], x = m.x[q][ch];
-          float o = 0.f;
+        const float dt = m.dt[q][ch], x = m.x[q][ch];
+        const float4 Bv = *reinterpret_cast<const float4*>(&m.B[q][n0]);
+        const float4 Cv = *reinterpret_cast<const float4*>(&m.C[q][n0]);
+        const float B4[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, C4[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
+        float o = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e[q][i] = __builtin_amdgcn_exp2f(dt * A2[i]);
-            const float b = FULL || i < nv ? x * m.B[q][n0 + i] : 0.f;
-            h[q][i] = __builtin_fmaf(e[q][i], q ? h[q ? q - 1 : 0][i] : hs[i], b);
-            o = __builtin_fmaf(h[q][i], FULL || i < nv ? m.C[q][n0 + i] : 0.f, o);
-          }
-          o = lanes_reduce<AddOp>(o, NG);
-          if (n0 == 0) m.o[q][ch] = o;
-        __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < 4; ++i) {
+          const float e = __builtin_amdgcn_exp2f(dt * A2[i]);
+          h[q][i] = __builtin_fmaf(e, q ? h[q ? q - 1 : 0][i] : hs[i], x * B4[i]);
+          o = __builtin_fmaf(h[q][i], C4[i], o);
+        }
+        o = lanes_reduce<AddOp>(o, NG);
+        keep = ng == q % NG ? o : keep;
+        if (q % NG == NG - 1) {
+          m.o[q - (NG - 1) + ng][ch] = keep;
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
       // Read B, C, D and D u again: kept from the sweep above they would take 160 registers more.  The compiler is
       // not to know that these are the same indices.
-      int ch2 = ch, n2 = n0;
-      asm volatile("" : "+v"(ch2), "+v"(n2));
+      int ch2 = ch, ng2 = ng;
+      asm volatile("" : "+v"(ch2), "+v"(ng2));
+      float keep_gb = 0.f, keep_da = 0.f, sums[kShare];
 #pragma unroll
       for (int q = kTile - 1; q >= 0; --q) {
-          const float dt = m.dt[q][ch2], x = m.x[q][ch2], dov = m.dov[q][ch2];
-          const float4 Bv = *reinterpret_cast<const float4*>(&m.B[q][n2]);
-          const float4 Cv = *reinterpret_cast<const float4*>(&m.C[q][n2]);
-          const float B4[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, C4[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
-          float gb = 0.f, da = 0.f, v[8];
+        const float dt = m.dt[q][ch2], x = m.x[q][ch2], dov = m.dov[q][ch2];
+        const float4 Bv = reinterpret_cast<const float4*>(&m.B[q][0])[ng2];
+        const float4 Cv = reinterpret_cast<const float4*>(&m.C[q][0])[ng2];
+        const float B4[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, C4[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
+        float gb = 0.f, da = 0.f, v[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float gi = FULL || i < nv ? __builtin_fmaf(dov, C4[i], c[i]) : 0.f;
-            v[i] = gi * x;                // lanes without a channel: x and do are zero
-            v[4 + i] = dov * h[q][i];
-            gb = __builtin_fmaf(gi, B4[i], gb);
-            c[i] = e[q][i] * gi;
-            const float r = c[i] * (q ? h[q ? q - 1 : 0][i] : hs[i]);
-            da = __builtin_fmaf(r, A2[i], da);
-            dA[i] = __builtin_fmaf(r, dt, dA[i]);
-          }
-          gb = lanes_reduce<AddOp>(gb, NG);
-          da = lanes_reduce<AddOp>(da, NG);
-          if (n0 == 0) {
-            m.gb[q][ch2] = gb;
-            m.da[q][ch2] = da * kLn2;   // A2 = A log2 e
-          }
-          const float r = channels_reduce<NG>(v);
-          // bits 3 .. 5 name the value; the bits below that are not the state's have the same sum
-          if ((lane & 7) < NG) m.bc[wave][q][(lane >> 5) * NP + n0 + ((lane >> 3) & 3)] = r;
-        __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < 4; ++i) {
+          const float gi = __builtin_fmaf(dov, C4[i], c[i]);
+          v[i] = gi * x;                // lanes without a channel: x and do are zero
+          v[4 + i] = dov * h[q][i];
+          gb = __builtin_fmaf(gi, B4[i], gb);
+          c[i] = __builtin_amdgcn_exp2f(dt * A2[i]) * gi;
+          const float r = c[i] * (q ? h[q ? q - 1 : 0][i] : hs[i]);
+          da = __builtin_fmaf(r, A2[i], da);
+          dA[i] = __builtin_fmaf(r, dt, dA[i]);
+        }
+        gb = lanes_reduce<AddOp>(gb, NG);
+        da = lanes_reduce<AddOp>(da, NG);
+        keep_gb = ng == q % NG ? gb : keep_gb;
+        keep_da = ng == q % NG ? da : keep_da;
+        if (q % NG == 0) {
+          m.gb[q + ng][ch2] = keep_gb;
+          m.da[q + ng][ch2] = keep_da * kLn2;   // A2 = A log2 e
+        }
+        sums[q % kShare] = channels_reduce(v);
+        if (q % kShare == 0) {
+          const int to = NG == 8 ? 0 : NG == 4 ? (lane >> 2) & 1 : ((lane >> 2) & 1) + (lane & 2);
+          m.bc[wave][q + to][(lane >> 5) * NP + n0 + ((lane >> 3) & 3)] = tokens_reduce<NG>(sums);
+        }
+        if (q % 2 == 0) __builtin_amdgcn_sched_barrier(0);
       }
       __syncthreads();
-      if (it < nt && iv > 0) {
-        float du[V], dd[V], dz[V];
+      if constexpr (NG == 2) fetch_items(j, cu, cdl, cz, cdy);
+      if (valid && (FULL || iv > 0)) {
+        const ArgsPtr w = args_again();
+        float du[V], dd[V];
 #pragma unroll
         for (int q = 0; q < V; ++q) {
           const float dov = m.dov[it][ic + q], dt = m.dt[it][ic + q], gb = m.gb[it][ic + q], uv = cu.get(q);
           du[q] = __builtin_fmaf(dt, gb, m.skip[ic + q] * dov);
           dd[q] = __builtin_fmaf(uv, gb, m.da[it][ic + q]);
-          if (a.softplus) dd[q] *= sigmoid(cdl.get(q) + m.bias[ic + q]);
           dskip[q] = __builtin_fmaf(dov, uv, dskip[q]);
-          dbias[q] += dd[q];
-          if (gated) {
-            const float zv = cz.get(q), sg = sigmoid(zv);
-            dz[q] = cdy.get(q) * __builtin_fmaf(m.skip[ic + q], uv, m.o[it][ic + q]) * (sg * __builtin_fmaf(zv, 1.f - sg, 1.f));
-          } else {
-            dz[q] = 0.f;
-          }
         }
-        const int64_t at = (row0 + t + it) * D + d0 + ic;
+        if (with_softplus) {
+#pragma unroll
+          for (int q = 0; q < V; ++q) dd[q] *= sigmoid(cdl.get(q) + m.bias[ic + q]);
+        }
+#pragma unroll
+        for (int q = 0; q < V; ++q) dbias[q] += dd[q];
+        const int64_t at = (row0 + j * kTile) * D + d0;
+        const uint32_t off = (uint32_t)(it * D + ic);
+        const int nvec = FULL ? V : iv;
         Raw<T, V> r;
         r.pack(du);
-        r.store_n(static_cast<T*>(k.g.du) + at, iv);
+        r.store_n(static_cast<T*>(w->g.du) + at + off, nvec);
         r.pack(dd);
-        r.store_n(static_cast<T*>(k.g.ddelta) + at, iv);
+        r.store_n(static_cast<T*>(w->g.ddelta) + at + off, nvec);
         if (gated) {
-          r.pack(dz);
-          r.store_n(static_cast<T*>(k.g.dz) + at, iv);
+#pragma unroll
+          for (int q = 0; q < V; ++q) {
+            const float zv = cz.get(q), sg = sigmoid(zv);
+            du[q] = cdy.get(q) * __builtin_fmaf(m.skip[ic + q], cu.get(q), m.o[it][ic + q]) *
+                    (sg * __builtin_fmaf(zv, 1.f - sg, 1.f));
+          }
+          r.pack(du);
+          r.store_n(static_cast<T*>(w->g.dz) + at + off, nvec);
         }
       }
-      // dB and dC of the block's channels: two values a lane, the waves in order.
+      // dB and dC of the block's channels: one state of one token a lane, the waves in order.
+      if (eT < nt && (FULL || eN < N)) {
+        float* const to = bc0 + (int64_t)j * kTile * bc_row + (uint32_t)eT * bc_row + eN;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int q = tid / NP, n = tid % NP;
-        if (q < nt && n < N) {
-          float r = m.bc[0][q][i * NP + n];
+        for (int i = 0; i < 2; ++i) {
+          float r = m.bc[0][eT][i * NP + eN];
 #pragma unroll
-          for (int w = 1; w < NG; ++w) r += m.bc[w][q][i * NP + n];
-          k.part_bc[(cblock * 2 + i) * bc + ((row0 + t + q) * a.groups + g) * N + n] = real ? r : 0.f;
+          for (int w = 1; w < NG; ++w) r += m.bc[w][eT][i * NP + eN];
+          to[i * bc] = r;
         }
       }
       __syncthreads();
     }
-    if (real && p.t0 == 0 && k.g.dstate && on) {
+    if (p.t0 == 0 && k.g.dstate && on) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (FULL || i < nv) k.g.dstate[((int64_t)p.seq * D + d) * N + n0 + i] = c[i];
+        if (FULL || i < nv) k.g.dstate[((int64_t)p.seq * D + d0 + ch) * N + n0 + i] = c[i];
     }
   }
   if (on) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (FULL || i < nv) k.part_a[(int64_t)part * D * N + (int64_t)d * N + n0 + i] = dA[i];
+      if (FULL || i < nv) k.part_a[(int64_t)part * D * N + (int64_t)(d0 + ch) * N + n0 + i] = dA[i];
   }
 #pragma unroll
   for (int q = 0; q < V; ++q) {
@@ -302,7 +418,8 @@ hipError_t grad_t(const GradArgs& k, hipStream_t stream) {
 
 hipError_t grad_any(const GradArgs& k, hipStream_t stream) {
 #define CALL(T, NP, FULL) grad_t<T, NP, FULL>(k, stream)
-  SCAN_DISPATCH(CALL, k.s.a.dtype, k.s.a.states)
+  const bool whole = k.s.a.channels / k.s.a.groups % 64 == 0;
+  SCAN_DISPATCH4(CALL, k.s.a.dtype, k.s.a.states, whole)
 #undef CALL
 }
 

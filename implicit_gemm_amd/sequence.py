@@ -20,11 +20,13 @@ is a function of its own, and there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from collections import namedtuple
 
 import torch
 
-from . import ConvWgradError, _dtype_code, load
+from . import BF16, F16, F32, ConvWgradError, load
 
 
 class _View(ctypes.Structure):
@@ -91,191 +93,200 @@ class ScanGradArgs(ctypes.Structure):
 ScanGrads = namedtuple("ScanGrads", "du ddelta dA dB dC dskip dz ddelta_bias dstate")
 ScanGrads.__doc__ = """Gradients of selective_scan; None where the input was not given."""
 
-_bound = None
+# A call on a few tokens takes a few microseconds on the GPU, so what the host does for it counts: arguments are packed
+# by one struct.pack, checks take one comparison of each property (a second function words the error), and workspace
+# sizes are remembered by the sizes that they depend on.
+
+def _format(struct_type):
+    """struct format of a ctypes Structure, nested ones flattened (native alignment, as in C)."""
+    codes = {ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f", ctypes.c_void_p: "P"}
+    return "".join(codes[t] if t in codes else _format(t) for _, t in struct_type._fields_)
 
 
+_NORM, _NORM_GRAD, _CONV, _CONV_GRAD, _SCAN, _SCAN_GRAD = (
+    struct.Struct("@" + _format(t)).pack
+    for t in (NormArgs, NormGradArgs, ConvArgs, ConvGradArgs, ScanArgs, ScanGradArgs))
+
+_CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+_f32 = torch.float32
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda index: torch.cuda.current_stream(index).cuda_stream
+
+
+@functools.lru_cache(None)
 def _lib():
     """The library with the argument types of the sequence entries."""
-    global _bound
-    if _bound is None:
-        lib = load()
-        P, ptr, size = ctypes.POINTER, ctypes.c_void_p, ctypes.c_size_t
-        for name, args in (("seq_rms_norm", NormArgs), ("seq_rms_norm_e4m3", NormArgs), ("seq_causal_conv", ConvArgs),
-                           ("seq_causal_conv_step", ConvArgs), ("seq_selective_scan_step", ScanArgs)):
-            getattr(lib, name).argtypes = [P(args), ptr]
-        for name, args in (("seq_rms_norm_grad", NormGradArgs), ("seq_causal_conv_grad", ConvGradArgs),
-                           ("seq_selective_scan", ScanArgs), ("seq_selective_scan_grad", ScanGradArgs)):
-            getattr(lib, name).argtypes = [P(args), ptr, size, ptr]
-        for name, args in (("seq_rms_norm_grad_workspace", NormGradArgs),
-                           ("seq_causal_conv_grad_workspace", ConvGradArgs), ("seq_selective_scan_save", ScanArgs),
-                           ("seq_selective_scan_workspace", ScanArgs),
-                           ("seq_selective_scan_grad_workspace", ScanGradArgs)):
-            getattr(lib, name).argtypes = [P(args), P(size)]
-        _bound = lib
-    return _bound
+    lib = load()
+    ptr, size = ctypes.c_void_p, ctypes.c_size_t
+    for name in ("seq_rms_norm", "seq_rms_norm_e4m3", "seq_causal_conv", "seq_causal_conv_step",
+                 "seq_selective_scan_step"):
+        getattr(lib, name).argtypes = [ptr, ptr]
+    for name in ("seq_rms_norm_grad", "seq_causal_conv_grad", "seq_selective_scan", "seq_selective_scan_grad"):
+        getattr(lib, name).argtypes = [ptr, ptr, size, ptr]
+    for name in ("seq_rms_norm_grad_workspace", "seq_causal_conv_grad_workspace", "seq_selective_scan_save",
+                 "seq_selective_scan_workspace", "seq_selective_scan_grad_workspace"):
+        getattr(lib, name).argtypes = [ptr, ctypes.POINTER(size)]
+    return lib
 
 
-def _check(status, what):
-    if status:
-        raise ConvWgradError(status, what)
-
-
-def _bytes(name, args):
+def _bytes(name, packed):
     n = ctypes.c_size_t(0)
-    _check(getattr(_lib(), name)(ctypes.byref(args), ctypes.byref(n)), name)
+    status = getattr(_lib(), name)(packed, ctypes.byref(n))
+    if status:
+        raise ConvWgradError(status, name)
     return n.value
 
 
-class _On:
-    """The stream of a call as the current one, on the device of its tensors (nothing to do where it already is):
-    outputs and workspaces allocated inside belong to the stream that the kernels run on."""
-
-    def __init__(self, t, stream):
-        if not t.is_cuda:
-            raise ValueError("tensors must be on a GPU")
-        self.guards = []
-        index = t.device.index
-        if index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(index))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(stream))
-        self.stream = stream
-        self.device = t.device
-
-    def __enter__(self):
-        for g in self.guards:
-            g.__enter__()
-        return (self.stream or torch.cuda.current_stream(self.device)).cuda_stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _here(t, stream):
+    """Handle of the current stream if a call on t runs there, None if it has to change stream or device first."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError("tensors must be on a GPU")
+    if stream is None and index == torch.cuda.current_device():
+        return _raw_stream(index)
+    return None
 
 
-def _like(t, name, shape, dtype, device):
-    """A tensor of that shape, type and device whose last axis is contiguous."""
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape):
+def _there(t, stream, call, *args):
+    """The call with the stream as the current one, so that what it allocates belongs to the stream that its kernels
+    run on, on the device of t."""
+    with torch.cuda.device(t.get_device()):
+        if stream is None:
+            return call(*args)
+        with torch.cuda.stream(stream):
+            return call(*args)
+
+
+def _refuse(t, name, shape, dtype, index):
+    if not isinstance(t, torch.Tensor) or t.shape != torch.Size(shape):
         raise ValueError("%s must be a tensor of shape %s, got %s" % (name, tuple(shape), getattr(t, "shape", t)))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError("the last axis of %s must be contiguous" % name)
-    return t
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, expected GPU %d" % (name, t.device, index))
+    raise ValueError("the last axis of %s must be contiguous" % name)
 
 
-def _param(t, name, shape, device):
-    """Pointer of a contiguous float32 parameter, 0 for None."""
+def _like(t, name, shape, dtype, index):
+    """Strides of a tensor of that shape, type and device whose last axis is contiguous."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        _refuse(t, name, shape, dtype, index)
+    strides = t.stride()
+    if strides[-1] != 1 and t.shape[-1] > 1:
+        _refuse(t, name, shape, dtype, index)
+    return strides
+
+
+def _dense(t, name, shape, dtype, index):
+    """Pointer of a contiguous tensor of that shape, type and device; 0 for None."""
     if t is None:
         return 0
-    _like(t, name, shape, torch.float32, device)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        _refuse(t, name, shape, dtype, index)
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
     return t.data_ptr()
 
 
-def _dense(t, name, shape, dtype, device):
-    _like(t, name, shape, dtype, device)
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t
+def _code(t):
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError("elements must be float32, bfloat16 or float16, got %s" % t.dtype)
+    return code
 
 
-def _view(t, packed):
-    """seq_view_t of [S, L, ...] or, packed, [T, ...]."""
-    return (t.data_ptr(), 0, t.stride(0)) if packed else (t.data_ptr(), t.stride(0), t.stride(1))
-
-
-def _index(t, name, n, device):
-    if t is None:
-        return 0
-    if t.dtype != torch.int32 or tuple(t.shape) != (n,) or t.device != device or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous int32 tensor of shape (%d,) on %s" % (name, n, device))
-    return t.data_ptr()
+def _empty(shape, dtype, like):
+    return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _sequences(x, offsets, name):
-    """(packed, sequences, rows) of [S, L, channels], or of [T, channels] with offsets."""
+    """(sequences, rows of each or in all) of [S, L, channels], or of [T, channels] with offsets."""
+    shape = x.shape
     if offsets is None:
-        if x.dim() != 3:
-            raise ValueError("%s must be [S, L, channels] without offsets, got shape %s" % (name, tuple(x.shape)))
-        return False, x.shape[0], x.shape[1]
-    if x.dim() != 2:
-        raise ValueError("%s must be [T, channels] with offsets, got shape %s" % (name, tuple(x.shape)))
+        if len(shape) != 3:
+            raise ValueError("%s must be [S, L, channels] without offsets, got shape %s" % (name, tuple(shape)))
+        return shape[0], shape[1]
+    if len(shape) != 2:
+        raise ValueError("%s must be [T, channels] with offsets, got shape %s" % (name, tuple(shape)))
     if offsets.dim() != 1 or offsets.shape[0] < 2:
         raise ValueError("offsets must hold S + 1 >= 2 row numbers")
-    return True, offsets.shape[0] - 1, x.shape[0]
+    return offsets.shape[0] - 1, shape[0]
 
 
-def _pool(state, state_out, slots, S, each, dtype, device):
-    """(slots pointer, pool) after the checks of the states and slots of a call."""
-    pools = {t.shape[0] for t in (state, state_out) if t is not None and t.dim() == 1 + len(each)}
-    if len(pools) > 1:
-        raise ValueError("state and state_out must hold the same number of states")
-    P = pools.pop() if pools else S
+def _pool(state, state_out, slots, S, each, dtype, index):
+    """(slots, pool, state, its stride, state_out, its stride) for the arguments, after the checks of the states."""
+    given = state if state is not None else state_out
+    P = S if given is None else given.shape[0] if given.dim() else -1
+    out = []
     for t, name in ((state, "state"), (state_out, "state_out")):
-        if t is not None:
-            _like(t, name, (P,) + each, dtype, device)
-            if t.shape[0] and not t[0].is_contiguous():
-                raise ValueError("each state of %s must be contiguous" % name)
+        if t is None:
+            out += (0, 0)
+            continue
+        if t is state and out and name == "state_out":
+            out += out
+            continue
+        strides = _like(t, name, (P,) + each, dtype, index)
+        if strides[1] != each[1] and each[0] > 1:
+            raise ValueError("each state of %s must be contiguous" % name)
+        out += (t.data_ptr(), strides[0])
     if slots is None and P != S:
         raise ValueError("%d states for %d sequences: slots must say which" % (P, S))
-    if P == 0:
-        raise ValueError("the pool is empty")
-    return _index(slots, "slots", S, device), P
+    if P < 1:
+        raise ValueError("there must be at least one sequence and one state")
+    return (_dense(slots, "slots", (S,), torch.int32, index), P), out
 
 
-def _state(t):
-    return (0, 0) if t is None else (t.data_ptr(), t.stride(0))
+def _default_out(state_out, slots, state, S, each, dtype, like):
+    """Where final states go: the pool itself with slots, else a new tensor."""
+    if state_out is not None:
+        return state_out
+    return state if slots is not None else _empty((S,) + each, dtype, like)
 
 
 # ---------------------------------------------------------------------------------------------------------- norm
 
 def _rows(t, name):
     """(row count, row stride) of [..., channels] whose rows lie a fixed distance apart."""
-    if t.dim() < 1 or t.shape[-1] < 1:
+    shape, strides = t.shape, t.stride()
+    if not shape or shape[-1] < 1:
         raise ValueError("%s must be [..., channels]" % name)
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError("the last axis of %s must be contiguous" % name)
-    if t.dim() == 2:
-        return t.shape[0], t.stride(0)
-    if t.dim() == 1:
-        return 1, t.shape[0]
-    rows = t.numel() // t.shape[-1]
-    axes = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n != 1]
+    if len(shape) == 2:
+        return shape[0], strides[0]
+    axes = [(n, s) for n, s in zip(shape[:-1], strides[:-1]) if n != 1]
     for (_, outer), (n, inner) in zip(axes, axes[1:]):
         if outer != n * inner:
             raise ValueError("the rows of %s must lie a fixed distance apart" % name)
-    return rows, axes[-1][1] if axes else t.shape[-1]
+    return t.numel() // shape[-1], axes[-1][1] if axes else shape[-1]
 
 
-def _norm_args(x, w, residual, eps, group):
-    dtype = _dtype_code(x)
-    rows, x_row = _rows(x, "x")
-    C = x.shape[-1]
-    res_row = 0
-    if residual is not None:
-        _like(residual, "residual", x.shape, x.dtype, x.device)
-        res_row = _rows(residual, "residual")[1]
-    return rows, NormArgs(rows, C, dtype, group, eps, 0, x.data_ptr(), x_row,
-                          residual.data_ptr() if residual is not None else 0, res_row, _param(w, "w", (C,), x.device))
+def _residual(residual, x, index):
+    """(pointer, row stride, h pointer, h): what the addition of a residual reads and writes."""
+    if residual is None:
+        return 0, 0, 0, x
+    if residual.shape != x.shape or residual.dtype is not x.dtype or residual.get_device() != index:
+        _refuse(residual, "residual", x.shape, x.dtype, index)
+    h = _empty(x.shape, x.dtype, x)
+    return residual.data_ptr(), _rows(residual, "residual")[1], h.data_ptr(), h
 
 
 def rms_norm(x, w, residual=None, eps=1e-5, stream=None):
     """y = h r w with h = x + residual and r = 1 / sqrt(mean(h^2) + eps) over the last axis of x [..., C]; returns
     (y, h, r).  h is rounded to the element type before the norm reads it and is x itself without a residual; w [C] and
     r [...] are float32."""
-    with _On(x, stream) as s:
-        rows, a = _norm_args(x, w, residual, eps, 0)
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        r = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        h = x
-        if residual is not None:
-            h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            a.h = h.data_ptr()
-        a.y, a.rstd = y.data_ptr(), r.data_ptr()
-        _check(_lib().seq_rms_norm(ctypes.byref(a), s), "rms_norm")
+    on = _here(x, stream)
+    if on is None:
+        return _there(x, stream, rms_norm, x, w, residual, eps)
+    shape, dtype, index, code = x.shape, x.dtype, x.get_device(), _code(x)
+    rows, x_row = _rows(x, "x")
+    res, res_row, h_ptr, h = _residual(residual, x, index)
+    y, r = _empty(shape, dtype, x), _empty(shape[:-1], _f32, x)
+    status = _lib().seq_rms_norm(
+        _NORM(rows, shape[-1], code, 0, eps, 0, x.data_ptr(), x_row, res, res_row, _dense(w, "w", shape[-1:], _f32, index),
+              y.data_ptr(), h_ptr, r.data_ptr(), 0), on)
+    if status:
+        raise ConvWgradError(status, "rms_norm")
     return y, h, r
 
 
@@ -283,58 +294,69 @@ def rms_norm_e4m3(x, w, residual=None, eps=1e-5, group=0, stream=None):
     """The norm of rms_norm in 8 bits: (q, scale, h) with q float8_e4m3fn [..., C] and float32 scale [..., ceil(C /
     group)], one per `group` (32, 64, 128 or 256) channels or, for group 0, one per row: scale = max|y| / 448 (1 where
     that is zero), q = y / scale."""
-    with _On(x, stream) as s:
-        rows, a = _norm_args(x, w, residual, eps, group)
-        C = x.shape[-1]
-        q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-        scale = torch.empty(x.shape[:-1] + (-(-C // group) if group else 1,), dtype=torch.float32, device=x.device)
-        h = x
-        if residual is not None:
-            h = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-            a.h = h.data_ptr()
-        a.y, a.scale = q.data_ptr(), scale.data_ptr()
-        _check(_lib().seq_rms_norm_e4m3(ctypes.byref(a), s), "rms_norm_e4m3")
+    on = _here(x, stream)
+    if on is None:
+        return _there(x, stream, rms_norm_e4m3, x, w, residual, eps, group)
+    shape, index, code = x.shape, x.get_device(), _code(x)
+    rows, x_row = _rows(x, "x")
+    C = shape[-1]
+    res, res_row, h_ptr, h = _residual(residual, x, index)
+    q, scale = _empty(shape, torch.float8_e4m3fn, x), _empty(shape[:-1] + (-(-C // group) if group > 0 else 1,), _f32, x)
+    status = _lib().seq_rms_norm_e4m3(
+        _NORM(rows, C, code, group, eps, 0, x.data_ptr(), x_row, res, res_row, _dense(w, "w", (C,), _f32, index),
+              q.data_ptr(), h_ptr, 0, scale.data_ptr()), on)
+    if status:
+        raise ConvWgradError(status, "rms_norm_e4m3")
     return q, scale, h
+
+
+@functools.lru_cache(4096)
+def _norm_grad_space(rows, C, code):
+    return _bytes("seq_rms_norm_grad_workspace", _NORM_GRAD(rows, C, code, *[0] * 11))
 
 
 def rms_norm_grad(dy, h, w, r, dh=None, stream=None):
     """Gradients of rms_norm, from its h and r: (dx, dw).  dx is the gradient of x and of the residual alike; dh is the
     gradient that reaches h by another way (the residual stream behind it)."""
-    with _On(h, stream) as s:
-        dtype = _dtype_code(h)
-        rows, h_row = _rows(h, "h")
-        C = h.shape[-1]
-        _like(dy, "dy", h.shape, h.dtype, h.device)
-        if dh is not None:
-            _like(dh, "dh", h.shape, h.dtype, h.device)
-        if r.dtype != torch.float32 or r.shape != h.shape[:-1] or r.device != h.device or not r.is_contiguous():
-            raise ValueError("r must be what rms_norm returned for h")
-        a = NormGradArgs(rows, C, dtype, 0, dy.data_ptr(), _rows(dy, "dy")[1], h.data_ptr(), h_row,
-                         dh.data_ptr() if dh is not None else 0, _rows(dh, "dh")[1] if dh is not None else 0,
-                         _param(w, "w", (C,), h.device), r.data_ptr())
-        dx = torch.empty(h.shape, dtype=h.dtype, device=h.device)
-        dw = torch.empty((C,), dtype=torch.float32, device=h.device)
-        a.dx, a.dw = dx.data_ptr(), dw.data_ptr()
-        n = _bytes("seq_rms_norm_grad_workspace", a)
-        ws = torch.empty(n, dtype=torch.uint8, device=h.device)
-        _check(_lib().seq_rms_norm_grad(ctypes.byref(a), ws.data_ptr(), n, s), "rms_norm_grad")
+    on = _here(h, stream)
+    if on is None:
+        return _there(h, stream, rms_norm_grad, dy, h, w, r, dh)
+    shape, dtype, index, code = h.shape, h.dtype, h.get_device(), _code(h)
+    rows, h_row = _rows(h, "h")
+    C = shape[-1]
+    _like(dy, "dy", shape, dtype, index)
+    if dh is not None:
+        _like(dh, "dh", shape, dtype, index)
+    dx, dw = _empty(shape, dtype, h), _empty((C,), _f32, h)
+    n = _norm_grad_space(rows, C, code)
+    ws = _empty(n, torch.uint8, h)
+    status = _lib().seq_rms_norm_grad(
+        _NORM_GRAD(rows, C, code, 0, dy.data_ptr(), _rows(dy, "dy")[1], h.data_ptr(), h_row,
+                   dh.data_ptr() if dh is not None else 0, _rows(dh, "dh")[1] if dh is not None else 0,
+                   _dense(w, "w", (C,), _f32, index), _dense(r, "r", shape[:-1], _f32, index), dx.data_ptr(),
+                   dw.data_ptr()), ws.data_ptr(), n, on)
+    if status:
+        raise ConvWgradError(status, "rms_norm_grad")
     return dx, dw
 
 
 # --------------------------------------------------------------------------------------------------- convolution
 
-def _conv_args(x, w, b, silu, offsets, slots, state, state_out, name="x"):
-    packed, S, L = _sequences(x, offsets, name)
+def _conv_args(x, xs, S, L, w, b, silu, offsets, slots, state, state_out, index):
+    """(taps, the arguments of seq_conv_args_t up to y); xs: (batch, row) strides of x."""
     D = x.shape[-1]
     if w.dim() != 2 or w.shape[0] != D:
         raise ValueError("w must be [%d, taps], got shape %s" % (D, tuple(w.shape)))
     W = w.shape[1]
-    _like(x, name, x.shape, x.dtype, x.device)
-    slot_ptr, P = _pool(state, state_out, slots, S, (W - 1, D), x.dtype, x.device)
-    tokens = (S, L, _index(offsets, "offsets", S + 1, x.device), slot_ptr, P)
-    a = ConvArgs(tokens, D, W, _dtype_code(x), bool(silu), 0, _view(x, packed), _param(w, "w", (D, W), x.device),
-                 _param(b, "b", (D,), x.device), *_state(state), *_state(state_out))
-    return packed, S, a
+    pool, states = _pool(state, state_out, slots, S, (W - 1, D), x.dtype, index)
+    return W, (S, L, _dense(offsets, "offsets", (S + 1,), torch.int32, index), *pool, D, W, _code(x), bool(silu), 0,
+               x.data_ptr(), *xs, _dense(w, "w", (D, W), _f32, index), _dense(b, "b", (D,), _f32, index), *states)
+
+
+def _strides(t, name, offsets, index):
+    """(batch, row) strides of x itself."""
+    s = _like(t, name, t.shape, t.dtype, index)
+    return s[:2] if offsets is None else (0, s[0])
 
 
 def causal_conv(x, w, b=None, silu=False, offsets=None, slots=None, state=None, state_out=None, stream=None):
@@ -344,80 +366,115 @@ def causal_conv(x, w, b=None, silu=False, offsets=None, slots=None, state=None, 
     `state` [P, W - 1, D] (the element type) holds the W - 1 inputs before each sequence, oldest first; None: zeros.
     The windows after the last tokens go to state_out: a new tensor by default or, with slots, `state` itself; it may
     be `state`, and must not overlap it otherwise."""
-    with _On(x, stream) as s:
-        if state_out is None:
-            if slots is not None:
-                state_out = state
-            else:
-                S = x.shape[0] if offsets is None else offsets.shape[0] - 1
-                state_out = torch.empty((S, w.shape[-1] - 1, x.shape[-1]), dtype=x.dtype, device=x.device)
-        packed, S, a = _conv_args(x, w, b, silu, offsets, slots, state, state_out)
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        a.y = _View(*_view(y, packed))
-        _check(_lib().seq_causal_conv(ctypes.byref(a), s), "causal_conv")
+    on = _here(x, stream)
+    if on is None:
+        return _there(x, stream, causal_conv, x, w, b, silu, offsets, slots, state, state_out)
+    index = x.get_device()
+    S, L = _sequences(x, offsets, "x")
+    shape = x.shape
+    state_out = _default_out(state_out, slots, state, S, (w.shape[-1] - 1, shape[-1]), x.dtype, x)
+    _, args = _conv_args(x, _strides(x, "x", offsets, index), S, L, w, b, silu, offsets, slots, state, state_out, index)
+    y = _empty(shape, x.dtype, x)
+    D = shape[-1]
+    status = _lib().seq_causal_conv(_CONV(*args, y.data_ptr(), L * D if offsets is None else 0, D), on)
+    if status:
+        raise ConvWgradError(status, "causal_conv")
     return y, state_out
 
 
 def causal_conv_step(x, state, w, b=None, silu=False, slots=None, state_out=None, stream=None):
     """causal_conv for one token of each sequence: x [S, D] -> y [S, D].  The new windows go to state_out, by default
     `state` itself."""
-    with _On(x, stream) as s:
-        if x.dim() != 2:
-            raise ValueError("x must be [S, D], got shape %s" % (tuple(x.shape),))
-        packed, S, a = _conv_args(x.unsqueeze(1), w, b, silu, None, slots, state, state if state_out is None else state_out)
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        a.y = _View(y.data_ptr(), y.stride(0), 0)
-        _check(_lib().seq_causal_conv_step(ctypes.byref(a), s), "causal_conv_step")
+    on = _here(x, stream)
+    if on is None:
+        return _there(x, stream, causal_conv_step, x, state, w, b, silu, slots, state_out)
+    shape, index = x.shape, x.get_device()
+    if len(shape) != 2:
+        raise ValueError("x must be [S, D], got shape %s" % (tuple(shape),))
+    batch = _like(x, "x", shape, x.dtype, index)[0]
+    _, args = _conv_args(x, (batch, 0), shape[0], 1, w, b, silu, None, slots, state,
+                         state if state_out is None else state_out, index)
+    y = _empty(shape, x.dtype, x)
+    status = _lib().seq_causal_conv_step(_CONV(*args, y.data_ptr(), shape[1], 0), on)
+    if status:
+        raise ConvWgradError(status, "causal_conv_step")
     return y
+
+
+@functools.lru_cache(4096)
+def _conv_grad_space(S, L, packed, D, W, code):
+    tokens = (S, L, 16 if packed else 0, 0, S)
+    fwd = (*tokens, D, W, code, 0, 0, 16, 0, 0, 16, 0, 0, 0, 0, 0, 16, 0, 0)
+    return _bytes("seq_causal_conv_grad_workspace", _CONV_GRAD(*fwd, *[0] * 10))
 
 
 def causal_conv_grad(dy, x, w, b=None, silu=False, offsets=None, slots=None, state=None, dstate_out=None, stream=None):
     """Gradients of causal_conv: (dx, dw, db, dstate), db None without b and dstate [S, W - 1, D] None without state.
     dstate_out [S, W - 1, D]: the gradient of the outgoing windows."""
-    with _On(x, stream) as s:
-        packed, S, a = _conv_args(x, w, b, silu, offsets, slots, state, None)
-        D, W = w.shape
-        _like(dy, "dy", x.shape, x.dtype, x.device)
-        if dstate_out is not None:
-            _dense(dstate_out, "dstate_out", (S, W - 1, D), x.dtype, x.device)
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty((D, W), dtype=torch.float32, device=x.device)
-        db = torch.empty((D,), dtype=torch.float32, device=x.device) if b is not None else None
-        dstate = torch.empty((S, W - 1, D), dtype=x.dtype, device=x.device) if state is not None else None
-        g = ConvGradArgs(a, _view(dy, packed), dstate_out.data_ptr() if dstate_out is not None else 0, _view(dx, packed),
-                         dw.data_ptr(), db.data_ptr() if b is not None else 0,
-                         dstate.data_ptr() if state is not None else 0)
-        n = _bytes("seq_causal_conv_grad_workspace", g)
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-        _check(_lib().seq_causal_conv_grad(ctypes.byref(g), ws.data_ptr(), n, s), "causal_conv_grad")
+    on = _here(x, stream)
+    if on is None:
+        return _there(x, stream, causal_conv_grad, dy, x, w, b, silu, offsets, slots, state, dstate_out)
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    S, L = _sequences(x, offsets, "x")
+    W, args = _conv_args(x, _strides(x, "x", offsets, index), S, L, w, b, silu, offsets, slots, state, None, index)
+    D = shape[-1]
+    dys = _like(dy, "dy", shape, dtype, index)
+    dx, dw = _empty(shape, dtype, x), _empty((D, W), _f32, x)
+    db = _empty((D,), _f32, x) if b is not None else None
+    dstate = _empty((S, W - 1, D), dtype, x) if state is not None else None
+    n = _conv_grad_space(S, L, offsets is not None, D, W, args[7])
+    ws = _empty(n, torch.uint8, x)
+    status = _lib().seq_causal_conv_grad(
+        _CONV_GRAD(*args, 0, 0, 0, dy.data_ptr(), *(dys[:2] if offsets is None else (0, dys[0])),
+                   _dense(dstate_out, "dstate_out", (S, W - 1, D), dtype, index), dx.data_ptr(),
+                   L * D if offsets is None else 0, D, dw.data_ptr(), db.data_ptr() if b is not None else 0,
+                   dstate.data_ptr() if state is not None else 0), ws.data_ptr(), n, on)
+    if status:
+        raise ConvWgradError(status, "causal_conv_grad")
     return dx, dw, db, dstate
 
 
 # ---------------------------------------------------------------------------------------------------------- scan
 
-def _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, slots, state, state_out, max_len):
-    packed, S, L = _sequences(u, offsets, "u")
-    D = u.shape[-1]
-    lead = 1 if packed else 2
+def _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, slots, state, state_out, max_len, S, L, step,
+               index):
+    """(groups, states, the arguments of seq_scan_args_t up to save)."""
+    shape, dtype = u.shape, u.dtype
+    D = shape[-1]
     if A.dim() != 2 or A.shape[0] != D:
         raise ValueError("A must be [%d, states], got shape %s" % (D, tuple(A.shape)))
     N = A.shape[1]
-    if B.dim() != lead + 2 or B.shape[-2] < 1 or D % B.shape[-2]:
+    G = B.shape[-2] if B.dim() == len(shape) + 1 else 0
+    if G < 1 or D % G:
         raise ValueError("B and C must be [..., groups, states] with groups dividing %d, got %s" % (D, tuple(B.shape)))
-    G = B.shape[-2]
-    _like(u, "u", u.shape, u.dtype, u.device)
-    for t, name in ((delta, "delta"), (z, "z")):
-        if t is not None:
-            _like(t, name, u.shape, u.dtype, u.device)
-    for t, name in ((B, "B"), (C, "C")):
-        _like(t, name, u.shape[:-1] + (G, N), u.dtype, u.device)
-    slot_ptr, P = _pool(state, state_out, slots, S, (D, N), torch.float32, u.device)
-    tokens = (S, L, _index(offsets, "offsets", S + 1, u.device), slot_ptr, P)
-    a = ScanArgs(tokens, D, G, N, _dtype_code(u), bool(softplus), 0, max_len or 0, _view(u, packed), _view(delta, packed),
-                 _view(z, packed) if z is not None else (0, 0, 0), _view(B, packed), _view(C, packed), B.stride(-2),
-                 C.stride(-2), _param(A, "A", (D, N), u.device), _param(skip, "skip", (D,), u.device),
-                 _param(delta_bias, "delta_bias", (D,), u.device), *_state(state), *_state(state_out))
-    return packed, S, a
+    wide = shape[:-1] + (G, N)
+    us, ds = _like(u, "u", shape, dtype, index), _like(delta, "delta", shape, dtype, index)
+    Bs, Cs = _like(B, "B", wide, dtype, index), _like(C, "C", wide, dtype, index)
+    zs = _like(z, "z", shape, dtype, index) if z is not None else us
+    z_ptr = z.data_ptr() if z is not None else 0
+    pool, states = _pool(state, state_out, slots, S, (D, N), _f32, index)
+    if step:
+        views = (u.data_ptr(), us[0], 0, delta.data_ptr(), ds[0], 0, z_ptr, zs[0], 0, B.data_ptr(), Bs[0], 0,
+                 C.data_ptr(), Cs[0], 0)
+    elif offsets is None:
+        views = (u.data_ptr(), us[0], us[1], delta.data_ptr(), ds[0], ds[1], z_ptr, zs[0], zs[1], B.data_ptr(), Bs[0],
+                 Bs[1], C.data_ptr(), Cs[0], Cs[1])
+    else:
+        views = (u.data_ptr(), 0, us[0], delta.data_ptr(), 0, ds[0], z_ptr, 0, zs[0], B.data_ptr(), 0, Bs[0],
+                 C.data_ptr(), 0, Cs[0])
+    return G, N, (S, L, _dense(offsets, "offsets", (S + 1,), torch.int32, index), *pool, D, G, N, _code(u),
+                  bool(softplus), 0, max_len or 0, *views, Bs[-2], Cs[-2], _dense(A, "A", (D, N), _f32, index),
+                  _dense(skip, "skip", (D,), _f32, index), _dense(delta_bias, "delta_bias", (D,), _f32, index), *states)
+
+
+@functools.lru_cache(4096)
+def _scan_space(S, L, packed, D, G, N, code, longest):
+    """Bytes of (saved, the forward's workspace, the gradient's)."""
+    fwd = (S, L, 16 if packed else 0, 0, S, D, G, N, code, 0, 0, longest, *[0] * 15, 0, 0, *[0] * 3, 0, 0, 0, 0, 0,
+           0, 0, 0)
+    a = _SCAN(*fwd)
+    return (_bytes("seq_selective_scan_save", a), _bytes("seq_selective_scan_workspace", a),
+            _bytes("seq_selective_scan_grad_workspace", _SCAN_GRAD(*fwd, *[0] * 13)))
 
 
 def selective_scan(u, delta, A, B, C, skip=None, z=None, delta_bias=None, softplus=False, offsets=None, max_len=None,
@@ -432,24 +489,26 @@ def selective_scan(u, delta, A, B, C, skip=None, z=None, delta_bias=None, softpl
     where their final states go: a new tensor by default or, with slots, `state` itself; the two may be the same.
     max_len (a Python int): no sequence is longer; with offsets, whose lengths the host does not see, it spares short
     sequences the launches that split long ones.  saved is for selective_scan_grad (None without save)."""
-    with _On(u, stream) as s:
-        if state_out is None:
-            if slots is not None:
-                state_out = state
-            else:
-                S = u.shape[0] if offsets is None else offsets.shape[0] - 1
-                state_out = torch.empty((S,) + tuple(A.shape), dtype=torch.float32, device=u.device)
-        packed, S, a = _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, slots, state, state_out,
-                                  max_len)
-        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
-        a.y = _View(*_view(y, packed))
-        saved = None
-        if save:
-            saved = torch.empty(_bytes("seq_selective_scan_save", a) // 4, dtype=torch.float32, device=u.device)
-            a.save = saved.data_ptr()
-        n = _bytes("seq_selective_scan_workspace", a)
-        ws = torch.empty(n, dtype=torch.uint8, device=u.device) if n else None
-        _check(_lib().seq_selective_scan(ctypes.byref(a), ws.data_ptr() if n else 0, n, s), "selective_scan")
+    on = _here(u, stream)
+    if on is None:
+        return _there(u, stream, selective_scan, u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, max_len,
+                      slots, state, state_out, save)
+    index = u.get_device()
+    S, L = _sequences(u, offsets, "u")
+    shape = u.shape
+    state_out = _default_out(state_out, slots, state, S, tuple(A.shape), _f32, u)
+    G, N, args = _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, slots, state, state_out, max_len, S,
+                            L, False, index)
+    D = shape[-1]
+    keep, n, _ = _scan_space(S, L, offsets is not None, D, G, N, args[8], max_len or 0)
+    y = _empty(shape, u.dtype, u)
+    saved = _empty(keep // 4, _f32, u) if save else None
+    ws = _empty(n, torch.uint8, u) if n else None
+    status = _lib().seq_selective_scan(
+        _SCAN(*args, saved.data_ptr() if save else 0, y.data_ptr(), L * D if offsets is None else 0, D),
+        ws.data_ptr() if n else 0, n, on)
+    if status:
+        raise ConvWgradError(status, "selective_scan")
     return y, state_out, saved
 
 
@@ -457,15 +516,19 @@ def selective_scan_step(u, delta, A, B, C, state, skip=None, z=None, delta_bias=
                         state_out=None, stream=None):
     """selective_scan for one token of each sequence: u, delta, z [S, D], B, C [S, G, N] -> y [S, D].  The new states
     go to state_out, by default `state` itself."""
-    with _On(u, stream) as s:
-        if u.dim() != 2:
-            raise ValueError("u must be [S, D], got shape %s" % (tuple(u.shape),))
-        packed, S, a = _scan_args(u.unsqueeze(1), delta.unsqueeze(1), A, B.unsqueeze(1), C.unsqueeze(1), skip,
-                                  z.unsqueeze(1) if z is not None else None, delta_bias, softplus, None, slots, state,
-                                  state if state_out is None else state_out, 1)
-        y = torch.empty(u.shape, dtype=u.dtype, device=u.device)
-        a.y = _View(y.data_ptr(), y.stride(0), 0)
-        _check(_lib().seq_selective_scan_step(ctypes.byref(a), s), "selective_scan_step")
+    on = _here(u, stream)
+    if on is None:
+        return _there(u, stream, selective_scan_step, u, delta, A, B, C, state, skip, z, delta_bias, softplus, slots,
+                      state_out)
+    shape = u.shape
+    if len(shape) != 2:
+        raise ValueError("u must be [S, D], got shape %s" % (tuple(shape),))
+    _, _, args = _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, None, slots, state,
+                            state if state_out is None else state_out, 1, shape[0], 1, True, u.get_device())
+    y = _empty(shape, u.dtype, u)
+    status = _lib().seq_selective_scan_step(_SCAN(*args, 0, y.data_ptr(), shape[1], 0), on)
+    if status:
+        raise ConvWgradError(status, "selective_scan_step")
     return y
 
 
@@ -473,29 +536,32 @@ def selective_scan_grad(dy, u, delta, A, B, C, saved, skip=None, z=None, delta_b
                         max_len=None, slots=None, state=None, dstate_out=None, stream=None):
     """Gradients of selective_scan, from dy, its inputs and its `saved`: a ScanGrads tuple.  dstate_out float32 [S, D,
     N]: the gradient of the final states; dstate is that of the first ones, in the order of the sequences."""
-    with _On(u, stream) as s:
-        packed, S, a = _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, slots, state, None, max_len)
-        D, N = A.shape
-        _like(dy, "dy", u.shape, u.dtype, u.device)
-        if dstate_out is not None:
-            _dense(dstate_out, "dstate_out", (S, D, N), torch.float32, u.device)
-        need = _bytes("seq_selective_scan_save", a) // 4
-        _dense(saved, "saved", (need,), torch.float32, u.device)
-        a.save = saved.data_ptr()
-
-        def empty(shape, dtype, wanted=True):
-            return torch.empty(shape, dtype=dtype, device=u.device) if wanted else None
-
-        f32 = torch.float32
-        out = ScanGrads(du=empty(u.shape, u.dtype), ddelta=empty(u.shape, u.dtype), dA=empty((D, N), f32),
-                        dB=empty(B.shape, u.dtype), dC=empty(B.shape, u.dtype), dskip=empty((D,), f32, skip is not None),
-                        dz=empty(u.shape, u.dtype, z is not None),
-                        ddelta_bias=empty((D,), f32, delta_bias is not None),
-                        dstate=empty((S, D, N), f32, state is not None))
-        g = ScanGradArgs(a, _view(dy, packed), dstate_out.data_ptr() if dstate_out is not None else 0,
-                         *(t.data_ptr() if t is not None else 0 for t in
-                           (out.du, out.ddelta, out.dz, out.dB, out.dC, out.dA, out.dskip, out.ddelta_bias, out.dstate)))
-        n = _bytes("seq_selective_scan_grad_workspace", g)
-        ws = torch.empty(n, dtype=torch.uint8, device=u.device)
-        _check(_lib().seq_selective_scan_grad(ctypes.byref(g), ws.data_ptr(), n, s), "selective_scan_grad")
-    return out
+    on = _here(u, stream)
+    if on is None:
+        return _there(u, stream, selective_scan_grad, dy, u, delta, A, B, C, saved, skip, z, delta_bias, softplus, offsets,
+                      max_len, slots, state, dstate_out)
+    shape, dtype, index = u.shape, u.dtype, u.get_device()
+    S, L = _sequences(u, offsets, "u")
+    G, N, args = _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, slots, state, None, max_len, S, L,
+                            False, index)
+    D = shape[-1]
+    keep, _, n = _scan_space(S, L, offsets is not None, D, G, N, args[8], max_len or 0)
+    dys = _like(dy, "dy", shape, dtype, index)
+    saved_ptr = _dense(saved, "saved", (keep // 4,), _f32, index)
+    du, ddelta = _empty(shape, dtype, u), _empty(shape, dtype, u)
+    dB, dC = _empty(B.shape, dtype, u), _empty(B.shape, dtype, u)
+    dA = _empty((D, N), _f32, u)
+    dz = _empty(shape, dtype, u) if z is not None else None
+    dskip = _empty((D,), _f32, u) if skip is not None else None
+    dbias = _empty((D,), _f32, u) if delta_bias is not None else None
+    dstate = _empty((S, D, N), _f32, u) if state is not None else None
+    ws = _empty(n, torch.uint8, u)
+    status = _lib().seq_selective_scan_grad(
+        _SCAN_GRAD(*args, saved_ptr, 0, 0, 0, dy.data_ptr(), *(dys[:2] if offsets is None else (0, dys[0])),
+                   _dense(dstate_out, "dstate_out", (S, D, N), _f32, index), du.data_ptr(), ddelta.data_ptr(),
+                   dz.data_ptr() if z is not None else 0, dB.data_ptr(), dC.data_ptr(), dA.data_ptr(),
+                   dskip.data_ptr() if skip is not None else 0, dbias.data_ptr() if delta_bias is not None else 0,
+                   dstate.data_ptr() if state is not None else 0), ws.data_ptr(), n, on)
+    if status:
+        raise ConvWgradError(status, "selective_scan_grad")
+    return ScanGrads(du, ddelta, dA, dB, dC, dskip, dz, dbias, dstate)

@@ -582,7 +582,7 @@ conv_wgrad_status_t seq_selective_scan_step(const seq_scan_args_t* args, void* s
 /* Gradients, from dy, dstate_out (dense fp32 [sequences][channels][states], gradient of the final states, NULL: zero)
  * and fwd.save as the forward filled it.  Outputs dense: du, ddelta, dz (NULL without a gate) rows x channels, dB and
  * dC rows x groups x states, dA, dskip and ddelta_bias fp32 (the last two may be NULL), dstate fp32 [sequences]
- * [channels][states] or NULL.  fwd.y, fwd.state and fwd.state_out are not read. */
+ * [channels][states] or NULL.  Row strides stay below 2^26 elements.  fwd.y, fwd.state and fwd.state_out are not read. */
 typedef struct seq_scan_grad_args {
   seq_scan_args_t fwd;
   seq_view_t dy;

@@ -160,7 +160,7 @@ def test_scan_step_and_grad_refusals():
     assert lib.seq_selective_scan_grad(grad(), P, n.value - 1, None) == WORKSPACE
     for over, status in ((dict(du=0), NULL), (dict(dz=0), NULL), (dict(dA=0), NULL), (dict(dB=P + 2), MISALIGNED),
                          (dict(dy=sq._View(0, 80, 8)), NULL), (dict(fwd=scan_args(save=0)), NULL),
-                         (dict(fwd=scan_args(states=40)), UNSUPPORTED)):
+                         (dict(fwd=scan_args(states=40)), UNSUPPORTED), (dict(dy=sq._View(P, 80, 1 << 26)), UNSUPPORTED)):
         assert lib.seq_selective_scan_grad(grad(**over), P, n.value, None) == status, over
 
 
