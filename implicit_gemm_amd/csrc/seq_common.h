@@ -179,7 +179,6 @@ __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirs
 __device__ __forceinline__ int seq_start(const SeqMap& m, int s) {
   return min(max(m.offsets[s], 0), m.rows);
 }
-__device__ __forceinline__ int seq_base(const SeqMap& m, int s) { return (seq_start(m, s) >> m.shift) + s; }
 
 // Finds a piece; false for a number that names none.  All 64 lanes of the wave call it with the same number.
 __device__ __forceinline__ bool find_piece(const SeqMap& m, int piece, Piece& p) {
@@ -192,19 +191,23 @@ __device__ __forceinline__ bool find_piece(const SeqMap& m, int piece, Piece& p)
     p.first = 0;
     p.len = m.rows;
   } else {
-    // The last s with seq_base(s) <= piece among 0 .. S, 64 candidates at a time.
+    // The last s with seq_base(s) <= piece among 0 .. S, 64 candidates at a time; where it begins and ends is with the
+    // last round's lanes, unless the next sequence is beyond them.
     const int lane = threadIdx.x & 63;
-    int lo = 0, n = m.S + 1;
-    while (n > 1) {
-      const int step = (n + 63) >> 6;
-      const bool in = lane * step < n && seq_base(m, lo + lane * step) <= piece;
-      const int cnt = __popcll(__ballot(in));
+    int lo = 0, n = m.S + 1, step, cnt, v, had;
+    do {
+      had = n;
+      step = (n + 63) >> 6;
+      v = lane * step < n ? seq_start(m, lo + lane * step) : 0;
+      cnt = __popcll(__ballot(lane * step < n && (v >> m.shift) + lo + lane * step <= piece));
       if (cnt == 0) return false;
       lo = uniform(lo + (cnt - 1) * step);
       n = uniform(min(step, n - (cnt - 1) * step));
-    }
-    const int start = uniform(seq_start(m, lo));
-    const int stop = lo < m.S ? uniform(seq_start(m, lo + 1)) : m.rows;
+    } while (n > 1);
+    const int start = __builtin_amdgcn_readlane(v, cnt - 1);
+    int stop = m.rows;
+    if (lo < m.S)
+      stop = step == 1 && cnt < min(had, 64) ? __builtin_amdgcn_readlane(v, cnt) : uniform(seq_start(m, lo + 1));
     p.seq = lo;
     p.batch = 0;
     p.first = start;

@@ -14,13 +14,10 @@ namespace cw {
 
 namespace {
 
-constexpr int kConvShift = 4;      // 16 tokens a piece: all its loads are in flight together
-constexpr int kConvTokens = 1 << kConvShift;
-constexpr int kGradShift = 5;      // 32 tokens a piece of the gradient: its halo is on both sides
-constexpr int kGradBatch = 8;      // tokens whose loads are issued together
-
-template <typename T>
-constexpr int kVec = 16 / sizeof(T);
+constexpr int kBatch = 8, kGradBatch = 4;   // tokens whose loads are issued together
+// Channels of a lane.  The gradient holds two windows, the filters and their sums for each: with four it takes 180
+// registers, two waves a SIMD and 99 us (16384 tokens x 4096 channels, bf16), with two 101 registers and 92 us.
+constexpr int kVec = 4, kGradVec = 2;
 
 struct ConvArgs {
   seq_conv_args_t a;
@@ -65,7 +62,7 @@ __device__ __forceinline__ void write_window(const seq_conv_args_t& a, const Pie
       load_state<T, V>(r[i], a, slot, t + W - 1, c, nv);
     } else {
       r[i].clear();
-      if (nv > 0) r[i].load_n(row_at<const T>(a.x, p, t) + c, nv);
+      if (nv > 0) r[i].load_n(&at_lane(row_at<const T>(a.x, p, t), c), nv);
     }
   }
   if (nv > 0 && slot >= 0) {
@@ -75,46 +72,53 @@ __device__ __forceinline__ void write_window(const seq_conv_args_t& a, const Pie
   }
 }
 
-template <typename T, int W>
+// FULL: the channels fill the blocks of 256, so that no load or store needs a check.
+template <typename T, int W, bool FULL>
 __global__ __launch_bounds__(256) void conv_kernel(ConvArgs k) {
-  constexpr int V = kVec<T>;
+  constexpr int V = kVec, B = kBatch;
   const seq_conv_args_t& a = k.a;
   const int cb = (int)blockIdx.x % k.cblocks;
   const int piece = uniform(((int)blockIdx.x / k.cblocks) * 4 + ((int)threadIdx.x >> 6));
+  const int c = (cb * 64 + ((int)threadIdx.x & 63)) * V;
+  const int nv = FULL ? V : (int)a.channels - c;   // <= 0: no channel of this lane
+  float w[W][V], b[V];
+  load_taps<V, W>(a, c, nv, w, b);
   Piece p;
   if (piece >= k.pieces || !find_piece(k.m, piece, p)) return;
-  const int c = (cb * 64 + ((int)threadIdx.x & 63)) * V;
-  const int nv = (int)a.channels - c;   // <= 0: no channel of this lane
   const int n = p.end - p.t0;
   if (p.seq >= k.m.S) {
     Raw<T, V> zero;
     zero.clear();
     for (int i = 0; i < n; ++i)
-      if (nv > 0) zero.store_n(row_at<T>(a.y, p, p.t0 + i) + c, nv);
+      if (nv > 0) zero.store_n(&at_lane(row_at<T>(a.y, p, p.t0 + i), c), nv);
     return;
   }
   const int64_t slot = pool_slot(a.tokens.slots, a.tokens.pool, p.seq);
-  Raw<T, V> x[W - 1 + kConvTokens];
+  Raw<T, V> x[W - 1 + B], next[B];   // the window and a batch of tokens
+  auto fetch = [&](int u0) {
+#pragma unroll
+    for (int i = 0; i < B; ++i) {   // past the piece's end the last row again
+      next[i].clear();
+      if (nv > 0) next[i].load_n(&at_lane(row_at<const T>(a.x, p, p.t0 + min(u0 + i, n - 1)), c), nv);
+    }
+  };
+  if (n > 0) fetch(0);
 #pragma unroll
   for (int i = 0; i < W - 1; ++i) {
     if (p.t0 == 0) {
       load_state<T, V>(x[i], a, slot, i, c, nv);
     } else {
       x[i].clear();
-      if (nv > 0) x[i].load_n(row_at<const T>(a.x, p, p.t0 - (W - 1) + i) + c, nv);
+      if (nv > 0) x[i].load_n(&at_lane(row_at<const T>(a.x, p, p.t0 - (W - 1) + i), c), nv);
     }
   }
+  for (int u0 = 0; u0 < n; u0 += B) {
 #pragma unroll
-  for (int i = 0; i < kConvTokens; ++i) {
-    x[W - 1 + i].clear();
-    if (i < n && nv > 0) x[W - 1 + i].load_n(row_at<const T>(a.x, p, p.t0 + i) + c, nv);
-  }
-  float w[W][V], b[V];
-  load_taps<V, W>(a, c, nv, w, b);
+    for (int i = 0; i < B; ++i) x[W - 1 + i] = next[i];
+    if (u0 + B < n) fetch(u0 + B);
+    Raw<T, V> y[B];
 #pragma unroll
-  for (int i = 0; i < kConvTokens; ++i) {
-    if (i < n) {
-      Raw<T, V> y;
+    for (int i = 0; i < B; ++i) {
       float o[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -123,9 +127,13 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs k) {
         for (int q = 0; q < W; ++q) s = __builtin_fmaf(w[q][j], x[i + q].get(j), s);
         o[j] = a.silu ? s * sigmoid(s) : s;
       }
-      y.pack(o);
-      if (nv > 0) y.store_n(row_at<T>(a.y, p, p.t0 + i) + c, nv);
+      y[i].pack(o);
     }
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+      if (u0 + i < n && nv > 0) y[i].store_n(&at_lane(row_at<T>(a.y, p, p.t0 + u0 + i), c), nv);
+#pragma unroll
+    for (int i = 0; i < W - 1; ++i) x[i] = x[B + i];
   }
   if (k.window && p.end == p.len) write_window<T, V, W>(a, p, slot, c, nv);
 }
@@ -133,7 +141,7 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvArgs k) {
 // Outgoing windows on the incoming ones: after the outputs, as other pieces of the sequence read the old window.
 template <typename T, int W>
 __global__ __launch_bounds__(64) void conv_window_kernel(ConvArgs k) {
-  constexpr int V = kVec<T>;
+  constexpr int V = kVec;
   const int s = (int)blockIdx.x / k.cblocks, cb = (int)blockIdx.x % k.cblocks;
   Piece p;
   p.seq = s;
@@ -147,7 +155,7 @@ __global__ __launch_bounds__(64) void conv_window_kernel(ConvArgs k) {
 // One token of each sequence: four channels a lane, all loads at once; latency is all there is.
 template <typename T, int W>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs k) {
-  constexpr int V = 4;
+  constexpr int V = kVec;
   const seq_conv_args_t& a = k.a;
   const int s = (int)blockIdx.x / k.cblocks, cb = (int)blockIdx.x % k.cblocks;
   const int c = (cb * 256 + (int)threadIdx.x) * V;
@@ -187,16 +195,16 @@ struct ConvGradArgs {
   float* part;       // [parts][channels * (W + 1)]: dw as [channels][W], then dbias
 };
 
-template <typename T, int W>
-__global__ __launch_bounds__(256) void conv_grad_kernel(ConvGradArgs k) {
-  constexpr int V = 4, B = kGradBatch;
+template <typename T, int W, bool FULL>
+__global__ __launch_bounds__(256, 4) void conv_grad_kernel(ConvGradArgs k) {
+  constexpr int V = kGradVec, B = kGradBatch;
   __shared__ float lds[(W + 1) * V * 64];
   const seq_conv_grad_args_t& g = k.g;
   const seq_conv_args_t& a = g.fwd;
-  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  const int lane = (int)threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int cb = (int)blockIdx.x % k.cblocks, wg = (int)blockIdx.x / k.cblocks;
   const int c = (cb * 64 + lane) * V;
-  const int D = (int)a.channels, nv = D - c;
+  const int D = (int)a.channels, nv = FULL ? V : D - c;
   float w[W][V], b[V], dw[W + 1][V];   // dw[W]: the bias
   load_taps<V, W>(a, c, nv, w, b);
 #pragma unroll
@@ -205,7 +213,7 @@ __global__ __launch_bounds__(256) void conv_grad_kernel(ConvGradArgs k) {
     for (int j = 0; j < V; ++j) dw[q][j] = 0.f;
 
   for (int first = wg * 4; first < k.pieces; first += k.parts * 4) {
-    const int piece = uniform(first + wave);
+    const int piece = first + wave;
     Piece p;
     if (piece >= k.pieces || !find_piece(k.m, piece, p)) continue;
     const int n = p.end - p.t0;
@@ -213,7 +221,7 @@ __global__ __launch_bounds__(256) void conv_grad_kernel(ConvGradArgs k) {
       Raw<T, V> zero;
       zero.clear();
       for (int i = 0; i < n; ++i)
-        if (nv > 0) zero.store_n(row_at<T>(g.dx, p, p.t0 + i) + c, nv);
+        if (nv > 0) zero.store_n(&at_lane(row_at<T>(g.dx, p, p.t0 + i), c), nv);
       continue;
     }
     const int64_t slot = pool_slot(a.tokens.slots, a.tokens.pool, p.seq);
@@ -225,7 +233,7 @@ __global__ __launch_bounds__(256) void conv_grad_kernel(ConvGradArgs k) {
         load_state<T, V>(r, a, slot, i, c, nv);
       } else {
         r.clear();
-        if (nv > 0) r.load_n(row_at<const T>(a.x, p, p.t0 - (W - 1) + i) + c, nv);
+        if (nv > 0) r.load_n(&at_lane(row_at<const T>(a.x, p, p.t0 - (W - 1) + i), c), nv);
       }
 #pragma unroll
       for (int j = 0; j < V; ++j) {
@@ -233,87 +241,94 @@ __global__ __launch_bounds__(256) void conv_grad_kernel(ConvGradArgs k) {
         gw[i][j] = 0.f;
       }
     }
-    // Token t0 + i gives g there and then dx of the token W - 1 before it, for which g is complete.
+    // Token t0 + u gives g there and then dx of the token W - 1 before it, for which g is complete.
     const int total = n + W - 1;
+    const int inside = min(total, p.len - p.t0);   // of these there is an input
     Raw<T, V> nx[B], ndy[B];
+    auto fetch = [&](int u0) {
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        // past the sequence's end the last row again, whose g is not used
+        const int t = p.t0 + min(u0 + i, inside - 1);
+        if (nv > 0) {
+          nx[i].load_n(&at_lane(row_at<const T>(a.x, p, t), c), nv);
+          ndy[i].load_n(&at_lane(row_at<const T>(g.dy, p, t), c), nv);
+        }
+      }
+    };
+    // Tokens u0 .. u0 + B - 1 of the piece from rx and rdy.  EDGE: some have no input, are the next piece's for dw, or
+    // give dx of a token before the piece or of one that the outgoing window holds.
+    auto batch = [&](int u0, const Raw<T, V> (&rx)[B], const Raw<T, V> (&rdy)[B], auto edge) {
+      constexpr bool EDGE = decltype(edge)::value;
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int u = u0 + i;
+        if (EDGE && u >= total) break;
+        float out[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          const float x = rx[i].get(j);
+          float s = __builtin_fmaf(w[W - 1][j], x, b[j]);
+#pragma unroll
+          for (int q = 0; q < W - 1; ++q) s = __builtin_fmaf(w[q][j], xw[q][j], s);
+          float gr = rdy[i].get(j);
+          if (a.silu) {
+            const float sg = sigmoid(s);
+            gr *= sg * __builtin_fmaf(s, 1.f - sg, 1.f);
+          }
+          if (EDGE) gr = u < inside ? gr : 0.f;
+          const float gm = !EDGE || u < n ? gr : 0.f;
+          dw[W][j] += gm;
+          dw[W - 1][j] = __builtin_fmaf(gm, x, dw[W - 1][j]);
+#pragma unroll
+          for (int q = 0; q < W - 1; ++q) dw[q][j] = __builtin_fmaf(gm, xw[q][j], dw[q][j]);
+          // dx[tau] = sum_q w[q] g[tau + (W - 1) - q]
+          float o = w[0][j] * gr;
+#pragma unroll
+          for (int q = 1; q < W; ++q) o = __builtin_fmaf(w[q][j], gw[W - 1 - q][j], o);
+          out[j] = o;
+#pragma unroll
+          for (int q = 0; q < W - 2; ++q) {
+            xw[q][j] = xw[q + 1][j];
+            gw[q][j] = gw[q + 1][j];
+          }
+          xw[W - 2][j] = x;
+          gw[W - 2][j] = gr;
+        }
+        const int tau = p.t0 + u - (W - 1);
+        if (EDGE) {
+          // before the piece: another piece's token, or the incoming window
+          if (tau < p.t0 && (p.t0 > 0 || !g.dstate)) continue;
+          if (g.dstate_out && tau >= p.len - (W - 1) && nv > 0) {
+            Raw<T, V> r;
+            r.load_n(static_cast<const T*>(g.dstate_out) + ((int64_t)p.seq * (W - 1) + (tau - p.len + W - 1)) * D + c, nv);
+#pragma unroll
+            for (int j = 0; j < V; ++j) out[j] += r.get(j);
+          }
+        }
+        Raw<T, V> r;
+        r.pack(out);
+        T* to = !EDGE || tau >= 0 ? row_at<T>(g.dx, p, tau)
+                                  : static_cast<T*>(g.dstate) + ((int64_t)p.seq * (W - 1) + tau + W - 1) * D;
+        if (nv > 0) r.store_n(&at_lane(to, c), nv);
+      }
+    };
 #pragma unroll
     for (int i = 0; i < B; ++i) {
       nx[i].clear();
       ndy[i].clear();
-      if (i < total && p.t0 + i < p.len && nv > 0) {
-        nx[i].load_n(row_at<const T>(a.x, p, p.t0 + i) + c, nv);
-        ndy[i].load_n(row_at<const T>(g.dy, p, p.t0 + i) + c, nv);
-      }
     }
-    for (int i0 = 0; i0 < total; i0 += B) {
+    if (inside > 0) fetch(0);
+    for (int u0 = 0; u0 < total; u0 += B) {
       Raw<T, V> rx[B], rdy[B];
 #pragma unroll
       for (int i = 0; i < B; ++i) {
         rx[i] = nx[i];
         rdy[i] = ndy[i];
-        nx[i].clear();
-        ndy[i].clear();
-        const int u = i0 + B + i;
-        if (u < total && p.t0 + u < p.len && nv > 0) {
-          nx[i].load_n(row_at<const T>(a.x, p, p.t0 + u) + c, nv);
-          ndy[i].load_n(row_at<const T>(g.dy, p, p.t0 + u) + c, nv);
-        }
       }
-#pragma unroll
-      for (int i = 0; i < B; ++i) {
-        const int u = i0 + i;
-        if (u < total) {
-          const bool in = p.t0 + u < p.len;       // else: g = 0 past the sequence's end
-          const bool mine = u < n;                // else: dw takes it in the next piece
-          const int tau = p.t0 + u - (W - 1);
-          float out[V];
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            const float x = rx[i].get(j);
-            float s = __builtin_fmaf(w[W - 1][j], x, b[j]);
-#pragma unroll
-            for (int q = 0; q < W - 1; ++q) s = __builtin_fmaf(w[q][j], xw[q][j], s);
-            float gr = rdy[i].get(j);
-            if (a.silu) {
-              const float sg = sigmoid(s);
-              gr *= sg * __builtin_fmaf(s, 1.f - sg, 1.f);
-            }
-            gr = in ? gr : 0.f;
-            const float gm = mine ? gr : 0.f;
-            dw[W][j] += gm;
-            dw[W - 1][j] = __builtin_fmaf(gm, x, dw[W - 1][j]);
-#pragma unroll
-            for (int q = 0; q < W - 1; ++q) dw[q][j] = __builtin_fmaf(gm, xw[q][j], dw[q][j]);
-            // dx[tau] = sum_q w[q] g[tau + (W - 1) - q]
-            float o = w[0][j] * gr;
-#pragma unroll
-            for (int q = 1; q < W; ++q) o = __builtin_fmaf(w[q][j], gw[W - 1 - q][j], o);
-            out[j] = o;
-#pragma unroll
-            for (int q = 0; q < W - 2; ++q) {
-              xw[q][j] = xw[q + 1][j];
-              gw[q][j] = gw[q + 1][j];
-            }
-            xw[W - 2][j] = x;
-            gw[W - 2][j] = gr;
-          }
-          // Before the piece: another piece's token, or the incoming window.
-          if (tau >= p.t0 || (p.t0 == 0 && g.dstate)) {
-            if (g.dstate_out && tau >= p.len - (W - 1) && nv > 0) {
-              Raw<T, V> r;
-              r.load_n(static_cast<const T*>(g.dstate_out) +
-                           ((int64_t)p.seq * (W - 1) + (tau - p.len + W - 1)) * D + c, nv);
-#pragma unroll
-              for (int j = 0; j < V; ++j) out[j] += r.get(j);
-            }
-            Raw<T, V> r;
-            r.pack(out);
-            T* to = tau >= 0 ? row_at<T>(g.dx, p, tau)
-                             : static_cast<T*>(g.dstate) + ((int64_t)p.seq * (W - 1) + tau + W - 1) * D;
-            if (nv > 0) r.store_n(to + c, nv);
-          }
-        }
-      }
+      if (u0 + B < inside) fetch(u0 + B);
+      if (u0 > 0 && u0 + B <= n && (p.t0 + u0 + B <= p.len || !g.dstate_out)) batch(u0, rx, rdy, std::false_type());
+      else batch(u0, rx, rdy, std::true_type());
     }
   }
   // The four waves' sums, in order.
@@ -346,19 +361,34 @@ __global__ __launch_bounds__(256) void conv_grad_kernel(ConvGradArgs k) {
   }
 }
 
+// A piece's filters and windows are read once for all its tokens, so pieces grow from 2^shift tokens while kConvWaves
+// waves are left.  16384 tokens x 4096 channels, bf16: 16 tokens a piece 65 us, 64 tokens (4096 waves) 52 us, 256 tokens
+// 67 us; the gradient with 32 tokens 100 us, with 64 (8192 waves of half as many channels) 92 us.
+constexpr int64_t kConvWaves = 4096;
+int piece_shift(const seq_conv_args_t& a, int shift, int cblocks) {
+  while (shift < 8 && (seq_rows(a.tokens) >> (shift + 1)) * cblocks >= kConvWaves) ++shift;
+  return shift;
+}
+SeqMap grad_map(const seq_conv_args_t& a) {
+  return seq_map(a.tokens, piece_shift(a, 5, (int)((a.channels + 64 * kVec - 1) / (64 * kVec))));
+}
 int cblocks(int64_t channels, int per) { return (int)((channels + per - 1) / per); }
+
+bool whole_blocks(int64_t channels) { return channels % (64 * kVec) == 0; }
 
 template <typename T, int W>
 hipError_t conv_tw(const seq_conv_args_t& a, hipStream_t stream) {
   ConvArgs k;
   k.a = a;
-  k.m = seq_map(a.tokens, kConvShift);
+  k.cblocks = cblocks(a.channels, 64 * kVec);
+  k.m = seq_map(a.tokens, piece_shift(a, 4, k.cblocks));
   k.pieces = (int32_t)seq_pieces(k.m);
-  k.cblocks = cblocks(a.channels, 64 * kVec<T>);
   const bool on_itself = a.state_out != nullptr && a.state_out == a.state;
   k.window = a.state_out != nullptr && !on_itself;
   const int64_t groups = ((int64_t)k.pieces + 3) / 4;
-  hipError_t err = launch_kernel(conv_kernel<T, W>, dim3((unsigned)(groups * k.cblocks)), dim3(256), k, stream);
+  const dim3 grid((unsigned)(groups * k.cblocks));
+  hipError_t err = whole_blocks(a.channels) ? launch_kernel(conv_kernel<T, W, true>, grid, dim3(256), k, stream)
+                                            : launch_kernel(conv_kernel<T, W, false>, grid, dim3(256), k, stream);
   if (err != hipSuccess || !on_itself) return err;
   return launch_kernel(conv_window_kernel<T, W>, dim3((unsigned)(a.tokens.sequences * k.cblocks)), dim3(64), k, stream);
 }
@@ -367,10 +397,10 @@ template <typename T, int W>
 hipError_t conv_step_tw(const seq_conv_args_t& a, hipStream_t stream) {
   ConvArgs k;
   k.a = a;
-  k.m = seq_map(a.tokens, kConvShift);
+  k.m = seq_map(a.tokens, 0);
   k.pieces = 0;
   k.window = 0;
-  k.cblocks = cblocks(a.channels, 256 * 4);
+  k.cblocks = cblocks(a.channels, 256 * kVec);
   return launch_kernel(conv_step_kernel<T, W>, dim3((unsigned)(a.tokens.sequences * k.cblocks)), dim3(256), k, stream);
 }
 
@@ -378,12 +408,14 @@ template <typename T, int W>
 hipError_t conv_grad_tw(const seq_conv_grad_args_t& g, float* ws, hipStream_t stream) {
   ConvGradArgs k;
   k.g = g;
-  k.m = seq_map(g.fwd.tokens, kGradShift);
+  k.m = grad_map(g.fwd);
   k.pieces = (int32_t)seq_pieces(k.m);
-  k.cblocks = cblocks(g.fwd.channels, 64 * 4);
+  k.cblocks = cblocks(g.fwd.channels, 64 * kGradVec);
   k.parts = (int32_t)conv_grad_parts(g);
   k.part = ws;
-  return launch_kernel(conv_grad_kernel<T, W>, dim3((unsigned)(k.parts * k.cblocks)), dim3(256), k, stream);
+  const dim3 grid((unsigned)(k.parts * k.cblocks));
+  return g.fwd.channels % (64 * kGradVec) == 0 ? launch_kernel(conv_grad_kernel<T, W, true>, grid, dim3(256), k, stream)
+                                      : launch_kernel(conv_grad_kernel<T, W, false>, grid, dim3(256), k, stream);
 }
 
 // The dtype and tap count of a call as template arguments.
@@ -419,7 +451,7 @@ hipError_t launch_conv_step(const seq_conv_args_t& a, hipStream_t stream) {
 
 // Workgroups along the pieces, each with a partial of dw: 128 of them give a 4096-channel layer 2048 workgroups.
 int64_t conv_grad_parts(const seq_conv_grad_args_t& g) {
-  const int64_t need = (seq_pieces(seq_map(g.fwd.tokens, kGradShift)) + 3) / 4;
+  const int64_t need = (seq_pieces(grad_map(g.fwd)) + 3) / 4;
   return need < 1 ? 1 : need < 256 ? need : 256;
 }
 
