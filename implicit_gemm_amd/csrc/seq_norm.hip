@@ -259,8 +259,10 @@ hipError_t norm_t(const seq_norm_args_t& a, hipStream_t stream) {
   const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(256);
   if (wave) {
     if (C <= 64 * 8) return launch_kernel(norm_kernel<T, 64, 8, E4M3>, grid, block, a, stream);
-    if (C <= 64 * 16) return launch_kernel(norm_kernel<T, 64, 16, E4M3>, grid, block, a, stream);
-    return launch_kernel(norm_kernel<T, 64, 32, E4M3>, grid, block, a, stream);
+    if constexpr (sizeof(T) == 2) {
+      if (C > 64 * 16) return launch_kernel(norm_kernel<T, 64, 32, E4M3>, grid, block, a, stream);
+    }
+    return launch_kernel(norm_kernel<T, 64, 16, E4M3>, grid, block, a, stream);
   }
   if (C <= 256 * 8) return launch_kernel(norm_kernel<T, 256, 8, E4M3>, grid, block, a, stream);
   if (C <= 256 * 16) return launch_kernel(norm_kernel<T, 256, 16, E4M3>, grid, block, a, stream);
@@ -279,10 +281,14 @@ hipError_t norm_grad_t(const seq_norm_grad_args_t& a, float* ws, hipStream_t str
   const dim3 grid((unsigned)norm_grad_parts(a));
   if (by_wave<T>(C)) {
     if (C <= 64 * 8) return launch_kernel(norm_grad_kernel<T, 64, 8>, grid, dim3(256), k, stream);
-    if (C <= 64 * 16) return launch_kernel(norm_grad_kernel<T, 64, 16>, grid, dim3(256), k, stream);
-    return launch_kernel(norm_grad_kernel<T, 64, 32>, grid, dim3(256), k, stream);
+    if constexpr (sizeof(T) == 2) {
+      if (C > 64 * 16) return launch_kernel(norm_grad_kernel<T, 64, 32>, grid, dim3(256), k, stream);
+    }
+    return launch_kernel(norm_grad_kernel<T, 64, 16>, grid, dim3(256), k, stream);
   }
-  if (C <= 256 * 8) return launch_kernel(norm_grad_kernel<T, 256, 8>, grid, dim3(256), k, stream);
+  if constexpr (sizeof(T) == 4) {
+    if (C <= 256 * 8) return launch_kernel(norm_grad_kernel<T, 256, 8>, grid, dim3(256), k, stream);
+  }
   if (C <= 256 * 16) return launch_kernel(norm_grad_kernel<T, 256, 16>, grid, dim3(256), k, stream);
   if (C <= 256 * 32) return launch_kernel(norm_grad_kernel<T, 256, 32>, grid, dim3(256), k, stream);
   return launch_kernel(norm_grad_kernel<T, 1024, 16>, grid, dim3(1024), k, stream);

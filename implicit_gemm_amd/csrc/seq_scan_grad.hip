@@ -10,11 +10,12 @@
 // Bound by the vector ALU.  A workgroup takes a piece of a sequence and 64 channels, 16 tokens at a time from the last:
 // what a token and channel need (D, D u, do) is computed once by the lane that loads it and passed through LDS; then
 // NG lanes share a channel, four states each, and keep h of the 16 tokens in 64 registers for the reversed sweep.
-// Keeping e^(D A) too would save the second exponential (3 of about 28 instructions a state) but 64 registers more leave
-// one wave a SIMD: 519 us against 341 on 8192 tokens x 2048 channels x 16 states in bf16.  Sums over states are taken
-// inside a group of NG lanes, each of which keeps one of NG tokens' results; sums over channels by exchanging halves of
-// the wave (each step halves the values a lane holds), then over the waves through LDS and over the channel blocks by a
-// fold, all in a fixed order.  Those 8192 tokens take 286 us; the vector ALU is busy 73 % of them.
+// Keeping all of e^(D A) too would save its second evaluation (3 of about 28 instructions a state) but 64 registers more
+// leave one wave a SIMD; kept for the last 12 tokens, the sweep meets its limit of 256 (8192 tokens x 2048 channels x 16
+// states in bf16: none 285 us, 8 tokens 271, 12 tokens 267, 14 tokens 266).  Sums over states are taken inside a group of
+// NG lanes, each of which keeps one of NG tokens' results; sums over channels by exchanging halves of the wave (each
+// step halves the values a lane holds), then over the waves through LDS and over the channel blocks by a
+// fold, all in a fixed order.  The vector ALU is busy 73 % of those 267 us.
 #include "seq_scan.h"
 
 namespace cw {
@@ -122,6 +123,7 @@ __device__ __forceinline__ seq_view_t view_of(const __attribute__((address_space
 template <typename T, int NG, bool FULL>
 __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
   constexpr int NP = 4 * NG, kWaveCh = 64 / NG, V = 16 / NG, kShare = 8 / NG;
+  constexpr int kHeld = NG == 2 ? 0 : sizeof(T) == 2 ? 12 : 8;   // of e^(D A): as many tokens as fit 256 registers
   constexpr bool kEarly = V * sizeof(T) < 32;   // the next tile's inputs fit the registers
   __shared__ GradTile<NG> m;
   const seq_scan_args_t& a = k.s.a;
@@ -272,7 +274,7 @@ __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
       __syncthreads();
       if (kEarly && j > 0) fetch(j - 1);
 
-      float h[kTile][4];
+      float h[kTile][4], held[kHeld > 0 ? kHeld : 1][4];
       float keep = 0.f;
 #pragma unroll
       for (int q = 0; q < kTile; ++q) {
@@ -284,6 +286,7 @@ __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float e = __builtin_amdgcn_exp2f(dt * A2[i]);
+          if (q >= kTile - kHeld) held[q >= kTile - kHeld ? q - (kTile - kHeld) : 0][i] = e;
           h[q][i] = __builtin_fmaf(e, q ? h[q ? q - 1 : 0][i] : hs[i], x * B4[i]);
           o = __builtin_fmaf(h[q][i], C4[i], o);
         }
@@ -312,7 +315,7 @@ __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
           v[i] = gi * x;                // lanes without a channel: x and do are zero
           v[4 + i] = dov * h[q][i];
           gb = __builtin_fmaf(gi, B4[i], gb);
-          c[i] = __builtin_amdgcn_exp2f(dt * A2[i]) * gi;
+          c[i] = (q >= kTile - kHeld ? held[q >= kTile - kHeld ? q - (kTile - kHeld) : 0][i] : __builtin_amdgcn_exp2f(dt * A2[i])) * gi;
           const float r = c[i] * (q ? h[q ? q - 1 : 0][i] : hs[i]);
           da = __builtin_fmaf(r, A2[i], da);
           dA[i] = __builtin_fmaf(r, dt, dA[i]);
@@ -423,10 +426,10 @@ hipError_t grad_any(const GradArgs& k, hipStream_t stream) {
 #undef CALL
 }
 
-// Workgroups along the pieces: one a piece, but no more than give about 4096 workgroups (each has a partial of dA).
+// Workgroups along the pieces: one a piece, but no more than give about 2048 workgroups (each has a partial of dA).
 int32_t grad_parts(const seq_scan_args_t& a, int64_t pieces) {
   const int64_t blocks = (int64_t)scan_dblocks(a) * a.groups;
-  int64_t most = 4096 / blocks;
+  int64_t most = 2048 / blocks;
   if (most < 16) most = 16;
   return (int32_t)(pieces < most ? pieces : most);
 }
