@@ -10,12 +10,12 @@
 // Bound by the vector ALU.  A workgroup takes a piece of a sequence and 64 channels, 16 tokens at a time from the last:
 // what a token and channel need (D, D u, do) is computed once by the lane that loads it and passed through LDS; then
 // NG lanes share a channel, four states each, and keep h of the 16 tokens in 64 registers for the reversed sweep.
-// Keeping all of e^(D A) too would save its second evaluation (3 of about 28 instructions a state) but 64 registers more
-// leave one wave a SIMD; kept for the last 12 tokens, the sweep meets its limit of 256 (8192 tokens x 2048 channels x 16
-// states in bf16: none 285 us, 8 tokens 271, 12 tokens 267, 14 tokens 266).  Sums over states are taken inside a group of
-// NG lanes, each of which keeps one of NG tokens' results; sums over channels by exchanging halves of the wave (each
-// step halves the values a lane holds), then over the waves through LDS and over the channel blocks by a
-// fold, all in a fixed order.  The vector ALU is busy 73 % of those 267 us.
+// Keeping all of e^(D A) too would save its second evaluation (3 of about 26 instructions a state) but 64 registers more
+// leave one wave a SIMD.  With two, what one token reads of LDS is read a token ahead, and the 256 registers then hold
+// e^(D A) of the last 8 tokens (8192 tokens x 2048 channels x 16 states in bf16: kept for no token 280 us, for 8 257,
+// for 12 but read where needed 272).  Sums over states are taken inside a group of NG lanes, each of which keeps one of
+// NG tokens' results; sums over channels by exchanging halves of the wave (each step halves the values a lane holds),
+// then over the waves through LDS and over the channel blocks by a fold, all in a fixed order.
 #include "seq_scan.h"
 
 namespace cw {
@@ -81,6 +81,9 @@ __device__ __forceinline__ float tokens_reduce(const float (&r)[8 / NG]) {
   }
 }
 
+// The tensors whose rows a tile reads.
+enum { kU, kDelta, kDy, kZ, kB, kC, kInputs };
+
 // What the lanes of a workgroup pass each other of one tile.
 template <int NG>
 struct GradTile {
@@ -89,23 +92,12 @@ struct GradTile {
   alignas(16) float o[kTile][64 + 64 / NG], gb[kTile][64 + 64 / NG], da[kTile][64 + 64 / NG];
   alignas(16) float B[kTile][4 * NG], C[kTile][4 * NG];
   float bias[64], skip[64];
+  // Address of a piece's first row (the block's channels, the group's states) and bytes between two rows, per input: in
+  // LDS, as six 64-bit products a tile would be a third of all instructions and six addresses too many scalar registers.
+  uint64_t base[kInputs];
+  uint32_t step[kInputs];
   float bc[NG][kTile][8 * NG];                                     // each wave's sums over its channels: dB, dC
 };
-
-// Rows of a tensor from the first token of a piece on: an address that is the same in the whole wave and the distance of
-// two rows, both in bytes.  A lane's own part of an address is a 32-bit offset.
-struct Rows {
-  const char* at;
-  uint32_t row;
-};
-template <typename T>
-__device__ __forceinline__ Rows rows_from(const seq_view_t& v, const Piece& p, int64_t offset) {
-  return Rows{reinterpret_cast<const char*>(row_at<const T>(v, p, p.t0) + offset), (uint32_t)v.row * (uint32_t)sizeof(T)};
-}
-template <typename T>
-__device__ __forceinline__ const T* lane_of(const Rows& r, int tile, uint32_t offset) {
-  return reinterpret_cast<const T*>(r.at + (int64_t)tile * kTile * r.row + offset);
-}
 
 // The kernel's arguments, to be loaded where they are used: held through the sweeps they need more scalar registers than
 // there are, and the compiler would keep them in vector lanes, an instruction for each use.
@@ -115,16 +107,38 @@ __device__ __forceinline__ ArgsPtr args_again() {
   asm volatile("" : "+s"(p));
   return p;
 }
-__device__ __forceinline__ seq_view_t view_of(const __attribute__((address_space(4))) seq_view_t& v) {
-  return seq_view_t{v.ptr, v.batch, v.row};
+
+// V floats of a row of LDS, in as few accesses as there are.
+template <int V>
+__device__ __forceinline__ void put_row(float* to, const float (&v)[V]) {
+  if constexpr (V == 2) {
+    *reinterpret_cast<float2*>(to) = float2{v[0], v[1]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(to + i) = float4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+  }
 }
+
+// What a sweep reads of one token: D, D u, do of the lane's channel, B and C of its states.
+template <int NG>
+struct Token {
+  float dt, x, dov;
+  float4 B, C;
+  __device__ __forceinline__ void read(const GradTile<NG>& m, int q, int ch, int ng) {
+    dt = m.dt[q][ch];
+    x = m.x[q][ch];
+    dov = m.dov[q][ch];
+    B = reinterpret_cast<const float4*>(&m.B[q][0])[ng];
+    C = reinterpret_cast<const float4*>(&m.C[q][0])[ng];
+  }
+};
 
 // FULL: every lane has a channel and four states (channels of a group a multiple of 64, states of 4 NG).
 template <typename T, int NG, bool FULL>
 __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
   constexpr int NP = 4 * NG, kWaveCh = 64 / NG, V = 16 / NG, kShare = 8 / NG;
-  constexpr int kHeld = NG == 2 ? 0 : sizeof(T) == 2 ? 12 : 8;   // of e^(D A): as many tokens as fit 256 registers
-  constexpr bool kEarly = V * sizeof(T) < 32;   // the next tile's inputs fit the registers
+  constexpr int kHeld = NG == 2 ? 0 : sizeof(T) == 2 ? 8 : 4;   // tokens whose e^(D A) is kept, as registers allow
+  constexpr bool kEarly = NG > 2;   // the next tile's inputs fit the registers (eight channels a lane do not)
   __shared__ GradTile<NG> m;
   const seq_scan_args_t& a = k.s.a;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -183,6 +197,13 @@ __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
       }
       continue;
     }
+    if (tid < kInputs) {
+      const seq_view_t& v = tid == kU ? a.u : tid == kDelta ? a.delta : tid == kDy ? k.s.dy : tid == kZ ? a.z : tid == kB ? a.B : a.C;
+      const int64_t from = tid == kB ? g * a.B_group : tid == kC ? g * a.C_group : d0;
+      m.base[tid] = reinterpret_cast<uint64_t>(row_at<const T>(v, p, p.t0) + from);
+      m.step[tid] = (uint32_t)v.row * (uint32_t)sizeof(T);
+    }
+    __syncthreads();
     const int64_t tile0 = (k.s.m.offsets ? (p.first >> kSaveShift) + p.seq
                                          : (int64_t)p.seq * (((k.s.m.rows - 1) >> kSaveShift) + 1)) +
                           (p.t0 >> kSaveShift);
@@ -205,34 +226,31 @@ __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
     dl.clear();
     z.clear();
     dy.clear();
+    // Row `r` of tile j of an input, from element `e` on.
+    auto row_of = [&](int input, int j, int r, int e) {
+      return reinterpret_cast<const T*>(m.base[input] + (uint64_t)(uint32_t)(j * kTile + r) * m.step[input] +
+                                        (uint32_t)e * (uint32_t)sizeof(T));
+    };
     // This lane's token and channels of tile j; rows past the end repeat the last one.
     auto fetch_items = [&](int j, Raw<T, V>& u, Raw<T, V>& dl, Raw<T, V>& z, Raw<T, V>& dy) {
-      const uint32_t r = (uint32_t)min(it, min(kTile, p.end - p.t0 - j * kTile) - 1), off = (uint32_t)ic * sizeof(T);
-      const ArgsPtr q = args_again();
+      const int r = min(it, min(kTile, p.end - p.t0 - j * kTile) - 1);
       if (FULL || iv > 0) {
         const int nvec = FULL ? V : iv;
-        const Rows ru = rows_from<T>(view_of(q->s.a.u), p, d0), rdl = rows_from<T>(view_of(q->s.a.delta), p, d0);
-        u.load_n(lane_of<T>(ru, j, r * ru.row + off), nvec);
-        dl.load_n(lane_of<T>(rdl, j, r * rdl.row + off), nvec);
-        const Rows rdy = rows_from<T>(view_of(q->s.dy), p, d0);
-        dy.load_n(lane_of<T>(rdy, j, r * rdy.row + off), nvec);
-        if (gated) {
-          const Rows rz = rows_from<T>(view_of(q->s.a.z), p, d0);
-          z.load_n(lane_of<T>(rz, j, r * rz.row + off), nvec);
-        }
+        u.load_n(row_of(kU, j, r, ic), nvec);
+        dl.load_n(row_of(kDelta, j, r, ic), nvec);
+        dy.load_n(row_of(kDy, j, r, ic), nvec);
+        if (gated) z.load_n(row_of(kZ, j, r, ic), nvec);
       }
     };
     // The inputs of tile j.
     auto fetch = [&](int j) {
       fetch_items(j, u, dl, z, dy);
-      const uint32_t e = (uint32_t)min(eT, min(kTile, p.end - p.t0 - j * kTile) - 1);
-      const ArgsPtr q = args_again();
+      const int e = min(eT, min(kTile, p.end - p.t0 - j * kTile) - 1);
       if (FULL || eN < N) {
-        const Rows rB = rows_from<T>(view_of(q->s.a.B), p, g * q->s.a.B_group);
-        const Rows rC = rows_from<T>(view_of(q->s.a.C), p, g * q->s.a.C_group);
-        eB = *lane_of<T>(rB, j, e * rB.row + (uint32_t)eN * (uint32_t)sizeof(T));
-        eC = *lane_of<T>(rC, j, e * rC.row + (uint32_t)eN * (uint32_t)sizeof(T));
+        eB = *row_of(kB, j, e, eN);
+        eC = *row_of(kC, j, e, eN);
       }
+      const ArgsPtr q = args_again();
       const float* const from = q->s.a.save + (tile0 + j) * D * N + d0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) h0[i] = FULL || i < nv ? from[state_off + i * D] : 0.f;
@@ -260,12 +278,16 @@ __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
 #pragma unroll
         for (int q = 0; q < V; ++q) pdo[q] *= cz.get(q) * sigmoid(cz.get(q));
       }
+      float px[V];
 #pragma unroll
       for (int q = 0; q < V; ++q) {
-        m.dt[it][ic + q] = valid ? pdt[q] : 0.f;
-        m.x[it][ic + q] = valid ? pdt[q] * cu.get(q) : 0.f;
-        m.dov[it][ic + q] = valid ? pdo[q] : 0.f;
+        pdt[q] = valid ? pdt[q] : 0.f;
+        px[q] = valid ? pdt[q] * cu.get(q) : 0.f;
+        pdo[q] = valid ? pdo[q] : 0.f;
       }
+      put_row(&m.dt[it][ic], pdt);
+      put_row(&m.x[it][ic], px);
+      put_row(&m.dov[it][ic], pdo);
       m.B[eT][eN] = to_f32(eB);
       m.C[eT][eN] = to_f32(eC);
       float hs[4];
@@ -276,12 +298,14 @@ __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
 
       float h[kTile][4], held[kHeld > 0 ? kHeld : 1][4];
       float keep = 0.f;
+      Token<NG> ahead;
+      ahead.read(m, 0, ch, ng);
 #pragma unroll
       for (int q = 0; q < kTile; ++q) {
-        const float dt = m.dt[q][ch], x = m.x[q][ch];
-        const float4 Bv = *reinterpret_cast<const float4*>(&m.B[q][n0]);
-        const float4 Cv = *reinterpret_cast<const float4*>(&m.C[q][n0]);
-        const float B4[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, C4[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
+        const Token<NG> now = ahead;
+        if (q + 1 < kTile) ahead.read(m, q + 1, ch, ng);
+        const float dt = now.dt, x = now.x;
+        const float B4[4] = {now.B.x, now.B.y, now.B.z, now.B.w}, C4[4] = {now.C.x, now.C.y, now.C.z, now.C.w};
         float o = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -292,22 +316,22 @@ __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
         }
         o = lanes_reduce<AddOp>(o, NG);
         keep = ng == q % NG ? o : keep;
-        if (q % NG == NG - 1) {
-          m.o[q - (NG - 1) + ng][ch] = keep;
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        if (q % NG == NG - 1) m.o[q - (NG - 1) + ng][ch] = keep;
+        __builtin_amdgcn_sched_barrier(0);
       }
       // Read B, C, D and D u again: kept from the sweep above they would take 160 registers more.  The compiler is
       // not to know that these are the same indices.
       int ch2 = ch, ng2 = ng;
       asm volatile("" : "+v"(ch2), "+v"(ng2));
       float keep_gb = 0.f, keep_da = 0.f, sums[kShare];
+      Token<NG> before;
+      before.read(m, kTile - 1, ch2, ng2);
 #pragma unroll
       for (int q = kTile - 1; q >= 0; --q) {
-        const float dt = m.dt[q][ch2], x = m.x[q][ch2], dov = m.dov[q][ch2];
-        const float4 Bv = reinterpret_cast<const float4*>(&m.B[q][0])[ng2];
-        const float4 Cv = reinterpret_cast<const float4*>(&m.C[q][0])[ng2];
-        const float B4[4] = {Bv.x, Bv.y, Bv.z, Bv.w}, C4[4] = {Cv.x, Cv.y, Cv.z, Cv.w};
+        const Token<NG> now = before;
+        if (q > 0) before.read(m, q - 1, ch2, ng2);
+        const float dt = now.dt, x = now.x, dov = now.dov;
+        const float B4[4] = {now.B.x, now.B.y, now.B.z, now.B.w}, C4[4] = {now.C.x, now.C.y, now.C.z, now.C.w};
         float gb = 0.f, da = 0.f, v[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -315,7 +339,9 @@ __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
           v[i] = gi * x;                // lanes without a channel: x and do are zero
           v[4 + i] = dov * h[q][i];
           gb = __builtin_fmaf(gi, B4[i], gb);
-          c[i] = (q >= kTile - kHeld ? held[q >= kTile - kHeld ? q - (kTile - kHeld) : 0][i] : __builtin_amdgcn_exp2f(dt * A2[i])) * gi;
+          const float e = q >= kTile - kHeld ? held[q >= kTile - kHeld ? q - (kTile - kHeld) : 0][i]
+                                             : __builtin_amdgcn_exp2f(dt * A2[i]);
+          c[i] = e * gi;
           const float r = c[i] * (q ? h[q ? q - 1 : 0][i] : hs[i]);
           da = __builtin_fmaf(r, A2[i], da);
           dA[i] = __builtin_fmaf(r, dt, dA[i]);
@@ -333,7 +359,7 @@ __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
           const int to = NG == 8 ? 0 : NG == 4 ? (lane >> 2) & 1 : ((lane >> 2) & 1) + (lane & 2);
           m.bc[wave][q + to][(lane >> 5) * NP + n0 + ((lane >> 3) & 3)] = tokens_reduce<NG>(sums);
         }
-        if (q % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
       }
       __syncthreads();
       if constexpr (NG == 2) fetch_items(j, cu, cdl, cz, cdy);
