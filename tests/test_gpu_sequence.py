@@ -506,3 +506,82 @@ def test_captured_into_a_graph(iga):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), i
         assert torch.equal(pool, p) and torch.equal(states, s)
+
+
+# -------------------------------------------------------------------------------------------------- the whole layer
+
+@pytest.fixture(scope="module")
+def layer_module():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "selective_layer.py")
+    spec = importlib.util.spec_from_file_location("selective_layer", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_layer_by_tokens_matches_prompts(layer_module, dtype):
+    """Four roundings to the element type lie between the layer's input and its output, on both sides, and the matrix
+    products between them sum in other orders: sixteen half steps of the largest output cover them."""
+    layer = layer_module.Layer(96, dtype=DT[dtype], seed=3)
+    off = layer_module.steps_against_prompt(layer, [130, 5, 33, 17])
+    assert off <= max(16 * ref.half_step(DT[dtype]), 1e-5)
+
+
+def test_layer_gradient_against_difference(layer_module):
+    """Central differences of a float32 loss: the step's square and the losses' rounding (2^-24 of their terms over the
+    step) leave about a thousandth."""
+    slope, difference = layer_module.gradient_against_difference()
+    assert abs(slope - difference) <= 1e-2 * abs(difference)
+
+
+# ------------------------------------------------------------------------------------------------ past 32-bit offsets
+
+@pytest.mark.slow
+def test_tensors_past_four_gigabytes(iga):
+    """Rows whose byte offsets (and element offsets) pass 2^32: the end of a long sequence against the same tokens alone,
+    from the carried window and state."""
+    T, D, N, tail = 540_000, 4096, 4, 96
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def big():
+        return torch.randn(1, T, D, generator=g, device="cuda", dtype=torch.bfloat16)
+
+    x, w, b = big(), torch.randn(D, 4, device="cuda"), torch.randn(D, device="cuda")
+    assert x.numel() > 1 << 31 and x.numel() * 2 > 1 << 32
+    end = slice(T - tail, T)
+    y, h, r = iga.rms_norm(x, torch.ones(D, device="cuda"), residual=x)
+    y2, h2, r2 = iga.rms_norm(x[:, end], torch.ones(D, device="cuda"), residual=x[:, end])
+    assert torch.equal(y[:, end], y2) and torch.equal(h[:, end], h2)
+    dx, _ = iga.rms_norm_grad(y, h, torch.ones(D, device="cuda"), r)
+    dx2, _ = iga.rms_norm_grad(y2, h2, torch.ones(D, device="cuda"), r2)
+    assert torch.equal(dx[:, end], dx2)
+    del y, h, dx
+    log("past 4 GiB: norm done")
+    window = x[:, T - tail - 3:T - tail].contiguous()
+    u, last = iga.causal_conv(x, w, b, silu=True)
+    u2, last2 = iga.causal_conv(x[:, end], w, b, silu=True, state=window)
+    assert torch.equal(u[:, end], u2) and torch.equal(last, last2)
+    dx = iga.causal_conv_grad(x, x, w, b, silu=True)[0]
+    dx2 = iga.causal_conv_grad(x[:, end], x[:, end], w, b, silu=True, state=window)[0]
+    assert torch.equal(dx[:, end], dx2)
+    del dx, u
+    log("past 4 GiB: convolution done")
+    A = -torch.arange(1, N + 1, device="cuda").float().repeat(D, 1)
+    B = torch.randn(1, T, 1, N, generator=g, device="cuda", dtype=torch.bfloat16)
+    bias = torch.full((D,), -3.0, device="cuda")
+    kw = dict(delta_bias=bias, softplus=True)
+    y, last, saved = iga.selective_scan(x, x, A, B, B, save=True, **kw)
+    _, before, _ = iga.selective_scan(x[:, :T - tail], x[:, :T - tail], A, B[:, :T - tail], B[:, :T - tail], **kw)
+    y2, last2, saved2 = iga.selective_scan(x[:, end], x[:, end], A, B[:, end], B[:, end], state=before, save=True, **kw)
+    close(y[:, end], y2.double(), torch.bfloat16, 16 + 12 * tail, "y")     # two roundings of one value: within two half steps
+    close(last, last2.double(), torch.float32, 16 + 12 * tail, "state")
+    del y
+    full = iga.selective_scan_grad(x, x, x, A, B, B, saved, **kw)
+    part = iga.selective_scan_grad(x[:, end], x[:, end], x[:, end], A, B[:, end], B[:, end], saved2, state=before, **kw)
+    for name in ("du", "ddelta", "dB", "dC"):
+        a, b2 = getattr(full, name)[:, end].double(), getattr(part, name).double()
+        assert (a - b2).abs().max() <= 2.0 ** -7 * b2.abs().max(), name   # both rounded to bf16: at most one step apart
+    log("past 4 GiB: scan done")
