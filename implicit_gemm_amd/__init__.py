@@ -6,6 +6,9 @@ through ctypes.  PyTorch is used for device memory and streams.  There is no
 fallback: if the library is missing or a call fails, an exception is raised.
 
     dw = wgrad(x, dy, R=3, S=3, pad=1)          # x [N,H,W,C], dy [N,Ho,Wo,K] -> dw [K,R,S,C/groups] fp32
+
+The operators of a sequence model's layer (rms_norm, causal_conv, selective_scan and their gradients and single-token
+forms) are in implicit_gemm_amd.sequence and are names of this module too.
 """
 from __future__ import annotations
 

@@ -2,11 +2,14 @@
 //
 //   D = softplus(delta + bias),  h[t] = e^(D A) h[t - 1] + D u B[t],  y = (sum_n h C[t] + skip u) z sigmoid(z)
 //
-// Bound by the vector ALU: every (token, channel, state) costs one exponential (a quarter-rate instruction) and four
-// multiply-adds, 16 states to the 8 bytes that a token and channel move.  A lane owns one channel with all its states
-// in registers, so the sum over states stays in the lane; a wave owns 64 channels and one piece of a sequence, with
-// B and C of its tokens broadcast from LDS in fp32.  Channels alone give a long prompt too few waves, so its tokens
-// are split as well (seq_scan.h).
+// Bound by the vector ALU: every (token, channel, state) costs one exponential (8 cycles a wave, twice an instruction)
+// and four multiply-adds, 16 states to the 8 bytes that a token and channel move.  A lane owns one channel with all its
+// states in registers, so the sum over states stays in the lane; a wave owns 64 channels and one piece of a sequence,
+// with B and C of its tokens broadcast from LDS in fp32.  Channels alone give a long prompt too few waves, so its tokens
+// are split as well (seq_scan.h).  8192 tokens x 2048 channels x 16 states in bf16: aggregates 60 us, their join 10,
+// outputs 83; the vector ALU is busy 75 % and 71 % of the first and the last (the rest is the end of each launch, when
+// the older waves of a SIMD have finished).  The rank-1 update h <- e h + x B and the sum h C on the matrix pipe
+// (v_mfma_f32_4x4x1) were slower, 75 and 120 us: its products take issue slots and their results come late.
 #include "seq_scan.h"
 
 namespace cw {
@@ -246,8 +249,9 @@ __global__ __launch_bounds__(64 * kScanGroup) void scan_carry_kernel(ScanArgs k)
 
 // The carry into every piece of a sequence, in place of the pieces' aggregates; a lane owns one channel and state.
 // WAVES waves take 16 consecutive pieces each, all their aggregates in registers after one wait for memory; what the
-// waves before pass on comes through LDS.  Four waves where a sequence has many pieces, one where it has few: twelve
-// sequences of up to 29 pieces, 1536 channels x 16 states, take 17 us with four and 12 with one.
+// waves before pass on comes through LDS.  Four waves for the shortest wait, one where sequences have few pieces and the
+// workgroups fill the GPU more than once: 12 sequences of up to 29 pieces, 1536 channels x 16 states (4608 workgroups),
+// take 17 us with four and 12 with one; 3 sequences of 33 pieces, 387 x 11 (231 workgroups), 4.5 and 6.8.
 constexpr int kJoinEach = 16;
 template <bool BACK, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void scan_join_kernel(ScanArgs k) {
@@ -440,8 +444,9 @@ int64_t scan_ws_floats(const seq_scan_args_t& a) {
 hipError_t launch_scan_carry(const ScanArgs& k, bool backward, hipStream_t stream) {
   const hipError_t err = carry_any(k, backward, stream);
   if (err != hipSuccess) return err;
-  const dim3 grid((unsigned)((k.a.channels + 63) / 64 * k.a.states * k.a.tokens.sequences));
-  const bool few = (scan_longest(k.a) >> k.m.shift) <= 2 * kJoinEach;
+  const int64_t groups = (k.a.channels + 63) / 64 * k.a.states * k.a.tokens.sequences;
+  const dim3 grid((unsigned)groups);
+  const bool few = (scan_longest(k.a) >> k.m.shift) <= 2 * kJoinEach && groups > 2048;
   if (backward)
     return few ? launch_kernel(scan_join_kernel<true, 1>, grid, dim3(64), k, stream)
                : launch_kernel(scan_join_kernel<true, 4>, grid, dim3(256), k, stream);
