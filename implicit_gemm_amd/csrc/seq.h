@@ -28,7 +28,7 @@ inline int64_t seq_pieces(const SeqMap& m) {
 }
 inline int64_t seq_rows(const seq_tokens_t& t) { return t.offsets ? t.rows : t.sequences * t.rows; }
 
-// out[e] = sum over p of part[p * stride + e] for e < E, in a fixed order; `rounded` type per dtype (CONV_WGRAD_F32 ..).
+// out[e] = sum over p of part[p * stride + e] for e < E, in a fixed order, rounded to dtype (CONV_WGRAD_F32 ..).
 struct FoldPart {
   const float* part;
   int64_t stride;
@@ -42,7 +42,6 @@ struct FoldList {
   FoldPart f[5];
   int32_t n;
 };
-int64_t fold_blocks(const FoldPart& f);
 hipError_t launch_seq_fold(const FoldList& list, hipStream_t stream);
 
 hipError_t launch_norm(const seq_norm_args_t& a, bool e4m3, hipStream_t stream);

@@ -17,13 +17,6 @@ __device__ __forceinline__ void from_f32(float v, float& out) { out = v; }
 __device__ __forceinline__ void from_f32(float v, Bf16& out) { out.bits = __builtin_bit_cast(uint16_t, (__bf16)v); }
 __device__ __forceinline__ void from_f32(float v, F16& out) { out.v = (_Float16)v; }
 
-template <typename T>
-__device__ __forceinline__ float rounded(float v) {
-  T t;
-  from_f32(v, t);
-  return to_f32(t);
-}
-
 // V consecutive elements as they lie in memory.  The copy claims the element's alignment only: gfx950 loads and stores
 // up to 16 bytes at any element-aligned global address in one instruction, so odd strides need no form of their own.
 // They are held as 32-bit words (two 16-bit elements in one register) until get() widens one.

@@ -196,7 +196,12 @@ def _code(t):
 
 
 def _empty(shape, dtype, like):
-    return torch.empty(shape, dtype=dtype, device=like.device)
+    return like.new_empty(shape, dtype=dtype)
+
+
+def _same(x):
+    """A dense tensor of the shape and type of x."""
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def _sequences(x, offsets, name):
@@ -213,27 +218,29 @@ def _sequences(x, offsets, name):
     return offsets.shape[0] - 1, shape[0]
 
 
+def _place(t, name, P, each, dtype, index):
+    """(pointer, stride between states) of a pool of P dense states."""
+    if t.shape != (P,) + each or t.dtype is not dtype or t.get_device() != index:
+        _refuse(t, name, (P,) + each, dtype, index)
+    outer, rows, one = t.stride()
+    if (rows != each[1] and each[0] > 1) or (one != 1 and each[1] > 1):
+        raise ValueError("each state of %s must be contiguous" % name)
+    return t.data_ptr(), outer
+
+
 def _pool(state, state_out, slots, S, each, dtype, index):
     """(slots, pool, state, its stride, state_out, its stride) for the arguments, after the checks of the states."""
     given = state if state is not None else state_out
-    P = S if given is None else given.shape[0] if given.dim() else -1
-    out = []
-    for t, name in ((state, "state"), (state_out, "state_out")):
-        if t is None:
-            out += (0, 0)
-            continue
-        if t is state and out and name == "state_out":
-            out += out
-            continue
-        strides = _like(t, name, (P,) + each, dtype, index)
-        if strides[1] != each[1] and each[0] > 1:
-            raise ValueError("each state of %s must be contiguous" % name)
-        out += (t.data_ptr(), strides[0])
-    if slots is None and P != S:
-        raise ValueError("%d states for %d sequences: slots must say which" % (P, S))
+    P = S if given is None else given.shape[0] if given.dim() else 0
     if P < 1:
         raise ValueError("there must be at least one sequence and one state")
-    return (_dense(slots, "slots", (S,), torch.int32, index), P), out
+    at = (0, 0) if state is None else _place(state, "state", P, each, dtype, index)
+    to = at if state_out is state else (0, 0) if state_out is None else _place(state_out, "state_out", P, each, dtype, index)
+    if slots is None:
+        if P != S:
+            raise ValueError("%d states for %d sequences: slots must say which" % (P, S))
+        return 0, P, at + to
+    return _dense(slots, "slots", (S,), torch.int32, index), P, at + to
 
 
 def _default_out(state_out, slots, state, S, each, dtype, like):
@@ -267,7 +274,7 @@ def _residual(residual, x, index):
         return 0, 0, 0, x
     if residual.shape != x.shape or residual.dtype is not x.dtype or residual.get_device() != index:
         _refuse(residual, "residual", x.shape, x.dtype, index)
-    h = _empty(x.shape, x.dtype, x)
+    h = _same(x)
     return residual.data_ptr(), _rows(residual, "residual")[1], h.data_ptr(), h
 
 
@@ -278,10 +285,10 @@ def rms_norm(x, w, residual=None, eps=1e-5, stream=None):
     on = _here(x, stream)
     if on is None:
         return _there(x, stream, rms_norm, x, w, residual, eps)
-    shape, dtype, index, code = x.shape, x.dtype, x.get_device(), _code(x)
+    shape, index, code = x.shape, x.get_device(), _code(x)
     rows, x_row = _rows(x, "x")
     res, res_row, h_ptr, h = _residual(residual, x, index)
-    y, r = _empty(shape, dtype, x), _empty(shape[:-1], _f32, x)
+    y, r = _same(x), _empty(shape[:-1], _f32, x)
     status = _lib().seq_rms_norm(
         _NORM(rows, shape[-1], code, 0, eps, 0, x.data_ptr(), x_row, res, res_row, _dense(w, "w", shape[-1:], _f32, index),
               y.data_ptr(), h_ptr, r.data_ptr(), 0), on)
@@ -327,7 +334,7 @@ def rms_norm_grad(dy, h, w, r, dh=None, stream=None):
     _like(dy, "dy", shape, dtype, index)
     if dh is not None:
         _like(dh, "dh", shape, dtype, index)
-    dx, dw = _empty(shape, dtype, h), _empty((C,), _f32, h)
+    dx, dw = _same(h), _empty((C,), _f32, h)
     n = _norm_grad_space(rows, C, code)
     ws = _empty(n, torch.uint8, h)
     status = _lib().seq_rms_norm_grad(
@@ -348,8 +355,8 @@ def _conv_args(x, xs, S, L, w, b, silu, offsets, slots, state, state_out, index)
     if w.dim() != 2 or w.shape[0] != D:
         raise ValueError("w must be [%d, taps], got shape %s" % (D, tuple(w.shape)))
     W = w.shape[1]
-    pool, states = _pool(state, state_out, slots, S, (W - 1, D), x.dtype, index)
-    return W, (S, L, _dense(offsets, "offsets", (S + 1,), torch.int32, index), *pool, D, W, _code(x), bool(silu), 0,
+    slot_ptr, P, states = _pool(state, state_out, slots, S, (W - 1, D), x.dtype, index)
+    return W, (S, L, _dense(offsets, "offsets", (S + 1,), torch.int32, index), slot_ptr, P, D, W, _code(x), bool(silu), 0,
                x.data_ptr(), *xs, _dense(w, "w", (D, W), _f32, index), _dense(b, "b", (D,), _f32, index), *states)
 
 
@@ -374,7 +381,7 @@ def causal_conv(x, w, b=None, silu=False, offsets=None, slots=None, state=None, 
     shape = x.shape
     state_out = _default_out(state_out, slots, state, S, (w.shape[-1] - 1, shape[-1]), x.dtype, x)
     _, args = _conv_args(x, _strides(x, "x", offsets, index), S, L, w, b, silu, offsets, slots, state, state_out, index)
-    y = _empty(shape, x.dtype, x)
+    y = _same(x)
     D = shape[-1]
     status = _lib().seq_causal_conv(_CONV(*args, y.data_ptr(), L * D if offsets is None else 0, D), on)
     if status:
@@ -394,7 +401,7 @@ def causal_conv_step(x, state, w, b=None, silu=False, slots=None, state_out=None
     batch = _like(x, "x", shape, x.dtype, index)[0]
     _, args = _conv_args(x, (batch, 0), shape[0], 1, w, b, silu, None, slots, state,
                          state if state_out is None else state_out, index)
-    y = _empty(shape, x.dtype, x)
+    y = _same(x)
     status = _lib().seq_causal_conv_step(_CONV(*args, y.data_ptr(), shape[1], 0), on)
     if status:
         raise ConvWgradError(status, "causal_conv_step")
@@ -419,7 +426,7 @@ def causal_conv_grad(dy, x, w, b=None, silu=False, offsets=None, slots=None, sta
     W, args = _conv_args(x, _strides(x, "x", offsets, index), S, L, w, b, silu, offsets, slots, state, None, index)
     D = shape[-1]
     dys = _like(dy, "dy", shape, dtype, index)
-    dx, dw = _empty(shape, dtype, x), _empty((D, W), _f32, x)
+    dx, dw = _same(x), _empty((D, W), _f32, x)
     db = _empty((D,), _f32, x) if b is not None else None
     dstate = _empty((S, W - 1, D), dtype, x) if state is not None else None
     n = _conv_grad_space(S, L, offsets is not None, D, W, args[7])
@@ -452,7 +459,7 @@ def _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, slots,
     Bs, Cs = _like(B, "B", wide, dtype, index), _like(C, "C", wide, dtype, index)
     zs = _like(z, "z", shape, dtype, index) if z is not None else us
     z_ptr = z.data_ptr() if z is not None else 0
-    pool, states = _pool(state, state_out, slots, S, (D, N), _f32, index)
+    slot_ptr, P, states = _pool(state, state_out, slots, S, (D, N), _f32, index)
     if step:
         views = (u.data_ptr(), us[0], 0, delta.data_ptr(), ds[0], 0, z_ptr, zs[0], 0, B.data_ptr(), Bs[0], 0,
                  C.data_ptr(), Cs[0], 0)
@@ -462,7 +469,7 @@ def _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, slots,
     else:
         views = (u.data_ptr(), 0, us[0], delta.data_ptr(), 0, ds[0], z_ptr, 0, zs[0], B.data_ptr(), 0, Bs[0],
                  C.data_ptr(), 0, Cs[0])
-    return G, N, (S, L, _dense(offsets, "offsets", (S + 1,), torch.int32, index), *pool, D, G, N, _code(u),
+    return G, N, (S, L, _dense(offsets, "offsets", (S + 1,), torch.int32, index), slot_ptr, P, D, G, N, _code(u),
                   bool(softplus), 0, max_len or 0, *views, Bs[-2], Cs[-2], _dense(A, "A", (D, N), _f32, index),
                   _dense(skip, "skip", (D,), _f32, index), _dense(delta_bias, "delta_bias", (D,), _f32, index), *states)
 
@@ -501,7 +508,7 @@ def selective_scan(u, delta, A, B, C, skip=None, z=None, delta_bias=None, softpl
                             L, False, index)
     D = shape[-1]
     keep, n, _ = _scan_space(S, L, offsets is not None, D, G, N, args[8], max_len or 0)
-    y = _empty(shape, u.dtype, u)
+    y = _same(u)
     saved = _empty(keep // 4, _f32, u) if save else None
     ws = _empty(n, torch.uint8, u) if n else None
     status = _lib().seq_selective_scan(
@@ -525,7 +532,7 @@ def selective_scan_step(u, delta, A, B, C, state, skip=None, z=None, delta_bias=
         raise ValueError("u must be [S, D], got shape %s" % (tuple(shape),))
     _, _, args = _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, None, slots, state,
                             state if state_out is None else state_out, 1, shape[0], 1, True, u.get_device())
-    y = _empty(shape, u.dtype, u)
+    y = _same(u)
     status = _lib().seq_selective_scan_step(_SCAN(*args, 0, y.data_ptr(), shape[1], 0), on)
     if status:
         raise ConvWgradError(status, "selective_scan_step")
@@ -548,10 +555,10 @@ def selective_scan_grad(dy, u, delta, A, B, C, saved, skip=None, z=None, delta_b
     keep, _, n = _scan_space(S, L, offsets is not None, D, G, N, args[8], max_len or 0)
     dys = _like(dy, "dy", shape, dtype, index)
     saved_ptr = _dense(saved, "saved", (keep // 4,), _f32, index)
-    du, ddelta = _empty(shape, dtype, u), _empty(shape, dtype, u)
+    du, ddelta = _same(u), _same(u)
     dB, dC = _empty(B.shape, dtype, u), _empty(B.shape, dtype, u)
     dA = _empty((D, N), _f32, u)
-    dz = _empty(shape, dtype, u) if z is not None else None
+    dz = _same(u) if z is not None else None
     dskip = _empty((D,), _f32, u) if skip is not None else None
     dbias = _empty((D,), _f32, u) if delta_bias is not None else None
     dstate = _empty((S, D, N), _f32, u) if state is not None else None
