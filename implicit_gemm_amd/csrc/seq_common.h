@@ -226,6 +226,28 @@ __device__ __forceinline__ T& at_lane(T* row, int c) {
   typedef typename std::conditional<std::is_const<T>::value, const char, char>::type Byte;
   return *reinterpret_cast<T*>(reinterpret_cast<Byte*>(row) + (uint32_t)c * (uint32_t)sizeof(T));
 }
+// The same for one element, with the row's address held to scalar registers: the compiler would rather add it to the
+// lane's part, a 64-bit vector addition a row.
+template <typename T>
+struct Bits {
+  typedef typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type Word;
+  typedef __attribute__((address_space(1))) Word Global;
+};
+__device__ __forceinline__ uint64_t scalar_address(const void* row) {
+  uint64_t b = reinterpret_cast<uint64_t>(row);
+  asm("" : "+s"(b));
+  return b;
+}
+template <typename T>
+__device__ __forceinline__ T load_lane(const T* row, int c) {
+  typedef const typename Bits<T>::Global G;
+  return __builtin_bit_cast(T, (typename Bits<T>::Word)*(G*)(scalar_address(row) + (uint32_t)c * (uint32_t)sizeof(T)));
+}
+template <typename T>
+__device__ __forceinline__ void store_lane(T* row, int c, T v) {
+  typedef typename Bits<T>::Global G;
+  *(G*)(scalar_address(row) + (uint32_t)c * (uint32_t)sizeof(T)) = __builtin_bit_cast(typename Bits<T>::Word, v);
+}
 
 template <typename T>
 __device__ __forceinline__ T* row_at(const seq_view_t& v, const Piece& p, int64_t t) {

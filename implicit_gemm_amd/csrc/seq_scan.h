@@ -46,9 +46,12 @@ template <typename T>
 struct ChannelTile {
   T v[kScanTile];
   __device__ __forceinline__ void load(const seq_view_t& view, const Piece& p, int t, int d) {
+    const T* row = row_at<const T>(view, p, min(max(t, p.t0), p.end - 1));
 #pragma unroll
-    for (int i = 0; i < kScanTile; ++i)
-      v[i] = at_lane(row_at<const T>(view, p, min(max(t + i, p.t0), p.end - 1)), d);
+    for (int i = 0; i < kScanTile; ++i) {
+      v[i] = load_lane(row, d);
+      row += t + i >= p.t0 && t + i + 1 < p.end ? view.row : 0;
+    }
   }
 };
 
@@ -74,6 +77,17 @@ struct StateTile {
     }
   }
 };
+
+// Lets the waves of a SIMD that have done less go first, in quarters of their work.  Left alone the oldest goes first, and
+// when the others have finished the youngest runs by itself, its waits in the open: 60 and 82 us for the aggregates and
+// the outputs of 8192 tokens x 2048 channels, against 53 and 74.
+__device__ __forceinline__ void yield_by_progress(int done, int all) {
+  const int quarter = done * 4 / all;
+  if (quarter == 0) __builtin_amdgcn_s_setprio(3);
+  else if (quarter == 1) __builtin_amdgcn_s_setprio(2);
+  else if (quarter == 2) __builtin_amdgcn_s_setprio(1);
+  else __builtin_amdgcn_s_setprio(0);
+}
 
 // D of a tile's tokens, zero past token n: such a token leaves the state as it is.
 template <typename T>

@@ -100,6 +100,7 @@ __global__ __launch_bounds__(64 * kScanGroup) void scan_kernel(ScanArgs k) {
     int buf = 0;
     for (int t = p.t0; t < p.end; t += kScanTile, buf ^= 1) {
       const int valid = p.end - t;
+      yield_by_progress(t - p.t0, p.end - p.t0);
       sb.put(lb[buf]);
       sc.put(lc[buf]);
       u = nu;
@@ -148,9 +149,18 @@ __global__ __launch_bounds__(64 * kScanGroup) void scan_kernel(ScanArgs k) {
         }
       }
       if (l.on) {
+        T y[kScanTile];
 #pragma unroll
-        for (int i = 0; i < kScanTile; ++i)
-          if (i < valid) from_f32(o[i], at_lane(row_at<T>(a.y, p, t + i), l.d));
+        for (int i = 0; i < kScanTile; ++i) from_f32(o[i], y[i]);
+        T* row = row_at<T>(a.y, p, t);
+        if (valid >= kScanTile) {
+#pragma unroll
+          for (int i = 0; i < kScanTile; ++i, row += a.y.row) store_lane(row, l.d, y[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kScanTile; ++i, row += a.y.row)
+            if (i < valid) store_lane(row, l.d, y[i]);
+        }
       }
     }
   }
@@ -195,6 +205,7 @@ __global__ __launch_bounds__(64 * kScanGroup) void scan_carry_kernel(ScanArgs k)
   for (int j = 0; j < tiles; ++j) {
     const int t = BACK ? t1 - j * kScanTile : t1 + j * kScanTile;
     const int next = BACK ? t - kScanTile : t + kScanTile;
+    yield_by_progress(j, tiles);
     s.put(lds[j & 1]);
     float dt[kScanTile], x[kScanTile];
     step_sizes<T>(dt, ndl, bias, a.softplus, p.end - t);
