@@ -6,10 +6,10 @@
 // and four multiply-adds, 16 states to the 8 bytes that a token and channel move.  A lane owns one channel with all its
 // states in registers, so the sum over states stays in the lane; a wave owns 64 channels and one piece of a sequence,
 // with B and C of its tokens broadcast from LDS in fp32.  Channels alone give a long prompt too few waves, so its tokens
-// are split as well (seq_scan.h).  8192 tokens x 2048 channels x 16 states in bf16: aggregates 60 us, their join 10,
-// outputs 83; the vector ALU is busy 75 % and 71 % of the first and the last (the rest is the end of each launch, when
-// the older waves of a SIMD have finished).  The rank-1 update h <- e h + x B and the sum h C on the matrix pipe
-// (v_mfma_f32_4x4x1) were slower, 75 and 120 us: its products take issue slots and their results come late.
+// are split as well (seq_scan.h).  8192 tokens x 2048 channels x 16 states in bf16: aggregates 54 us, their join 10,
+// outputs 75; the vector ALU is busy 84 % and 76 % of the first and the last.  The rank-1 update h <- e h + x B and the
+// sum h C on the matrix pipe (v_mfma_f32_4x4x1) were slower, 67 -> 75 and 99 -> 120 us when tried: its products take issue
+// slots and their results come late.
 #include "seq_scan.h"
 
 namespace cw {

@@ -5,7 +5,7 @@
 //   dD = sum_n A c[t - 1] h[t - 1] + u sum_n g B,  ddelta = dD sigmoid(delta + bias),  dA = sum_t D c[t - 1] h[t - 1]
 // and dz from o = sum_n h C + skip u.  All of it needs the states again: the forward saved one state of every 16 tokens
 // (4 bytes a token and channel for 16 states; scanning forward once more to find them would cost as much as the first
-// of the three forward launches, 67 us where writing and reading them costs 13 and 14).
+// of the three forward launches, 54 us where writing and reading them costs 10 and 14).
 //
 // Bound by the vector ALU.  A workgroup takes a piece of a sequence and 64 channels, 16 tokens at a time from the last:
 // what a token and channel need (D, D u, do) is computed once by the lane that loads it and passed through LDS; then
@@ -16,7 +16,7 @@
 // for 12 but read where needed 272).  Sums over states are taken inside a group of NG lanes, each of which keeps one of
 // NG tokens' results; sums over channels by exchanging halves of the wave (each step halves the values a lane holds),
 // then over the waves through LDS and over the channel blocks by a fold, all in a fixed order.  The vector ALU is busy
-// 83 % of the kernel's time.
+// 86 % of the kernel's 261 us.
 #include "seq_scan.h"
 
 namespace cw {
