@@ -27,9 +27,9 @@ struct ScanCut {
   bool split;
 };
 // Long sequences are cut so that pieces x channel blocks come to about kScanWaves waves, four to a SIMD; a piece has at
-// least 16 tokens.  8192 tokens x 2048 channels: 2048 waves 169 us for the three launches, 4096 152, 8192 154 (a piece
-// of 32 tokens, whose carries are then as many bytes as the inputs).  Up to kScanWhole tokens one launch is as quick as
-// three.
+// least 16 tokens.  8192 tokens x 2048 channels: 2048 waves 165 us for the three launches, 4096 138, 8192 158 (a piece
+// of 32 tokens, whose carries are then as many bytes as the inputs); 5003 x 1536 in 12 sequences: 107, 84 and 102.
+// Up to kScanWhole tokens one launch is as quick as three.
 constexpr int64_t kScanWaves = 4096, kScanWhole = 64;
 ScanCut scan_cut(const seq_scan_args_t& a);
 inline int scan_dblocks(const seq_scan_args_t& a) { return (int)((a.channels / a.groups + 63) / 64); }
