@@ -129,15 +129,22 @@ __global__ __launch_bounds__(256) void norm_kernel(seq_norm_args_t a) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int c = (v * TEAM + lane) * V;
-        // top / 448 underflows to zero for the smallest denormals too
+        // top / 448 underflows to zero for the smallest denormals too; a denormal scale can be so much smaller than top /
+        // 448 that the quotient passes 464, whose code is NaN: there it is held to 448 (and is a number, as top is).
         float scale = top[v] / 448.f;
         scale = scale == 0.f ? 1.f : scale;
+        const bool rough = scale < __FLT_MIN__;
         if (c < C) {
           if (group == 0 ? c == 0 : c % group == 0) a.scale[row * nscale + (group ? c / group : 0)] = scale;
+          float f[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            f[i] = y[v][i] / scale;
+            f[i] = rough ? __builtin_amdgcn_fmed3f(f[i], -448.f, 448.f) : f[i];
+          }
           uint32_t packed[V / 4];
 #pragma unroll
-          for (int i = 0; i < V; i += 4)
-            packed[i / 4] = e4m3x4(y[v][i] / scale, y[v][i + 1] / scale, y[v][i + 2] / scale, y[v][i + 3] / scale);
+          for (int i = 0; i < V; i += 4) packed[i / 4] = e4m3x4(f[i], f[i + 1], f[i + 2], f[i + 3]);
           if (c + V <= C) {
             __builtin_memcpy(q + c, packed, V);
           } else {

@@ -300,7 +300,7 @@ def rms_norm(x, w, residual=None, eps=1e-5, stream=None):
 def rms_norm_e4m3(x, w, residual=None, eps=1e-5, group=0, stream=None):
     """The norm of rms_norm in 8 bits: (q, scale, h) with q float8_e4m3fn [..., C] and float32 scale [..., ceil(C /
     group)], one per `group` (32, 64, 128 or 256) channels or, for group 0, one per row: scale = max|y| / 448 (1 where
-    that is zero), q = y / scale."""
+    that is zero), q = y / scale, held to 448 where the scale lies below float32's normal range."""
     on = _here(x, stream)
     if on is None:
         return _there(x, stream, rms_norm_e4m3, x, w, residual, eps, group)

@@ -469,7 +469,8 @@ typedef struct seq_norm_args {
 conv_wgrad_status_t seq_rms_norm(const seq_norm_args_t* args, void* stream);
 
 /* The norm with an 8-bit output (OCP e4m3, largest value 448): per group of channels scale = max|h r w| / 448 (1 where
- * that is zero) and y = e4m3(h r w / scale), rounded to nearest even. */
+ * that is zero) and y = e4m3(h r w / scale), rounded to nearest even.  A scale below fp32's normal range has few bits,
+ * so that the quotient can pass 448: it is held to that. */
 conv_wgrad_status_t seq_rms_norm_e4m3(const seq_norm_args_t* args, void* stream);
 
 /*

@@ -122,6 +122,23 @@ def test_norm_keeps_nan_and_infinity_in_their_row(iga):
     assert scale[0].isnan().all() and scale[1, 0].isnan() and bool(torch.isfinite(scale[2]).all())
 
 
+def test_norm_e4m3_below_the_normal_range(iga):
+    """A scale below the normal range can be rounded to far less than max|y| / 448: the codes stay finite.  x = 1 and
+    eps = 0 make y = w."""
+    unit = 2.0 ** -149
+    tops = torch.tensor([1, 223, 225, 313, 470, 667, 673, 6048, 100000, 2.0 ** 33])      # of the groups, in units
+    w = (torch.linspace(-1, 1, 32)[None, :] * tops[:, None] * unit).double().flatten().float()
+    for group, shape in ((32, (len(tops), 32)), (0, (1, -1))):
+        q, scale, _ = iga.rms_norm_e4m3(torch.ones(2, len(w)).cuda(), w.cuda(), eps=0.0, group=group)
+        want = w.view(shape).abs().amax(1) / 448           # 32 bits, denormals among them
+        want = torch.where(want == 0, torch.ones_like(want), want)
+        assert torch.equal(scale.cpu(), want.expand(2, -1))
+        v = (w.view(shape).double() / want.double()[:, None]).clamp(-448, 448).flatten()
+        got = q.cpu().float().double()
+        assert bool(torch.isfinite(got).all()) and float(got.abs().max()) <= 448
+        assert bool(((got - v).abs() <= v.abs() * 2.0 ** -4 + 2.0 ** -10).all())
+
+
 def test_norm_of_higher_rank_and_its_refusals(iga):
     rand = gen(1)
     x = rand(2, 3, 5, 64).cuda()
