@@ -230,7 +230,9 @@ __global__ __launch_bounds__(256, 4) void conv_grad_kernel(ConvGradArgs k) {
 #pragma unroll
     for (int i = 0; i < W - 1; ++i) {
       Raw<T, V> r;
-      if (p.t0 == 0) {
+      if (n == 0) {   // no token: its window, whatever it holds, is no part of dw
+        r.clear();
+      } else if (p.t0 == 0) {
         load_state<T, V>(r, a, slot, i, c, nv);
       } else {
         r.clear();

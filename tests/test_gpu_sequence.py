@@ -238,6 +238,23 @@ def test_conv_long_has_many_pieces_a_workgroup(iga, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D", [128, 70])
+def test_conv_gradient_of_an_empty_sequence_ignores_its_window(iga, D, dtype):
+    rand, dt = gen(D), DT[dtype]
+    off = torch.tensor([0, 20, 20, 20, 53, 53], dtype=torch.int32).cuda()
+    x, dy, w, b = rand(53, D, dtype=dt).cuda(), rand(53, D, dtype=dt).cuda(), rand(D, 4, std=0.5).cuda(), rand(D).cuda()
+    state, dlast = rand(5, 3, D, dtype=dt).cuda(), rand(5, 3, D, dtype=dt).cuda()
+    state[[1, 2, 4]] = 0
+    kw = dict(silu=True, offsets=off, dstate_out=dlast)
+    want = iga.causal_conv_grad(dy, x, w, b, state=state, **kw)
+    state[1], state[2, 1], state[4] = float("nan"), float("inf"), -float("inf")
+    got = iga.causal_conv_grad(dy, x, w, b, state=state, **kw)
+    for g, e in zip(got, want):
+        assert bool(torch.isfinite(g).all()) and torch.equal(g, e)
+    assert torch.equal(got[3][[1, 2, 4]], dlast[[1, 2, 4]])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("W,D,S", [(4, 300, 1), (4, 1030, 5), (2, 3, 4), (3, 64, 2)])
 def test_conv_step_matches_prompt(iga, W, D, S, dtype):
     """Tokens one at a time give the prompt's outputs bit for bit (the same sums in the same order) and its window."""
