@@ -434,6 +434,24 @@ def test_scan_in_place_and_in_two_halves(iga, split):
     close(state, last.double(), torch.float32, 16 + 12 * L, "state")
 
 
+@pytest.mark.parametrize("late", [True, False])
+def test_scan_of_growing_states(iga, late):
+    """Where A D is positive a state of zero stays zero and a tiny one grows to what it should, though e^(A sum D) of the
+    tokens between overflows (late: inputs in the last 20 tokens and gradients in the first 10, so that both directions
+    carry zeros; else a tiny first state)."""
+    c = scan_case(24, 3, 1, None, 0, "f32", ("skip", "state", "last"), 31, L=400 if late else 100)
+    c["A"] = c["A"].abs()                      # 0.8 .. 3.6
+    c["delta"] = torch.full_like(c["delta"], 0.4 if late else 0.28)
+    if late:
+        c["u"][:, :380], c["dy"][:, 10:] = 0, 0
+        c["state"], c["dlast"] = torch.zeros_like(c["state"]), torch.zeros_like(c["dlast"])
+        check_scan(c, run_scan(iga, c), 400)
+    else:
+        c["u"] = torch.zeros_like(c["u"])
+        c["state"] *= 1e-30
+        check_scan(c, run_scan(iga, c, grad=False), 100)
+
+
 def test_scan_gradient_against_differences(iga):
     """The directional derivative from the GPU's gradients against central differences of the 64-bit definition."""
     c = scan_case(20, 16, 1, None, 0, "f32", ALL, 8, L=70)
