@@ -53,6 +53,12 @@ struct ChannelTile {
       row += t + i >= p.t0 && t + i + 1 < p.end ? view.row : 0;
     }
   }
+  // Zeros past token n.
+  __device__ __forceinline__ void cut(int n) {
+#pragma unroll
+    for (int i = 0; i < kScanTile; ++i)
+      if (i >= n) from_f32(0.f, v[i]);
+  }
 };
 
 // Rows [t, t + kScanTile) of B or C, widened, through registers into LDS ([token][NP]); zeros where there is none.
@@ -89,10 +95,18 @@ __device__ __forceinline__ void yield_by_progress(int done, int all) {
   else __builtin_amdgcn_s_setprio(0);
 }
 
-// D of a tile's tokens, zero past token n: such a token leaves the state as it is.
+// A log2 e.  Where that is -inf (a state that holds one token's input only) it is fp32's lowest value instead: e^(D A) is
+// zero for every D but zero, that of a token past the end, which has to leave the state as it is.
+__device__ __forceinline__ float decay_rate(float A) {
+  const float v = A * kLog2e;
+  return v < -__FLT_MAX__ ? -__FLT_MAX__ : v;
+}
+
+// D of a tile's tokens, zero past token n, as is `in`, which repeats its last row there: such a token leaves the state as it
+// is, also where that row is infinite.
 template <typename T>
 __device__ __forceinline__ void step_sizes(float (&dt)[kScanTile], const ChannelTile<T>& delta, float bias,
-                                           int32_t with_softplus, int n) {
+                                           int32_t with_softplus, int n, ChannelTile<T>& in) {
 #pragma unroll
   for (int i = 0; i < kScanTile; ++i) dt[i] = to_f32(delta.v[i]) + bias;
   if (with_softplus) {
@@ -102,6 +116,7 @@ __device__ __forceinline__ void step_sizes(float (&dt)[kScanTile], const Channel
   if (n < kScanTile) {
 #pragma unroll
     for (int i = 0; i < kScanTile; ++i) dt[i] = i < n ? dt[i] : 0.f;
+    in.cut(n);
   }
 }
 

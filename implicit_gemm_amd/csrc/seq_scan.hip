@@ -33,7 +33,7 @@ __device__ __forceinline__ Lane lane_channel(const ScanArgs& k, int block) {
   return Lane{g * Dg + min(c, Dg - 1), g, c < Dg};
 }
 
-// A log2 e of a channel, zero for the states past N.  The lanes' rows lie 4 N bytes apart, and a load takes a cycle for
+// Decay rates of a channel, zero for the states past N.  The lanes' rows lie 4 N bytes apart, and a load takes a cycle for
 // each of the 64 lines that it touches: four states a load where they come in fours.
 template <int NP>
 __device__ __forceinline__ void load_decay(const seq_scan_args_t& a, int d, float (&A2)[NP]) {
@@ -45,11 +45,11 @@ __device__ __forceinline__ void load_decay(const seq_scan_args_t& a, int d, floa
       r.clear();
       if (n < a.states) r.load(row + n);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) A2[n + i] = r.get(i) * kLog2e;
+      for (int i = 0; i < 4; ++i) A2[n + i] = decay_rate(r.get(i));
     }
   } else {
 #pragma unroll
-    for (int n = 0; n < NP; ++n) A2[n] = n < a.states ? row[n] * kLog2e : 0.f;
+    for (int n = 0; n < NP; ++n) A2[n] = n < a.states ? decay_rate(row[n]) : 0.f;
   }
 }
 
@@ -105,7 +105,7 @@ __global__ __launch_bounds__(64 * kScanGroup) void scan_kernel(ScanArgs k) {
       sc.put(lc[buf]);
       u = nu;
       float dt[kScanTile], o[kScanTile];
-      step_sizes<T>(dt, ndl, bias, a.softplus, valid);
+      step_sizes<T>(dt, ndl, bias, a.softplus, valid, u);
       wave_sync();
       nu.load(a.u, p, t + kScanTile, l.d);
       ndl.load(a.delta, p, t + kScanTile, l.d);
@@ -200,7 +200,10 @@ __global__ __launch_bounds__(64 * kScanGroup) void scan_carry_kernel(ScanArgs k)
   const int t1 = BACK ? p.t0 + (tiles - 1) * kScanTile : p.t0;
   nu.load(in, p, t1, l.d);
   ndl.load(a.delta, p, t1, l.d);
-  if (BACK && a.z.ptr) nz.load(a.z, p, t1, l.d);
+  if (BACK && a.z.ptr) {
+    nz.load(a.z, p, t1, l.d);
+    nz.cut(p.end - t1);   // the only tile that can pass the end
+  }
   s.load(side, goff, p, t1, N);
   for (int j = 0; j < tiles; ++j) {
     const int t = BACK ? t1 - j * kScanTile : t1 + j * kScanTile;
@@ -208,7 +211,7 @@ __global__ __launch_bounds__(64 * kScanGroup) void scan_carry_kernel(ScanArgs k)
     yield_by_progress(j, tiles);
     s.put(lds[j & 1]);
     float dt[kScanTile], x[kScanTile];
-    step_sizes<T>(dt, ndl, bias, a.softplus, p.end - t);
+    step_sizes<T>(dt, ndl, bias, a.softplus, p.end - t, nu);
 #pragma unroll
     for (int i = 0; i < kScanTile; ++i) x[i] = to_f32(nu.v[i]);
     if constexpr (BACK) {
@@ -294,7 +297,7 @@ __global__ __launch_bounds__(64 * WAVES) void scan_join_kernel(ScanArgs k) {
     len = k.m.rows;
   }
   const int count = max(1, ((len - 1) >> k.m.shift) + 1);   // len 0: one piece
-  const float A2 = a.A[(int64_t)d * N + n] * kLog2e;
+  const float A2 = decay_rate(a.A[(int64_t)d * N + n]);
   float h = 0.f;
   if (BACK) {
     if (k.last) h = k.last[((int64_t)s * D + d) * N + n];
@@ -401,7 +404,7 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs k) {
   for (int i = 0; i < 4; ++i) {
     out[i] = 0.f;
     if (FULL || i < nv) {
-      out[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * (A.get(i) * kLog2e)), h.get(i), x * B.get(i));
+      out[i] = __builtin_fmaf(__builtin_amdgcn_exp2f(dt * decay_rate(A.get(i))), h.get(i), x * B.get(i));
       o = __builtin_fmaf(out[i], C.get(i), o);
     }
   }

@@ -160,7 +160,7 @@ __global__ __launch_bounds__(64 * NG, 2) void scan_grad_kernel(GradArgs k) {
 
   float A2[4], dA[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) A2[i] = FULL || i < nv ? a.A[(int64_t)(d0 + chc) * N + n0 + i] * kLog2e : 0.f;
+  for (int i = 0; i < 4; ++i) A2[i] = FULL || i < nv ? decay_rate(a.A[(int64_t)(d0 + chc) * N + n0 + i]) : 0.f;
   float dskip[V], dbias[V];
 #pragma unroll
   for (int j = 0; j < V; ++j) dskip[j] = dbias[j] = 0.f;

@@ -452,6 +452,41 @@ def test_scan_of_growing_states(iga, late):
         check_scan(c, run_scan(iga, c, grad=False), 100)
 
 
+@pytest.mark.parametrize("L", [37, 64, 100])
+def test_scan_of_infinite_inputs_and_decays(iga, L):
+    """A of -inf forgets at each token; an infinite last input gives an infinite state, whatever the length is a multiple
+    of."""
+    c = scan_case(24, 8, 1, None, 0, "f32", ("skip", "state"), 32, L=L)
+    c["B"], c["C"], c["skip"] = c["B"].abs() + 0.1, c["C"].abs() + 0.1, c["skip"].abs()
+    c["A"][:, 2] = -float("inf")
+    y, last = run_scan(iga, c, grad=False)
+    assert bool(torch.isfinite(last).all()) and bool(torch.isfinite(y).all())
+    check_scan(c, (y, last), L)
+    c["u"][0, -1, 3], c["u"][1, -1, 4] = float("inf"), -float("inf")
+    y, last = run_scan(iga, c, grad=False)
+    check_scan(c, (y, last), L)
+    assert bool((last[0, 3] == float("inf")).all()) and bool((last[1, 4] == -float("inf")).all())
+    state = c["state"].cuda()
+    out = iga.selective_scan_step(c["u"].cuda()[:, 0], c["delta"].cuda()[:, 0], c["A"].cuda(), c["B"].cuda()[:, 0],
+                                  c["C"].cuda()[:, 0], state, skip=c["skip"].cuda())
+    one = {k: v[:, :1] if k in ("u", "delta", "B", "C", "dy") else v for k, v in c.items()}
+    check_scan(one, (out[:, None], state), 1)
+
+
+@pytest.mark.parametrize("L", [37, 64, 100])
+def test_scan_gradient_of_an_infinite_last_gradient(iga, L):
+    c = scan_case(24, 8, 1, None, 0, "f32", ("skip",), 33, L=L)
+    for k in ("B", "C", "skip"):
+        c[k] = c[k].abs() + 0.1
+    c["dy"][0, -1, 3], c["dy"][1, -1, 4] = float("inf"), -float("inf")
+    du = run_scan(iga, c)[2].du
+    leaves = [leaf(c[n]) for n in ("u", "delta", "A", "B", "C", "skip")]
+    y, _ = ref.scan(*leaves, None, None, False, None, None)
+    want = ref.grads((y,), (c["dy"].double(),), leaves)[0]
+    assert bool((want[0, :, 3] == float("inf")).all()) and bool((want[1, :, 4] == -float("inf")).all())
+    close(du, want, torch.float32, 4 * (16 + 12 * L), "du")
+
+
 def test_scan_gradient_against_differences(iga):
     """The directional derivative from the GPU's gradients against central differences of the 64-bit definition."""
     c = scan_case(20, 16, 1, None, 0, "f32", ALL, 8, L=70)
