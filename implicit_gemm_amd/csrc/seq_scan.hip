@@ -267,19 +267,15 @@ __global__ __launch_bounds__(64 * kScanGroup) void scan_carry_kernel(ScanArgs k)
 // workgroups fill the GPU more than once: 12 sequences of up to 29 pieces, 1536 channels x 16 states (4608 workgroups),
 // take 17 us with four and 12 with one; 3 sequences of 33 pieces, 387 x 11 (231 workgroups), 4.5 and 6.8.
 //
-// A decay is e^(A sum D) of a whole piece (or of sixteen).  Where A D is positive, states grow, and over a piece by more
-// than fp32 holds though the state itself stays small, or zero: 2^x h is then 2^127 (2^(x - 127) h), for x up to 254, past
-// which any state that is not zero overflows.  Only a wave with such a piece (none where A < 0) takes this way, in a rolled
-// loop of its own: unrolled it cost every join 2 us of 11.
+// A decay is 2^x, x = A log2 e sum D, of a whole piece (or of sixteen).  Where A D is positive, states grow, and over a piece
+// by more than fp32 holds though the state itself stays small, or zero (inf x 0): so 2^x h is 2^(x/2) (2^(x/2) h), for x up
+// to 254, past which any state that is not zero overflows.
 constexpr int kJoinEach = 16;
-constexpr float kMaxExp = 127.f;
-__device__ __forceinline__ float piece_decay(float x) { return __builtin_amdgcn_exp2f(x > kMaxExp ? kMaxExp : x); }
-__device__ __forceinline__ float piece_growth(float x) {
-  return __builtin_amdgcn_exp2f(__builtin_amdgcn_fmed3f(x - kMaxExp, 0.f, kMaxExp));
-}
+// 2^half; a sum of D that is NaN comes with an end state that is.
+__device__ __forceinline__ float half_decay(float half) { return __builtin_amdgcn_exp2f(fminf(half, 127.f)); }
 template <bool BACK, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void scan_join_kernel(ScanArgs k) {
-  __shared__ float l_end[WAVES][64], l_decay[WAVES][64], l_growth[WAVES][64];
+  __shared__ float l_end[WAVES][64], l_decay[WAVES][64];
   const seq_scan_args_t& a = k.a;
   const int N = a.states, D = (int)a.channels;
   const int dblocks = (D + 63) / 64;
@@ -297,7 +293,7 @@ __global__ __launch_bounds__(64 * WAVES) void scan_join_kernel(ScanArgs k) {
     len = k.m.rows;
   }
   const int count = max(1, ((len - 1) >> k.m.shift) + 1);   // len 0: one piece
-  const float A2 = decay_rate(a.A[(int64_t)d * N + n]);
+  const float half = 0.5f * decay_rate(a.A[(int64_t)d * N + n]);
   float h = 0.f;
   if (BACK) {
     if (k.last) h = k.last[((int64_t)s * D + d) * N + n];
@@ -318,49 +314,27 @@ __global__ __launch_bounds__(64 * WAVES) void scan_join_kernel(ScanArgs k) {
         q[i] = k.sums[at * D + d];
       }
     }
-    float end = 0.f, sum = 0.f, most = 0.f;
+    float end = 0.f, sum = 0.f;
 #pragma unroll
     for (int i = 0; i < kJoinEach; ++i) {
-      const float x = A2 * q[i];
       sum += q[i];
-      most = fmaxf(most, x);
-      q[i] = __builtin_amdgcn_exp2f(x);
-      end = __builtin_fmaf(q[i], end, e[i]);
-    }
-    const bool grows = __any(most > kMaxExp);
-    auto slowly = [&](float& c, bool put) {   // this wave's pieces, read again one by one
-#pragma unroll 1
-      for (int j = mine; j < min(mine + kJoinEach, count); ++j) {
-        const int64_t at = first + (BACK ? count - 1 - j : j);
-        float& e = k.carry[(at * N + n) * D + d];
-        const float x = A2 * k.sums[at * D + d], to = __builtin_fmaf(piece_decay(x), piece_growth(x) * c, e);
-        if (put && on) e = c;
-        if (j < count - 1) c = to;   // the last piece has no aggregates
-      }
-    };
-    if (grows) {
-      end = 0.f;
-      slowly(end, false);
+      q[i] = half_decay(half * q[i]);
+      end = __builtin_fmaf(q[i], q[i] * end, e[i]);
     }
     l_end[wave][lane] = end;
-    l_decay[wave][lane] = piece_decay(A2 * sum);
-    l_growth[wave][lane] = piece_growth(A2 * sum);
+    l_decay[wave][lane] = half_decay(half * sum);
     __syncthreads();
     float c = h;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
       if (w == wave) c = h;
-      h = __builtin_fmaf(l_decay[w][lane], l_growth[w][lane] * h, l_end[w][lane]);
+      h = __builtin_fmaf(l_decay[w][lane], l_decay[w][lane] * h, l_end[w][lane]);
     }
-    if (grows) {
-      slowly(c, true);
-    } else {
 #pragma unroll
-      for (int i = 0; i < kJoinEach; ++i) {
-        const int j = mine + i;
-        if (j < count && on) k.carry[((int64_t)(first + (BACK ? count - 1 - j : j)) * N + n) * D + d] = c;
-        c = __builtin_fmaf(q[i], c, e[i]);
-      }
+    for (int i = 0; i < kJoinEach; ++i) {
+      const int j = mine + i;
+      if (j < count && on) k.carry[((int64_t)(first + (BACK ? count - 1 - j : j)) * N + n) * D + d] = c;
+      c = __builtin_fmaf(q[i], q[i] * c, e[i]);
     }
     __syncthreads();
   }
