@@ -42,6 +42,7 @@ struct FoldList {
   FoldPart f[5];
   int32_t n;
 };
+int64_t fold_lanes(const FoldList& list);   // of the launch
 hipError_t launch_seq_fold(const FoldList& list, hipStream_t stream);
 
 hipError_t launch_norm(const seq_norm_args_t& a, bool e4m3, hipStream_t stream);
@@ -61,7 +62,10 @@ int64_t scan_save_floats(const seq_scan_args_t& a);
 int64_t scan_ws_floats(const seq_scan_args_t& a);
 hipError_t launch_scan(const seq_scan_args_t& a, float* ws, hipStream_t stream);
 hipError_t launch_scan_step(const seq_scan_args_t& a, hipStream_t stream);
-int64_t scan_grad_ws_floats(const seq_scan_grad_args_t& a);
+int64_t scan_grad_ws_floats(const seq_scan_grad_args_t& g);
+// Lanes of the largest launch of a call.
+int64_t scan_lanes(const seq_scan_args_t& a);
+int64_t scan_grad_lanes(const seq_scan_grad_args_t& g);
 hipError_t launch_scan_grad(const seq_scan_grad_args_t& a, float* ws, hipStream_t stream);
 
 }  // namespace cw

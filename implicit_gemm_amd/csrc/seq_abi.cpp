@@ -161,12 +161,10 @@ Status check_scan_grad(const seq_scan_grad_args_t* g) {
   const Status st = check_scan_shape(a, false);
   if (st != CONV_WGRAD_OK) return st;
   if (negative(g->dy)) return CONV_WGRAD_ERR_BAD_SHAPE;
-  // a lane's part of an address, up to 15 rows, is 32 bits
+  // the bytes between two rows are 32 bits in the kernel
   for (const seq_view_t* v : {&a.u, &a.delta, &a.z, &a.B, &a.C, &g->dy})
     if (v->row >= (int64_t)1 << 26) return CONV_WGRAD_ERR_UNSUPPORTED;
-  // the fold's lanes over dB: at most 32 an output
-  if (!fits(seq_rows(a.tokens), 32 * a.groups * a.states)) return CONV_WGRAD_ERR_UNSUPPORTED;
-  return CONV_WGRAD_OK;
+  return cw::scan_grad_lanes(*g) <= kMaxLanes ? CONV_WGRAD_OK : CONV_WGRAD_ERR_UNSUPPORTED;
 }
 
 Status check_space(const void* ws, size_t have, uint64_t floats) {

@@ -56,17 +56,37 @@ __global__ __launch_bounds__(kThreads) void seq_fold_kernel(FoldArgs a) {
 
 }  // namespace
 
+namespace {
+
+bool all_few(const FoldList& list) {
+  for (int i = 0; i < list.n; ++i)
+    if (list.f[i].count > kFewMax) return false;
+  return true;
+}
+
+// Workgroups of fold i.
+int64_t fold_blocks(const FoldList& list, int i, bool few) {
+  const int cols = few ? 64 : list.f[i].count <= kFewMax ? 256 : 32;
+  return (list.f[i].E + cols - 1) / cols;
+}
+
+}  // namespace
+
+int64_t fold_lanes(const FoldList& list) {
+  const bool few = all_few(list);
+  int64_t blocks = 0;
+  for (int i = 0; i < list.n; ++i) blocks += fold_blocks(list, i, few);
+  return blocks * (few ? 256 : 1024);
+}
+
 hipError_t launch_seq_fold(const FoldList& list, hipStream_t stream) {
   FoldArgs a;
   a.l = list;
-  int32_t most = 0;
-  for (int i = 0; i < list.n; ++i) most = list.f[i].count > most ? list.f[i].count : most;
-  const bool few = most <= kFewMax;
+  const bool few = all_few(list);
   int64_t blocks = 0;
   for (int i = 0; i < list.n; ++i) {
     a.first[i] = (int32_t)blocks;
-    const int cols = few ? 64 : list.f[i].count <= kFewMax ? 256 : 32;
-    blocks += (list.f[i].E + cols - 1) / cols;
+    blocks += fold_blocks(list, i, few);
   }
   if (blocks == 0) return hipSuccess;
   if (few) return launch_kernel(seq_fold_kernel<256>, dim3((unsigned)blocks), dim3(256), a, stream);

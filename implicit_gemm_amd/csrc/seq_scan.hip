@@ -398,9 +398,8 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanArgs k) {
   }
 }
 
-unsigned scan_grid(const ScanArgs& k) {
-  return (unsigned)(((int64_t)k.pieces * k.dblocks * k.a.groups + kScanGroup - 1) / kScanGroup);
-}
+int64_t scan_groups(int64_t pieces, const seq_scan_args_t& a) { return (pieces * scan_blocks(a) + kScanGroup - 1) / kScanGroup; }
+unsigned scan_grid(const ScanArgs& k) { return (unsigned)scan_groups(k.pieces, k.a); }
 
 template <typename T, int NP>
 hipError_t scan_t(const ScanArgs& k, hipStream_t stream) {
@@ -461,12 +460,23 @@ int64_t scan_ws_floats(const seq_scan_args_t& a) {
   return scan_round(pieces * a.channels * a.states) + scan_round(pieces * a.channels);
 }
 
+static int64_t join_groups(const seq_scan_args_t& a) { return (a.channels + 63) / 64 * a.states * a.tokens.sequences; }
+static bool join_few(const seq_scan_args_t& a, int shift) {
+  return (scan_longest(a) >> shift) <= 2 * kJoinEach && join_groups(a) > 2048;
+}
+
+int64_t scan_lanes(const seq_scan_args_t& a) {
+  const ScanCut cut = scan_cut(a);
+  const int64_t pieces = scan_groups(seq_pieces(seq_map(a.tokens, cut.shift)), a) * 64 * kScanGroup;
+  const int64_t join = cut.split ? join_groups(a) * (join_few(a, cut.shift) ? 64 : 256) : 0;
+  return pieces > join ? pieces : join;
+}
+
 hipError_t launch_scan_carry(const ScanArgs& k, bool backward, hipStream_t stream) {
   const hipError_t err = carry_any(k, backward, stream);
   if (err != hipSuccess) return err;
-  const int64_t groups = (k.a.channels + 63) / 64 * k.a.states * k.a.tokens.sequences;
-  const dim3 grid((unsigned)groups);
-  const bool few = (scan_longest(k.a) >> k.m.shift) <= 2 * kJoinEach && groups > 2048;
+  const dim3 grid((unsigned)join_groups(k.a));
+  const bool few = join_few(k.a, k.m.shift);
   if (backward)
     return few ? launch_kernel(scan_join_kernel<true, 1>, grid, dim3(64), k, stream)
                : launch_kernel(scan_join_kernel<true, 4>, grid, dim3(256), k, stream);

@@ -488,7 +488,30 @@ GradSpace grad_space(const seq_scan_args_t& a) {
   return w;
 }
 
+// The sums over channel blocks and workgroups, from the partial results.
+FoldList grad_folds(const seq_scan_grad_args_t& g, const GradSpace& w, const float* ws) {
+  const seq_scan_args_t& a = g.fwd;
+  const int64_t D = a.channels, bc = seq_rows(a.tokens) * a.groups * a.states;
+  const float *part_bc = ws + w.bc, *part_a = ws + w.a, *part_s = ws + w.s;
+  FoldList l;
+  l.n = 0;
+  l.f[l.n++] = FoldPart{part_bc, 2 * bc, scan_dblocks(a), bc, g.dB, a.dtype};
+  l.f[l.n++] = FoldPart{part_bc + bc, 2 * bc, scan_dblocks(a), bc, g.dC, a.dtype};
+  l.f[l.n++] = FoldPart{part_a, D * a.states, w.parts, D * a.states, g.dA, CONV_WGRAD_F32};
+  if (g.dskip) l.f[l.n++] = FoldPart{part_s, 2 * D, w.parts, D, g.dskip, CONV_WGRAD_F32};
+  if (g.ddelta_bias) l.f[l.n++] = FoldPart{part_s + D, 2 * D, w.parts, D, g.ddelta_bias, CONV_WGRAD_F32};
+  return l;
+}
+
 }  // namespace
+
+int64_t scan_grad_lanes(const seq_scan_grad_args_t& g) {
+  const GradSpace w = grad_space(g.fwd);
+  const int64_t n = g.fwd.states, lanes = 64 * (n <= 8 ? 2 : n <= 16 ? 4 : 8);
+  const int64_t sweep = w.parts * scan_blocks(g.fwd) * lanes, fold = fold_lanes(grad_folds(g, w, nullptr));
+  const int64_t before = scan_lanes(g.fwd);   // aggregates and join of the same cut
+  return sweep > fold ? sweep > before ? sweep : before : fold > before ? fold : before;
+}
 
 int64_t scan_grad_ws_floats(const seq_scan_grad_args_t& g) { return grad_space(g.fwd).total; }
 
@@ -514,15 +537,7 @@ hipError_t launch_scan_grad(const seq_scan_grad_args_t& g, float* ws, hipStream_
   hipError_t err;
   if (cut.split && (err = launch_scan_carry(k.s, true, stream)) != hipSuccess) return err;
   if ((err = grad_any(k, stream)) != hipSuccess) return err;
-  const int64_t D = a.channels, bc = seq_rows(a.tokens) * a.groups * a.states;
-  FoldList l;
-  l.n = 0;
-  l.f[l.n++] = FoldPart{k.part_bc, 2 * bc, k.s.dblocks, bc, g.dB, a.dtype};
-  l.f[l.n++] = FoldPart{k.part_bc + bc, 2 * bc, k.s.dblocks, bc, g.dC, a.dtype};
-  l.f[l.n++] = FoldPart{k.part_a, D * a.states, w.parts, D * a.states, g.dA, CONV_WGRAD_F32};
-  if (g.dskip) l.f[l.n++] = FoldPart{k.part_s, 2 * D, w.parts, D, g.dskip, CONV_WGRAD_F32};
-  if (g.ddelta_bias) l.f[l.n++] = FoldPart{k.part_s + D, 2 * D, w.parts, D, g.ddelta_bias, CONV_WGRAD_F32};
-  return launch_seq_fold(l, stream);
+  return launch_seq_fold(grad_folds(g, w, ws), stream);
 }
 
 }  // namespace cw

@@ -164,6 +164,30 @@ def test_scan_step_and_grad_refusals():
         assert lib.seq_selective_scan_grad(grad(**over), P, n.value, None) == status, over
 
 
+def grad_of(tokens, channels, groups, states):
+    row = sq._View(P, 0, channels)
+    f = sq.ScanArgs((*tokens, 0, 0, tokens[0]), channels, groups, states, 1, 1, 0, 0, row, row, row, row, row, 0, 0, P, P, P,
+                    0, 0, 0, 0, P, row)
+    return sq.ScanGradArgs(f, row, 0, *([P] * 9))
+
+
+@pytest.mark.parametrize("tokens,channels,groups,states", [
+    ((1, (1 << 21) + 16), 4160, 1, 32),      # the fold of dB and dC: 65 channel blocks, 32 lanes an output of both
+    ((1, (1 << 22) + 16), 8192, 1, 16),
+    ((16, 0), 1 << 20, 1 << 20, 32),         # the sweep: a workgroup of 512 lanes a channel and sequence
+])
+def test_scan_gradient_too_large_for_one_of_its_launches(tokens, channels, groups, states):
+    """Refused before anything is enqueued, not by the launch that it does not fit after others ran."""
+    n = ctypes.c_size_t(0)
+    g = grad_of(tokens, channels, groups, states)
+    lib = sq._lib()
+    assert lib.seq_selective_scan_grad_workspace(ctypes.byref(g), ctypes.byref(n)) == UNSUPPORTED
+    assert lib.seq_selective_scan_grad(ctypes.byref(g), P, 1 << 62, None) == UNSUPPORTED
+    assert lib.seq_selective_scan_workspace(ctypes.byref(g.fwd), ctypes.byref(n)) == OK
+    half = grad_of((tokens[0], tokens[1] // 2) if tokens[1] else (tokens[0] // 4, 0), channels, groups, states)
+    assert lib.seq_selective_scan_grad_workspace(ctypes.byref(half), ctypes.byref(n)) == OK
+
+
 def test_tensors_on_the_host_are_refused():
     x, w = torch.zeros(2, 8), torch.ones(8)
     with pytest.raises(ValueError):
