@@ -474,14 +474,22 @@ def _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, slots,
                   _dense(skip, "skip", (D,), _f32, index), _dense(delta_bias, "delta_bias", (D,), _f32, index), *states)
 
 
+def _scan_sizes(S, L, packed, D, G, N, code, longest):
+    """The arguments that space depends on."""
+    return (S, L, 16 if packed else 0, 0, S, D, G, N, code, 0, 0, longest, *[0] * 15, 0, 0, *[0] * 3, 0, 0, 0, 0, 0, 0, 0, 0)
+
+
 @functools.lru_cache(4096)
-def _scan_space(S, L, packed, D, G, N, code, longest):
-    """Bytes of (saved, the forward's workspace, the gradient's)."""
-    fwd = (S, L, 16 if packed else 0, 0, S, D, G, N, code, 0, 0, longest, *[0] * 15, 0, 0, *[0] * 3, 0, 0, 0, 0, 0,
-           0, 0, 0)
-    a = _SCAN(*fwd)
-    return (_bytes("seq_selective_scan_save", a), _bytes("seq_selective_scan_workspace", a),
-            _bytes("seq_selective_scan_grad_workspace", _SCAN_GRAD(*fwd, *[0] * 13)))
+def _scan_space(*sizes):
+    """Bytes of (saved, the forward's workspace)."""
+    a = _SCAN(*_scan_sizes(*sizes))
+    return _bytes("seq_selective_scan_save", a), _bytes("seq_selective_scan_workspace", a)
+
+
+@functools.lru_cache(4096)
+def _scan_grad_space(*sizes):
+    """Bytes of (saved, the gradient's workspace); fewer sizes have a gradient than a forward."""
+    return _scan_space(*sizes)[0], _bytes("seq_selective_scan_grad_workspace", _SCAN_GRAD(*_scan_sizes(*sizes), *[0] * 13))
 
 
 def selective_scan(u, delta, A, B, C, skip=None, z=None, delta_bias=None, softplus=False, offsets=None, max_len=None,
@@ -507,7 +515,7 @@ def selective_scan(u, delta, A, B, C, skip=None, z=None, delta_bias=None, softpl
     G, N, args = _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, slots, state, state_out, max_len, S,
                             L, False, index)
     D = shape[-1]
-    keep, n, _ = _scan_space(S, L, offsets is not None, D, G, N, args[8], max_len or 0)
+    keep, n = _scan_space(S, L, offsets is not None, D, G, N, args[8], max_len or 0)
     y = _same(u)
     saved = _empty(keep // 4, _f32, u) if save else None
     ws = _empty(n, torch.uint8, u) if n else None
@@ -552,7 +560,7 @@ def selective_scan_grad(dy, u, delta, A, B, C, saved, skip=None, z=None, delta_b
     G, N, args = _scan_args(u, delta, A, B, C, skip, z, delta_bias, softplus, offsets, slots, state, None, max_len, S, L,
                             False, index)
     D = shape[-1]
-    keep, _, n = _scan_space(S, L, offsets is not None, D, G, N, args[8], max_len or 0)
+    keep, n = _scan_grad_space(S, L, offsets is not None, D, G, N, args[8], max_len or 0)
     dys = _like(dy, "dy", shape, dtype, index)
     saved_ptr = _dense(saved, "saved", (keep // 4,), _f32, index)
     du, ddelta = _same(u), _same(u)

@@ -188,6 +188,16 @@ def test_scan_gradient_too_large_for_one_of_its_launches(tokens, channels, group
     assert lib.seq_selective_scan_grad_workspace(ctypes.byref(half), ctypes.byref(n)) == OK
 
 
+def test_a_forward_scan_needs_no_gradient_of_its_size():
+    """The Python call asks for the gradient's workspace only when it computes one."""
+    sizes = (1, (1 << 21) + 16, False, 4160, 1, 32, 1, 0)
+    saved, space = sq._scan_space(*sizes)
+    assert saved == ((1 << 17) + 1) * 4160 * 32 * 4 and space > 0
+    with pytest.raises(iga.ConvWgradError):
+        sq._scan_grad_space(*sizes)
+    assert sq._scan_grad_space(1, 1 << 20, *sizes[2:])[1] > 0
+
+
 def test_tensors_on_the_host_are_refused():
     x, w = torch.zeros(2, 8), torch.ones(8)
     with pytest.raises(ValueError):
