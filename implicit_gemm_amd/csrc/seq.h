@@ -9,6 +9,8 @@
 
 namespace cw {
 
+constexpr int64_t kMaxLanes = ((int64_t)1 << 32) - 1;   // of a launch
+
 // How tokens are cut into pieces (device side: find_piece).
 struct SeqMap {
   const int32_t* offsets;
@@ -65,6 +67,7 @@ hipError_t launch_scan_step(const seq_scan_args_t& a, hipStream_t stream);
 int64_t scan_grad_ws_floats(const seq_scan_grad_args_t& g);
 // Lanes of the largest launch of a call.
 int64_t scan_lanes(const seq_scan_args_t& a);
+int64_t scan_step_lanes(const seq_scan_args_t& a);
 int64_t scan_grad_lanes(const seq_scan_grad_args_t& g);
 hipError_t launch_scan_grad(const seq_scan_grad_args_t& a, float* ws, hipStream_t stream);
 

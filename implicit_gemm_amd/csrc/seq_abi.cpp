@@ -14,7 +14,7 @@ constexpr int64_t kMaxRows = (int64_t)1 << 30;       // tokens of a sequence, pa
 constexpr int64_t kMaxAll = (int64_t)1 << 40;        // rows of all sequences
 constexpr int64_t kMaxChannels = (int64_t)1 << 20;
 constexpr int64_t kMaxNorm = 16384;                  // channels of a norm: a row stays in registers
-constexpr int64_t kMaxLanes = ((int64_t)1 << 32) - 1;
+using cw::kMaxLanes;
 
 Status of(hipError_t err) { return err == hipSuccess ? CONV_WGRAD_OK : CONV_WGRAD_ERR_HIP; }
 bool bad_dtype(int32_t t) { return t != CONV_WGRAD_F32 && t != CONV_WGRAD_BF16 && t != CONV_WGRAD_F16; }
@@ -122,12 +122,7 @@ Status check_scan_shape(const seq_scan_args_t& a, bool step) {
     return CONV_WGRAD_ERR_BAD_SHAPE;
   if (step && (a.tokens.offsets || a.tokens.rows != 1)) return CONV_WGRAD_ERR_BAD_SHAPE;
   if (a.channels > kMaxChannels || a.states > 32 || !pieces_fit(a.tokens)) return CONV_WGRAD_ERR_UNSUPPORTED;
-  const int64_t blocks = (int64_t)cw::scan_blocks(a);
-  const int64_t pieces = seq_pieces(cw::seq_map(a.tokens, 6));
-  const int64_t padded = a.states <= 8 ? 8 : a.states <= 16 ? 16 : 32;
-  if (!fits(pieces, 64 * blocks) || !fits(a.tokens.sequences, 256 * a.states * ((a.channels + 63) / 64)) ||
-      !fits(a.tokens.sequences, 256 * ((a.channels * padded / 4 + 255) / 256)))
-    return CONV_WGRAD_ERR_UNSUPPORTED;
+  if ((step ? cw::scan_step_lanes(a) : cw::scan_lanes(a)) > kMaxLanes) return CONV_WGRAD_ERR_UNSUPPORTED;
   return CONV_WGRAD_OK;
 }
 

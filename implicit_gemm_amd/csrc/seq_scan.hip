@@ -413,11 +413,14 @@ hipError_t carry_t(const ScanArgs& k, bool back, hipStream_t stream) {
   return launch_kernel(scan_carry_kernel<T, NP, false>, grid, block, k, stream);
 }
 
+// Workgroups of the single-token kernel, `lanes` lanes a channel.
+int64_t step_grid(const seq_scan_args_t& a, int lanes) {
+  return (a.channels * lanes + 255) / 256 * a.tokens.sequences;
+}
+
 template <typename T, int NP, bool FULL>
 hipError_t step_t(const ScanArgs& k, hipStream_t stream) {
-  constexpr int kChannels = 256 / (NP / 4);
-  const int64_t grid = (k.a.channels + kChannels - 1) / kChannels * k.a.tokens.sequences;
-  return launch_kernel(scan_step_kernel<T, NP, FULL>, dim3((unsigned)grid), dim3(256), k, stream);
+  return launch_kernel(scan_step_kernel<T, NP, FULL>, dim3((unsigned)step_grid(k.a, NP / 4)), dim3(256), k, stream);
 }
 
 hipError_t scan_any(const ScanArgs& k, hipStream_t stream) {
@@ -439,6 +442,8 @@ static int64_t scan_longest(const seq_scan_args_t& a) {
   return a.tokens.offsets && a.longest > 0 && a.longest < a.tokens.rows ? a.longest : a.tokens.rows;
 }
 
+static int64_t join_groups(const seq_scan_args_t& a) { return (a.channels + 63) / 64 * a.states * a.tokens.sequences; }
+
 ScanCut scan_cut(const seq_scan_args_t& a) {
   const int64_t waves = scan_blocks(a), rows = seq_rows(a.tokens);
   const int64_t longest = scan_longest(a);
@@ -446,6 +451,8 @@ ScanCut scan_cut(const seq_scan_args_t& a) {
   while (shift < kWholeShift && (rows >> shift) * waves > kScanWaves) ++shift;
   const int64_t piece = (int64_t)1 << shift;
   if (longest <= (piece > kScanWhole ? piece : kScanWhole)) return ScanCut{kWholeShift, false};
+  // 2^24 sequences x channels / 64 x states: waves enough without a cut, and past what a launch of the join can hold.
+  if (join_groups(a) > kMaxLanes / 256) return ScanCut{kWholeShift, false};
   return ScanCut{shift, true};
 }
 
@@ -460,16 +467,17 @@ int64_t scan_ws_floats(const seq_scan_args_t& a) {
   return scan_round(pieces * a.channels * a.states) + scan_round(pieces * a.channels);
 }
 
-static int64_t join_groups(const seq_scan_args_t& a) { return (a.channels + 63) / 64 * a.states * a.tokens.sequences; }
 static bool join_few(const seq_scan_args_t& a, int shift) {
   return (scan_longest(a) >> shift) <= 2 * kJoinEach && join_groups(a) > 2048;
 }
 
+// The join has fewer than kMaxLanes: scan_cut.
 int64_t scan_lanes(const seq_scan_args_t& a) {
-  const ScanCut cut = scan_cut(a);
-  const int64_t pieces = scan_groups(seq_pieces(seq_map(a.tokens, cut.shift)), a) * 64 * kScanGroup;
-  const int64_t join = cut.split ? join_groups(a) * (join_few(a, cut.shift) ? 64 : 256) : 0;
-  return pieces > join ? pieces : join;
+  return scan_groups(seq_pieces(seq_map(a.tokens, scan_cut(a).shift)), a) * 64 * kScanGroup;
+}
+
+int64_t scan_step_lanes(const seq_scan_args_t& a) {
+  return step_grid(a, a.states <= 8 ? 2 : a.states <= 16 ? 4 : 8) * 256;
 }
 
 hipError_t launch_scan_carry(const ScanArgs& k, bool backward, hipStream_t stream) {

@@ -416,6 +416,38 @@ def test_scan_step_matches_prompt(iga, D, N, G, S, dtype):
     assert bool((other[:2] == 3).all())
 
 
+@pytest.mark.slow
+def test_scan_of_very_many_sequences(iga):
+    """2^14 sequences of 4096 channels x 16 states (a join of them would not fit a launch): a token of each, and packed
+    prompts of 0 .. 3 tokens, give what the two halves give, bit for bit."""
+    S, D, N = 1 << 14, 4096, 16
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=g, device="cuda", dtype=torch.bfloat16)
+
+    A, bias = -torch.rand(D, N, device="cuda") - 0.1, torch.full((D,), -1.0, device="cuda")
+    kw = dict(delta_bias=bias, softplus=True)
+    state = torch.randn(S, D, N, generator=g, device="cuda")
+    halves = (slice(0, S // 2), slice(S // 2, S))
+    u, B = rand(S, D), rand(S, 1, N)
+    new = torch.empty_like(state)
+    y = iga.selective_scan_step(u, u, A, B, B, state, state_out=new, **kw)
+    for h in halves:
+        part = torch.empty_like(state[h])
+        assert torch.equal(y[h], iga.selective_scan_step(u[h], u[h], A, B[h], B[h], state[h], state_out=part, **kw))
+        assert torch.equal(new[h], part)
+    lens = torch.arange(S, device="cuda") % 4
+    off = torch.cat([lens.new_zeros(1), lens.cumsum(0)]).int()
+    cut = int(off[S // 2])
+    u, B = rand(int(off[-1]), D), rand(int(off[-1]), 1, N)
+    y = iga.selective_scan(u, u, A, B, B, offsets=off, state=state, state_out=new, **kw)[0]
+    for h, r, o in ((halves[0], slice(0, cut), off[:S // 2 + 1]), (halves[1], slice(cut, None), off[S // 2:] - cut)):
+        part = torch.empty_like(state[h])
+        y2 = iga.selective_scan(u[r], u[r], A, B[r], B[r], offsets=o.int(), max_len=3, state=state[h], state_out=part, **kw)[0]
+        assert torch.equal(y[r], y2) and torch.equal(new[h], part)
+
+
 @pytest.mark.parametrize("split", [False, True])
 def test_scan_in_place_and_in_two_halves(iga, split):
     """A prompt in two calls, its state carried in place, gives the states of one call; sums are split elsewhere, so

@@ -188,6 +188,25 @@ def test_scan_gradient_too_large_for_one_of_its_launches(tokens, channels, group
     assert lib.seq_selective_scan_grad_workspace(ctypes.byref(half), ctypes.byref(n)) == OK
 
 
+def test_scan_is_refused_for_its_own_launches_only():
+    """The size of a join that many sequences do not have, or do not need, is no reason."""
+    n = ctypes.c_size_t(0)
+    lib = sq._lib()
+
+    def args(sequences, rows, offsets=None, A=P):
+        f = grad_of((sequences, rows), 4096, 1, 16).fwd
+        f.tokens.offsets, f.A = offsets, A
+        return ctypes.byref(f)
+
+    assert lib.seq_selective_scan_step(args(1 << 14, 1, A=0), None) == NULL           # its size passes
+    assert lib.seq_selective_scan_step(args(1 << 18, 1, A=0), None) == UNSUPPORTED
+    assert lib.seq_selective_scan_workspace(args(1 << 14, 64), ctypes.byref(n)) == OK and n.value == 0
+    # packed rows that would be split for a sequence of all of them: a join of 2^32 lanes, and the half of it
+    assert lib.seq_selective_scan_workspace(args(1 << 14, 1 << 20, P), ctypes.byref(n)) == OK and n.value == 0
+    assert lib.seq_selective_scan_workspace(args(1 << 13, 1 << 20, P), ctypes.byref(n)) == OK and n.value > 0
+    assert lib.seq_selective_scan_workspace(args(1 << 20, 1 << 20, P), ctypes.byref(n)) == UNSUPPORTED
+
+
 def test_a_forward_scan_needs_no_gradient_of_its_size():
     """The Python call asks for the gradient's workspace only when it computes one."""
     sizes = (1, (1 << 21) + 16, False, 4160, 1, 32, 1, 0)
