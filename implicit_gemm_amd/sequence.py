@@ -372,7 +372,8 @@ def causal_conv(x, w, b=None, silu=False, offsets=None, slots=None, state=None, 
 
     `state` [P, W - 1, D] (the element type) holds the W - 1 inputs before each sequence, oldest first; None: zeros.
     The windows after the last tokens go to state_out: a new tensor by default or, with slots, `state` itself; it may
-    be `state`, and must not overlap it otherwise."""
+    be `state`, and must not overlap it otherwise.  causal_conv_grad reads the windows before the sequences: for a
+    gradient give a state_out of its own, or keep a copy of `state`."""
     on = _here(x, stream)
     if on is None:
         return _there(x, stream, causal_conv, x, w, b, silu, offsets, slots, state, state_out)
@@ -417,7 +418,11 @@ def _conv_grad_space(S, L, packed, D, W, code):
 
 def causal_conv_grad(dy, x, w, b=None, silu=False, offsets=None, slots=None, state=None, dstate_out=None, stream=None):
     """Gradients of causal_conv: (dx, dw, db, dstate), db None without b and dstate [S, W - 1, D] None without state.
-    dstate_out [S, W - 1, D]: the gradient of the outgoing windows."""
+    dstate_out [S, W - 1, D]: the gradient of the outgoing windows.
+
+    `state` holds the windows as they were before causal_conv: where that wrote the new ones over them (with slots it
+    does unless told otherwise by state_out) dw and dx would be those of other inputs.  Give it a state_out of its own,
+    or a copy of `state` here."""
     on = _here(x, stream)
     if on is None:
         return _there(x, stream, causal_conv_grad, dy, x, w, b, silu, offsets, slots, state, dstate_out)

@@ -527,8 +527,9 @@ conv_wgrad_status_t seq_causal_conv(const seq_conv_args_t* args, void* stream);
 conv_wgrad_status_t seq_causal_conv_step(const seq_conv_args_t* args, void* stream);
 
 /* Gradients: dx, dw, dbias (NULL: not needed) and dstate (dense [sequences][width - 1][channels], NULL: not needed)
- * from dy and dstate_out (the same shape; gradient of the outgoing windows, NULL: zero).  fwd.y, fwd.state_out and
- * their strides are not read. */
+ * from dy and dstate_out (the same shape; gradient of the outgoing windows, NULL: zero).  fwd.state holds the windows as
+ * they were before the forward: a caller whose forward wrote state_out over them keeps a copy.  fwd.y, fwd.state_out
+ * and their strides are not read. */
 typedef struct seq_conv_grad_args {
   seq_conv_args_t fwd;
   seq_view_t dy;

@@ -255,6 +255,32 @@ def test_conv_gradient_of_an_empty_sequence_ignores_its_window(iga, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("keep", ["state_out", "copy", "copy in order"])
+def test_conv_gradient_beside_a_pool(iga, keep, dtype):
+    """The gradient reads the windows before the sequences, which a call with slots writes over: the ways of keeping them
+    that the two calls name, against the definition."""
+    rand, dt = gen(15), DT[dtype]
+    offsets, P, D, W = [0, 1, 8, 8, 60], 6, 70, 4
+    x, dy, w, b = rand(60, D, dtype=dt), rand(60, D, dtype=dt), rand(D, W, std=0.5), rand(D)
+    pool, slots = rand(P, W - 1, D, dtype=dt), torch.tensor([4, 0, 5, 2], dtype=torch.int32)
+    state, kw = pool.cuda(), dict(silu=True, offsets=torch.tensor(offsets, dtype=torch.int32).cuda())
+    xd, wd, bd, at = x.cuda(), w.cuda(), b.cuda(), slots.cuda()
+    if keep == "state_out":
+        iga.causal_conv(xd, wd, bd, slots=at, state=state, state_out=torch.empty_like(state), **kw)
+        got = iga.causal_conv_grad(dy.cuda(), xd, wd, bd, slots=at, state=state, **kw)
+    else:
+        before = state.clone() if keep == "copy" else state[at.long()]
+        _, new = iga.causal_conv(xd, wd, bd, slots=at, state=state, **kw)
+        assert new is state and not torch.equal(state, pool.cuda())
+        got = iga.causal_conv_grad(dy.cuda(), xd, wd, bd, state=before, slots=at if keep == "copy" else None, **kw)
+    leaves = [leaf(x), leaf(w), leaf(b), leaf(pool[slots.long()])]
+    yr, _ = ref.conv(*leaves[:3], True, offsets, leaves[3])
+    for name, g, e, t, c in zip(("dx", "dw", "db", "dstate"), got, ref.grads((yr,), (dy.double(),), leaves),
+                                (dt, torch.float32, torch.float32, dt), (64, 64 + 60, 64 + 60, 64)):
+        close(g, e, t, c, name)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("W,D,S", [(4, 300, 1), (4, 1030, 5), (2, 3, 4), (3, 64, 2)])
 def test_conv_step_matches_prompt(iga, W, D, S, dtype):
     """Tokens one at a time give the prompt's outputs bit for bit (the same sums in the same order) and its window."""

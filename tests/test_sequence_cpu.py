@@ -111,6 +111,12 @@ def test_conv_step_and_grad_refusals():
     assert lib.seq_causal_conv_grad(ctypes.byref(h), P, n.value, None) == MISALIGNED
 
 
+def test_conv_says_which_windows_its_gradient_reads():
+    """A call with slots writes the new windows over those that the gradient needs: each of the two calls says so."""
+    assert "causal_conv_grad reads the windows before" in iga.causal_conv.__doc__
+    assert "as they were before causal_conv" in iga.causal_conv_grad.__doc__
+
+
 def scan_args(**over):
     tokens = [2, 10, 0, 0, 2]
     for i, k in enumerate(("sequences", "rows", "offsets", "slots", "pool")):
