@@ -222,6 +222,17 @@ def test_conv_and_gradient(iga, W, D, act, offsets, tail, carried, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("W,D,act,offsets,tail", [
+    (4, 256, True, None, 0), (3, 512, False, None, 0), (2, 256, True, [0, 70, 70, 71, 180, 183], 9),
+    (4, 512, True, [0, 70, 70, 71, 180, 183], 9), (4, 128, True, [0, 33, 66, 67, 200], 0), (3, 256, True, [0, 1, 3, 130], 40)])
+@pytest.mark.parametrize("carried", [False, True])
+def test_conv_of_whole_channel_blocks(iga, W, D, act, offsets, tail, carried, dtype):
+    """The kernels without channel checks (blocks of 256 channels forward, 128 backward), over sequences of several pieces,
+    of one, and of none."""
+    test_conv_and_gradient(iga, W, D, act, offsets, tail, carried, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_conv_long_has_many_pieces_a_workgroup(iga, dtype):
     """More pieces than partial sums: each workgroup of the gradient walks along several."""
     rand, dt = gen(3), DT[dtype]
@@ -235,6 +246,23 @@ def test_conv_long_has_many_pieces_a_workgroup(iga, dtype):
     close(dx, exp[0], dt, 64, "dx")
     close(dw, exp[1], torch.float32, 2000, "dw")
     close(db, exp[2], torch.float32, 2000, "db")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_conv_of_long_pieces(iga, dtype):
+    """Enough tokens for pieces of 64, whose windows and gradients pass many batches; odd lengths end inside one."""
+    rand, dt = gen(4), DT[dtype]
+    S, L, D = 3, 90001, 8
+    x, dy, w, b = rand(S, L, D, dtype=dt), rand(S, L, D, dtype=dt), rand(D, 4, std=0.5), rand(D)
+    y, _ = iga.causal_conv(x.cuda(), w.cuda(), b.cuda(), silu=True)
+    dx, dw, db, _ = iga.causal_conv_grad(dy.cuda(), x.cuda(), w.cuda(), b.cuda(), silu=True)
+    xl, wl, bl = leaf(x), leaf(w), leaf(b)
+    yr, _ = ref.conv(xl, wl, bl, True, None, None)
+    exp = ref.grads((yr,), (dy.double(),), (xl, wl, bl))
+    close(y, yr, dt, 16, "y")
+    close(dx, exp[0], dt, 64, "dx")
+    close(dw, exp[1], torch.float32, 64 + S * L, "dw")
+    close(db, exp[2], torch.float32, 64 + S * L, "db")
 
 
 @pytest.mark.parametrize("dtype", TYPES)
@@ -402,6 +430,57 @@ def test_scan_and_gradient(iga, D, N, G, offsets, tail, opts, L, dtype):
         check_scan(c, run_scan(iga, c, max_len=max(longest, 1)), longest)
         y, _ = run_scan(iga, c, max_len=1, grad=False)      # a hint that is wrong changes nothing either
         check_scan(c, (y, run_scan(iga, c, grad=False)[1]), longest)
+
+
+# Long scans: a state forgets, so that its error comes from the tokens within its memory, 1 / (1 - e^(D A)) of the slowest
+# state: that many roundings, where they are fewer than the tokens.  Without softplus D is 0.01 and more, which makes it 125
+# at most, with a good part of every state handed from piece to piece.
+SLOW = ("skip", "z", "bias", "state", "last")
+
+
+def memory(c):
+    dt = c["delta"].double() + (c["bias"].double() if c["bias"] is not None else 0)
+    dt = torch.logaddexp(dt, torch.zeros_like(dt)) if c["softplus"] else dt
+    slow = (dt.amin(tuple(range(dt.dim() - 1)))[:, None] * -c["A"].double()).min()
+    return round(float(1 / -torch.expm1(-slow)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("D,N,G,S,L,opts", [
+    (24, 11, 1, 2, 1100, SLOW), (64, 16, 1, 1, 1030, SLOW),          # 69 and 65 pieces: the join takes another round
+    (64, 8, 1, 2, 300, SLOW), (128, 32, 1, 2, 150, SLOW), (128, 32, 2, 1, 100, ALL),   # whole blocks of channels and states
+    (64, 4, 64, 2, 1100, SLOW)])                                     # pieces of 64 tokens
+def test_long_scan_and_gradient(iga, D, N, G, S, L, opts, dtype):
+    log("long scan", D, N, G, S, L, dtype)
+    c = scan_case(D, N, G, None, 0, dtype, opts, D + N, L=L, S=S)
+    check_scan(c, run_scan(iga, c), min(L, memory(c)))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_wide_scan_and_gradient(iga, dtype):
+    """Pieces of 64 tokens, four tiles of the gradient, in whole blocks of channels."""
+    c = scan_case(4096, 8, 64, None, 0, dtype, SLOW, 5, L=1100, S=2)
+    check_scan(c, run_scan(iga, c), min(1100, memory(c)))
+
+
+@pytest.mark.parametrize("max_len", [None, 500, 1, 65])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_packed_scan_by_the_join_of_one_wave(iga, dtype, max_len):
+    """50 sequences x 3 channel blocks x 16 states are joined by a wave each, 32 pieces of the longest in two rounds, where
+    no sequence is known to be longer (500; 65, which is wrong, as is 1, with which none is split); else by four."""
+    offsets = [0]
+    for i in range(50):
+        offsets.append(offsets[-1] + {3: 500, 20: 257, 21: 256, 40: 273}.get(i, [0, 1, 15, 16, 17, 40][i % 6]))
+    c = scan_case(192, 16, 1, offsets, 11, dtype, SLOW, 6)
+    check_scan(c, run_scan(iga, c, max_len=max_len), min(500, memory(c)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("max_len", [1, 65])
+def test_scan_with_a_wrong_longest_length(iga, dtype, max_len):
+    """Outputs, states and gradients do not depend on max_len being right, in one piece (1) and split (65)."""
+    c = scan_case(40, 11, 2, [0, 300, 300, 301, 520], 7, dtype, SLOW, 7)
+    check_scan(c, run_scan(iga, c, max_len=max_len), min(300, memory(c)))
 
 
 @pytest.mark.parametrize("dtype", TYPES)
