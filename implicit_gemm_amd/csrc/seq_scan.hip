@@ -264,8 +264,7 @@ __global__ __launch_bounds__(64 * kScanGroup) void scan_carry_kernel(ScanArgs k)
 // The carry into every piece of a sequence, in place of the pieces' aggregates; a lane owns one channel and state.
 // WAVES waves take 16 consecutive pieces each, all their aggregates in registers after one wait for memory; what the
 // waves before pass on comes through LDS.  Four waves for the shortest wait, one where sequences have few pieces and the
-// workgroups fill the GPU more than once: 12 sequences of up to 29 pieces, 1536 channels x 16 states (4608 workgroups),
-// take 17 us with four and 12 with one; 3 sequences of 33 pieces, 387 x 11 (231 workgroups), 4.5 and 6.8.
+// workgroups fill the GPU by themselves (join_few).
 //
 // A decay is 2^x, x = A log2 e sum D, of a whole piece (or of sixteen).  Where A D is positive, states grow, and over a piece
 // by more than fp32 holds though the state itself stays small, or zero (inf x 0): so 2^x h is 2^(x/2) (2^(x/2) h), for x up
@@ -467,8 +466,13 @@ int64_t scan_ws_floats(const seq_scan_args_t& a) {
   return scan_round(pieces * a.channels * a.states) + scan_round(pieces * a.channels);
 }
 
+// One wave a workgroup: for sequences of up to 16 pieces, which are one wave's, and up to 32 where workgroups fill the GPU
+// by themselves.  us with one and with four (16 states): 16 pieces, 240 workgroups 4.2 and 3.7, 480 4.4 and 4.7, 1024 5.1 and
+// 6.3, 2048 7.3 and 10.5; 32 pieces, 768 8.2 and 6.8, 1152 8.2 and 7.7, 1536 8.6 and 9.1, 2048 9.2 and 10.1, but a whole
+// training step of that size 450.0 and 449.3; packed, up to 29 pieces, 4608 12 and 17; 64 pieces, 1024 11.6 and 8.8.
 static bool join_few(const seq_scan_args_t& a, int shift) {
-  return (scan_longest(a) >> shift) <= 2 * kJoinEach && join_groups(a) > 2048;
+  const int64_t pieces = ((scan_longest(a) - 1) >> shift) + 1;
+  return pieces <= kJoinEach || (pieces <= 2 * kJoinEach && join_groups(a) > 2048);
 }
 
 // The join has fewer than kMaxLanes: scan_cut.
