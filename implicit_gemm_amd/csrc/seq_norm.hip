@@ -138,9 +138,10 @@ __global__ __launch_bounds__(256) void norm_kernel(seq_norm_args_t a) {
           if (group == 0 ? c == 0 : c % group == 0) a.scale[row * nscale + (group ? c / group : 0)] = scale;
           float f[V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            f[i] = y[v][i] / scale;
-            f[i] = rough ? __builtin_amdgcn_fmed3f(f[i], -448.f, 448.f) : f[i];
+          for (int i = 0; i < V; ++i) f[i] = y[v][i] / scale;
+          if (__any(rough)) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = rough ? __builtin_amdgcn_fmed3f(f[i], -448.f, 448.f) : f[i];
           }
           uint32_t packed[V / 4];
 #pragma unroll
