@@ -330,7 +330,7 @@ __global__ __launch_bounds__(256, 4) void conv_grad_kernel(ConvGradArgs k) {
         rdy[i] = ndy[i];
       }
       if (u0 + B < inside) fetch(u0 + B);
-      if (u0 > 0 && u0 + B <= n && (p.t0 + u0 + B <= p.len || !g.dstate_out)) batch(u0, rx, rdy, std::false_type());
+      if (u0 > 0 && u0 + B <= n) batch(u0, rx, rdy, std::false_type());
       else batch(u0, rx, rdy, std::true_type());
     }
   }
@@ -452,7 +452,8 @@ hipError_t launch_conv_step(const seq_conv_args_t& a, hipStream_t stream) {
 #undef CALL
 }
 
-// Workgroups along the pieces, each with a partial of dw: 128 of them give a 4096-channel layer 2048 workgroups.
+// Workgroups along the pieces, four at a time and each with a partial of dw.  A layer of 4096 channels has 32 blocks of 128:
+// the 256 pieces of 16384 tokens give it 64 x 32 = 2048 workgroups, more tokens 8192 at most.
 int64_t conv_grad_parts(const seq_conv_grad_args_t& g) {
   const int64_t need = (seq_pieces(grad_map(g.fwd)) + 3) / 4;
   return need < 1 ? 1 : need < 256 ? need : 256;

@@ -1,7 +1,8 @@
 // Fixed-order sums of partial results: the last step of every gradient that is summed over tokens or channel blocks.
 // out[e] = sum_p part[p][e].  A workgroup of kCols x kGroups lanes owns kCols outputs; group g sums the partials g,
 // g + kGroups, ... with eight loads in flight, and the group sums are added in order through LDS.  Few partials
-// (<= 64) take 64 columns x 4 groups, many take 32 x 32: the longest chain of dependent loads stays at a few.
+// (<= 64) take 64 columns x 4 groups, or 256 x 4 beside a fold of many in the same launch; many take 32 x 32: the longest
+// chain of dependent loads stays at a few.
 #include "seq_common.h"
 
 namespace cw {
