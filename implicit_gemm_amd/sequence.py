@@ -349,12 +349,16 @@ def rms_norm_grad(dy, h, w, r, dh=None, stream=None):
 
 # --------------------------------------------------------------------------------------------------- convolution
 
+def _taps(w, D):
+    if w.dim() != 2 or w.shape[0] != D or w.shape[1] < 1:
+        raise ValueError("w must be [%d, taps], got shape %s" % (D, tuple(w.shape)))
+    return w.shape[1]
+
+
 def _conv_args(x, xs, S, L, w, b, silu, offsets, slots, state, state_out, index):
     """(taps, the arguments of seq_conv_args_t up to y); xs: (batch, row) strides of x."""
     D = x.shape[-1]
-    if w.dim() != 2 or w.shape[0] != D:
-        raise ValueError("w must be [%d, taps], got shape %s" % (D, tuple(w.shape)))
-    W = w.shape[1]
+    W = _taps(w, D)
     slot_ptr, P, states = _pool(state, state_out, slots, S, (W - 1, D), x.dtype, index)
     return W, (S, L, _dense(offsets, "offsets", (S + 1,), torch.int32, index), slot_ptr, P, D, W, _code(x), bool(silu), 0,
                x.data_ptr(), *xs, _dense(w, "w", (D, W), _f32, index), _dense(b, "b", (D,), _f32, index), *states)
@@ -380,7 +384,7 @@ def causal_conv(x, w, b=None, silu=False, offsets=None, slots=None, state=None, 
     index = x.get_device()
     S, L = _sequences(x, offsets, "x")
     shape = x.shape
-    state_out = _default_out(state_out, slots, state, S, (w.shape[-1] - 1, shape[-1]), x.dtype, x)
+    state_out = _default_out(state_out, slots, state, S, (_taps(w, shape[-1]) - 1, shape[-1]), x.dtype, x)
     _, args = _conv_args(x, _strides(x, "x", offsets, index), S, L, w, b, silu, offsets, slots, state, state_out, index)
     y = _same(x)
     D = shape[-1]

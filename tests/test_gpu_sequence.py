@@ -673,6 +673,16 @@ def test_scan_refusals(iga):
             bad()
 
 
+def test_conv_refuses_its_filters_before_it_allocates(iga):
+    x = torch.zeros(1, 2, 1 << 15).cuda()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    for w in (torch.zeros(1 << 15).cuda(), torch.tensor(1.0).cuda(), torch.zeros(4, 1 << 15).cuda(), torch.zeros(1 << 15, 0).cuda()):
+        with pytest.raises(ValueError):
+            iga.causal_conv(x, w)
+    assert torch.cuda.max_memory_allocated() <= before + (1 << 20)
+
+
 # ------------------------------------------------------------------------------------------------ streams, graphs
 
 def test_on_another_stream(iga):
