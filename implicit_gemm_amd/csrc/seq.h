@@ -51,6 +51,10 @@ hipError_t launch_norm(const seq_norm_args_t& a, bool e4m3, hipStream_t stream);
 int norm_grad_parts(const seq_norm_grad_args_t& a);
 hipError_t launch_norm_grad(const seq_norm_grad_args_t& a, float* ws, hipStream_t stream);
 
+hipError_t launch_layer_norm(const seq_layer_norm_args_t& a, hipStream_t stream);
+int layer_norm_grad_parts(const seq_layer_norm_grad_args_t& a);
+hipError_t launch_layer_norm_grad(const seq_layer_norm_grad_args_t& a, float* ws, hipStream_t stream);
+
 hipError_t launch_conv(const seq_conv_args_t& a, hipStream_t stream);
 hipError_t launch_conv_step(const seq_conv_args_t& a, hipStream_t stream);
 int64_t conv_grad_parts(const seq_conv_grad_args_t& a);

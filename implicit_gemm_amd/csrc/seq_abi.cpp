@@ -64,6 +64,34 @@ Status check_norm_grad(const seq_norm_grad_args_t* a) {
   return CONV_WGRAD_OK;
 }
 
+// ---- layer norm ---------------------------------------------------------------------------------------------------
+Status check_layer_norm(const seq_layer_norm_args_t* a) {
+  if (!a) return CONV_WGRAD_ERR_NULL_ARG;
+  if (bad_dtype(a->dtype)) return CONV_WGRAD_ERR_BAD_DTYPE;
+  if (a->rows < 0 || a->channels < 1 || a->x_row < 0 || a->residual_row < 0 || !(a->eps >= 0.f))
+    return CONV_WGRAD_ERR_BAD_SHAPE;
+  if (a->channels > kMaxNorm || a->rows >= kMaxAll) return CONV_WGRAD_ERR_UNSUPPORTED;
+  if (a->rows && (!a->x || !a->w || !a->y || (a->h && !a->residual))) return CONV_WGRAD_ERR_NULL_ARG;
+  const int64_t e = elem(a->dtype);
+  if (off(a->x, e) || off(a->residual, e) || off(a->h, e) || off(a->y, e) || off(a->w, 4) || off(a->b, 4) ||
+      off(a->mean, 4) || off(a->rstd, 4))
+    return CONV_WGRAD_ERR_MISALIGNED;
+  return CONV_WGRAD_OK;
+}
+
+Status check_layer_norm_grad(const seq_layer_norm_grad_args_t* a) {
+  if (!a) return CONV_WGRAD_ERR_NULL_ARG;
+  if (bad_dtype(a->dtype)) return CONV_WGRAD_ERR_BAD_DTYPE;
+  if (a->rows < 0 || a->channels < 1 || a->dy_row < 0 || a->h_row < 0 || a->dh_row < 0)
+    return CONV_WGRAD_ERR_BAD_SHAPE;
+  if (a->channels > kMaxNorm || a->rows >= kMaxAll) return CONV_WGRAD_ERR_UNSUPPORTED;
+  return CONV_WGRAD_OK;
+}
+
+uint64_t layer_norm_grad_floats(const seq_layer_norm_grad_args_t& a) {
+  return (uint64_t)cw::layer_norm_grad_parts(a) * 2 * a.channels;
+}
+
 // ---- convolution --------------------------------------------------------------------------------------------------
 Status check_conv(const seq_conv_args_t& a, bool step) {
   const Status st = check_tokens(a.tokens);
@@ -206,6 +234,32 @@ conv_wgrad_status_t seq_rms_norm_grad(const seq_norm_grad_args_t* args, void* wo
   st = check_space(workspace, ws_bytes, (uint64_t)cw::norm_grad_parts(a) * a.channels);
   if (st != CONV_WGRAD_OK) return st;
   return of(cw::launch_norm_grad(a, static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+conv_wgrad_status_t seq_layer_norm(const seq_layer_norm_args_t* args, void* stream) {
+  const Status st = check_layer_norm(args);
+  return st != CONV_WGRAD_OK ? st : of(cw::launch_layer_norm(*args, static_cast<hipStream_t>(stream)));
+}
+
+conv_wgrad_status_t seq_layer_norm_grad_workspace(const seq_layer_norm_grad_args_t* args, size_t* bytes) {
+  if (!bytes) return CONV_WGRAD_ERR_NULL_ARG;
+  const Status st = check_layer_norm_grad(args);
+  return size_of(st, st == CONV_WGRAD_OK ? layer_norm_grad_floats(*args) : 0, bytes);
+}
+
+conv_wgrad_status_t seq_layer_norm_grad(const seq_layer_norm_grad_args_t* args, void* workspace, size_t ws_bytes,
+                                        void* stream) {
+  Status st = check_layer_norm_grad(args);
+  if (st != CONV_WGRAD_OK) return st;
+  const seq_layer_norm_grad_args_t& a = *args;
+  if (!a.w || !a.dw || (a.rows && (!a.dy || !a.h || !a.mean || !a.rstd || !a.dx))) return CONV_WGRAD_ERR_NULL_ARG;
+  const int64_t e = elem(a.dtype);
+  if (off(a.dy, e) || off(a.h, e) || off(a.dh, e) || off(a.dx, e) || off(a.w, 4) || off(a.mean, 4) || off(a.rstd, 4) ||
+      off(a.dw, 4) || off(a.db, 4))
+    return CONV_WGRAD_ERR_MISALIGNED;
+  st = check_space(workspace, ws_bytes, layer_norm_grad_floats(a));
+  if (st != CONV_WGRAD_OK) return st;
+  return of(cw::launch_layer_norm_grad(a, static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
 conv_wgrad_status_t seq_causal_conv(const seq_conv_args_t* args, void* stream) {

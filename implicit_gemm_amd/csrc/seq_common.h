@@ -146,6 +146,23 @@ __device__ __forceinline__ float lanes_reduce(float v, int n) {
   return v;
 }
 
+// Combines the values of a team of TEAM lanes (16 or 64: part of a wave or a whole one; more: the waves of a workgroup,
+// all of which call it, with TEAM / 64 floats of lds).
+template <class Op, int TEAM>
+__device__ __forceinline__ float team_reduce(float v, float* lds) {
+  v = lanes_reduce<Op>(v, TEAM < 64 ? TEAM : 64);
+  if constexpr (TEAM > 64) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();  // the last reduction's reads are done
+    if ((threadIdx.x & 63) == 0) lds[w] = v;
+    __syncthreads();
+    v = lds[0];
+#pragma unroll
+    for (int i = 1; i < TEAM / 64; ++i) v = Op::of(v, lds[i]);
+  }
+  return v;
+}
+
 // Orders a wave's LDS accesses before and after it.  The LDS serves one wave's accesses in order, so this costs nothing.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

@@ -1,0 +1,302 @@
+// Layer norm with the residual's addition, and its gradient (gfx950).
+//
+//   h = x + residual (rounded: the next layer reads it back), m = mean(h), r = 1 / sqrt(mean((h - m)^2) + eps)
+//   y = (h - m) r w + b
+//   with n = (h - m) r and g = dy w:  dx = r (g - mean(g) - n mean(g n)) + dh,  dw = sum dy n,  db = sum dy over rows
+//
+// Both are bound by HBM: a row is read once, kept in registers between its reductions and its outputs, and written once.
+// The squares are summed about the mean, from the registers, so that a mean far above the deviation costs no bits.  A
+// row belongs to a team of 16 lanes (four rows a wave: feature maps of few channels), of 64, of 256, or of 1024 for the
+// widest gradients; each lane holds up to 64 elements in 16-byte vectors, and a team of at most a wave needs no barrier.
+#include "seq_common.h"
+
+namespace cw {
+
+namespace {
+
+template <typename T, int TEAM, int NE>
+__global__ __launch_bounds__(256) void layer_norm_kernel(seq_layer_norm_args_t a) {
+  constexpr int V = 16 / sizeof(T), NV = NE / V, kTeams = 256 / TEAM;
+  __shared__ float lds[4];
+  const int lane = threadIdx.x % TEAM;
+  const int C = (int)a.channels;
+  for (int64_t row = (int64_t)blockIdx.x * kTeams + threadIdx.x / TEAM; row < a.rows; row += (int64_t)gridDim.x * kTeams) {
+    const T* x = static_cast<const T*>(a.x) + row * a.x_row;
+    Raw<T, V> raw[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TEAM + lane) * V;
+      if (c < C) raw[v].load_n(x + c, C - c);
+      else raw[v].clear();
+    }
+    if (a.residual) {
+      const T* p = static_cast<const T*>(a.residual) + row * a.residual_row;
+      Raw<T, V> res[NV];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int c = (v * TEAM + lane) * V;
+        if (c < C) res[v].load_n(p + c, C - c);
+        else res[v].clear();
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        float s[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = raw[v].get(i) + res[v].get(i);
+        raw[v].pack(s);
+      }
+      if (a.h) {
+        T* h = static_cast<T*>(a.h) + row * C;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const int c = (v * TEAM + lane) * V;
+          if (c < C) raw[v].store_n(h + c, C - c);
+        }
+      }
+    }
+    float sum = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += raw[v].get(i);
+    const float mean = team_reduce<AddOp, TEAM>(sum, lds) / (float)C;
+    float ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int n = C - (v * TEAM + lane) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float d = i < n ? raw[v].get(i) - mean : 0.f;
+        ss = __builtin_fmaf(d, d, ss);
+      }
+    }
+    const float r = 1.f / sqrtf(team_reduce<AddOp, TEAM>(ss, lds) / (float)C + a.eps);
+    if (lane == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = r;
+    }
+    T* y = static_cast<T*>(a.y) + row * C;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TEAM + lane) * V;
+      if (c < C) {
+        Raw<float, V> w, b;
+        w.load_n(a.w + c, C - c);
+        b.clear();
+        if (a.b) b.load_n(a.b + c, C - c);
+        Raw<T, V> o;
+        float s[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = __builtin_fmaf((raw[v].get(i) - mean) * r, w.get(i), b.get(i));
+        o.pack(s);
+        o.store_n(y + c, C - c);
+      }
+    }
+  }
+}
+
+struct LayerNormGradArgs {
+  seq_layer_norm_grad_args_t a;
+  float* part;   // [gridDim.x][2][channels]: partial sums of dw and db
+};
+
+template <typename T, int TEAM, int NE>
+__global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_grad_kernel(LayerNormGradArgs args) {
+  constexpr int V = 16 / sizeof(T), NV = NE / V, kThreads = TEAM > 256 ? TEAM : 256, kTeams = kThreads / TEAM;
+  __shared__ float lds[TEAM > 64 ? TEAM / 64 : 2 * TEAM * NE];
+  const seq_layer_norm_grad_args_t& a = args.a;
+  const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+  const int C = (int)a.channels;
+  float w[NV][V], accw[NV][V], accb[NV][V];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * TEAM + lane) * V;
+    Raw<float, V> t;
+    t.clear();
+    if (c < C) t.load_n(a.w + c, C - c);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      w[v][i] = t.get(i);
+      accw[v][i] = accb[v][i] = 0.f;
+    }
+  }
+  for (int64_t row = (int64_t)blockIdx.x * kTeams + team; row < a.rows; row += (int64_t)gridDim.x * kTeams) {
+    const T* pdy = static_cast<const T*>(a.dy) + row * a.dy_row;
+    const T* ph = static_cast<const T*>(a.h) + row * a.h_row;
+    const T* pdh = static_cast<const T*>(a.dh) + row * a.dh_row;
+    Raw<T, V> dy[NV], h[NV], dh[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TEAM + lane) * V;
+      dy[v].clear();
+      h[v].clear();
+      dh[v].clear();
+      if (c < C) {
+        dy[v].load_n(pdy + c, C - c);
+        h[v].load_n(ph + c, C - c);
+        if (a.dh) dh[v].load_n(pdh + c, C - c);
+      }
+    }
+    const float mean = a.mean[row], r = a.rstd[row];
+    // Channels past the end have dy = w = 0; their n is a number that no output takes.
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float g = dy[v].get(i) * w[v][i];
+        s1 += g;
+        s2 = __builtin_fmaf(g, h[v].get(i) - mean, s2);
+      }
+    s1 = team_reduce<AddOp, TEAM>(s1, lds) / (float)C;
+    s2 = team_reduce<AddOp, TEAM>(s2, lds) * r / (float)C;
+    T* dx = static_cast<T*>(a.dx) + row * C;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * TEAM + lane) * V;
+      Raw<T, V> o;
+      float s[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float d = dy[v].get(i), n = (h[v].get(i) - mean) * r;
+        s[i] = __builtin_fmaf(r, __builtin_fmaf(d, w[v][i], -s1) - n * s2, dh[v].get(i));
+        accw[v][i] = __builtin_fmaf(d, n, accw[v][i]);
+        accb[v][i] += d;
+      }
+      o.pack(s);
+      if (c < C) o.store_n(dx + c, C - c);
+    }
+  }
+  float* part = args.part + (int64_t)blockIdx.x * 2 * C;
+  if constexpr (kTeams > 1) {
+    // The teams' sums are added in order through LDS.
+    for (int q = 0; q < kTeams; ++q) {
+      if (team == q) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float& sw = lds[(v * V + i) * TEAM + lane];
+            float& sb = lds[TEAM * NE + (v * V + i) * TEAM + lane];
+            accw[v][i] += q ? sw : 0.f;
+            accb[v][i] += q ? sb : 0.f;
+            sw = accw[v][i];
+            sb = accb[v][i];
+          }
+      }
+      __syncthreads();
+    }
+    if (team != kTeams - 1) return;
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) {
+    const int c = (v * TEAM + lane) * V;
+    Raw<float, V> ow, ob;
+    ow.pack(accw[v]);
+    ob.pack(accb[v]);
+    if (c < C) {
+      ow.store_n(part + c, C - c);
+      ob.store_n(part + C + c, C - c);
+    }
+  }
+}
+
+constexpr int64_t kNarrow = 512;   // channels of a row that 16 lanes take
+template <typename T>
+constexpr bool by_wave(int64_t C) { return C * (int64_t)sizeof(T) <= 4096; }
+
+template <typename T>
+hipError_t layer_norm_t(const seq_layer_norm_args_t& a, hipStream_t stream) {
+  const int64_t C = a.channels;
+  const bool narrow = C <= kNarrow && a.rows >= 4096, wave = by_wave<T>(C) && a.rows >= 1024;
+  const int64_t teams = narrow ? 16 : wave ? 4 : 1;
+  const int64_t most = 1 << 20;
+  const int64_t blocks = (a.rows + teams - 1) / teams;
+  const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(256);
+  if (narrow) {
+    if (C <= 16 * 8) return launch_kernel(layer_norm_kernel<T, 16, 8>, grid, block, a, stream);
+    if (C <= 16 * 16) return launch_kernel(layer_norm_kernel<T, 16, 16>, grid, block, a, stream);
+    if (C <= 16 * 24) return launch_kernel(layer_norm_kernel<T, 16, 24>, grid, block, a, stream);
+    return launch_kernel(layer_norm_kernel<T, 16, 32>, grid, block, a, stream);
+  }
+  if (wave) {
+    if (C <= 64 * 8) return launch_kernel(layer_norm_kernel<T, 64, 8>, grid, block, a, stream);
+    if constexpr (sizeof(T) == 2) {
+      if (C > 64 * 16) return launch_kernel(layer_norm_kernel<T, 64, 32>, grid, block, a, stream);
+    }
+    return launch_kernel(layer_norm_kernel<T, 64, 16>, grid, block, a, stream);
+  }
+  if (C <= 256 * 8) return launch_kernel(layer_norm_kernel<T, 256, 8>, grid, block, a, stream);
+  if (C <= 256 * 16) return launch_kernel(layer_norm_kernel<T, 256, 16>, grid, block, a, stream);
+  if (C <= 256 * 32) return launch_kernel(layer_norm_kernel<T, 256, 32>, grid, block, a, stream);
+  return launch_kernel(layer_norm_kernel<T, 256, 64>, grid, block, a, stream);
+}
+
+bool grad_narrow(const seq_layer_norm_grad_args_t& a) { return a.channels <= kNarrow && a.rows >= 4096; }
+bool grad_by_wave(const seq_layer_norm_grad_args_t& a) {
+  return a.dtype == CONV_WGRAD_F32 ? by_wave<float>(a.channels) : by_wave<Bf16>(a.channels);
+}
+
+template <typename T>
+hipError_t layer_norm_grad_t(const seq_layer_norm_grad_args_t& a, float* ws, hipStream_t stream) {
+  const int64_t C = a.channels;
+  const LayerNormGradArgs k{a, ws};
+  const dim3 grid((unsigned)layer_norm_grad_parts(a)), block(256);
+  if (grad_narrow(a)) {
+    if (C <= 16 * 8) return launch_kernel(layer_norm_grad_kernel<T, 16, 8>, grid, block, k, stream);
+    if (C <= 16 * 16) return launch_kernel(layer_norm_grad_kernel<T, 16, 16>, grid, block, k, stream);
+    if (C <= 16 * 24) return launch_kernel(layer_norm_grad_kernel<T, 16, 24>, grid, block, k, stream);
+    return launch_kernel(layer_norm_grad_kernel<T, 16, 32>, grid, block, k, stream);
+  }
+  if (by_wave<T>(C)) {
+    if (C <= 64 * 8) return launch_kernel(layer_norm_grad_kernel<T, 64, 8>, grid, block, k, stream);
+    if constexpr (sizeof(T) == 2) {
+      if (C > 64 * 16) return launch_kernel(layer_norm_grad_kernel<T, 64, 32>, grid, block, k, stream);
+    }
+    return launch_kernel(layer_norm_grad_kernel<T, 64, 16>, grid, block, k, stream);
+  }
+  if constexpr (sizeof(T) == 4) {
+    if (C <= 256 * 8) return launch_kernel(layer_norm_grad_kernel<T, 256, 8>, grid, block, k, stream);
+  }
+  if (C <= 256 * 16) return launch_kernel(layer_norm_grad_kernel<T, 256, 16>, grid, block, k, stream);
+  if (C <= 256 * 32) return launch_kernel(layer_norm_grad_kernel<T, 256, 32>, grid, block, k, stream);
+  return launch_kernel(layer_norm_grad_kernel<T, 1024, 16>, grid, dim3(1024), k, stream);
+}
+
+}  // namespace
+
+hipError_t launch_layer_norm(const seq_layer_norm_args_t& a, hipStream_t stream) {
+  if (a.rows == 0) return hipSuccess;
+  switch (a.dtype) {
+    case CONV_WGRAD_F32: return layer_norm_t<float>(a, stream);
+    case CONV_WGRAD_BF16: return layer_norm_t<Bf16>(a, stream);
+    default: return layer_norm_t<F16>(a, stream);
+  }
+}
+
+// Workgroups of the gradient, each with its own partial dw and db: as many as rows need, up to 2048 waves, or 4096 where
+// four share a row.
+int layer_norm_grad_parts(const seq_layer_norm_grad_args_t& a) {
+  const int64_t teams = grad_narrow(a) ? 16 : grad_by_wave(a) ? 4 : 1;
+  const int64_t need = (a.rows + teams - 1) / teams;
+  const int64_t most = teams == 1 ? 1024 : 512;
+  return (int)(need < 1 ? 1 : need < most ? need : most);
+}
+
+hipError_t launch_layer_norm_grad(const seq_layer_norm_grad_args_t& a, float* ws, hipStream_t stream) {
+  hipError_t err;
+  switch (a.dtype) {
+    case CONV_WGRAD_F32: err = layer_norm_grad_t<float>(a, ws, stream); break;
+    case CONV_WGRAD_BF16: err = layer_norm_grad_t<Bf16>(a, ws, stream); break;
+    default: err = layer_norm_grad_t<F16>(a, ws, stream); break;
+  }
+  if (err != hipSuccess) return err;
+  FoldList l;
+  const int parts = layer_norm_grad_parts(a);
+  l.n = a.db ? 2 : 1;
+  l.f[0] = FoldPart{ws, 2 * a.channels, parts, a.channels, a.dw, CONV_WGRAD_F32};
+  l.f[1] = FoldPart{ws + a.channels, 2 * a.channels, parts, a.channels, a.db, CONV_WGRAD_F32};
+  return launch_seq_fold(l, stream);
+}
+
+}  // namespace cw

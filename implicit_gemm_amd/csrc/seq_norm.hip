@@ -14,21 +14,6 @@ namespace cw {
 
 namespace {
 
-template <class Op, int TEAM>
-__device__ __forceinline__ float team_reduce(float v, float* lds) {
-  v = lanes_reduce<Op>(v, 64);
-  if constexpr (TEAM > 64) {
-    const int w = threadIdx.x >> 6;
-    __syncthreads();  // the last reduction's reads are done
-    if ((threadIdx.x & 63) == 0) lds[w] = v;
-    __syncthreads();
-    v = lds[0];
-#pragma unroll
-    for (int i = 1; i < TEAM / 64; ++i) v = Op::of(v, lds[i]);
-  }
-  return v;
-}
-
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);

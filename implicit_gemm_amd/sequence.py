@@ -58,6 +58,24 @@ class NormGradArgs(ctypes.Structure):
                 ("dx", ctypes.c_void_p), ("dw", ctypes.c_void_p)]
 
 
+class LayerNormArgs(ctypes.Structure):
+    """seq_layer_norm_args_t."""
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x", ctypes.c_void_p), ("x_row", ctypes.c_int64),
+                ("residual", ctypes.c_void_p), ("residual_row", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("b", ctypes.c_void_p), ("y", ctypes.c_void_p), ("h", ctypes.c_void_p), ("mean", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p)]
+
+
+class LayerNormGradArgs(ctypes.Structure):
+    """seq_layer_norm_grad_args_t."""
+    _fields_ = [("rows", ctypes.c_int64), ("channels", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("dy", ctypes.c_void_p), ("dy_row", ctypes.c_int64),
+                ("h", ctypes.c_void_p), ("h_row", ctypes.c_int64), ("dh", ctypes.c_void_p),
+                ("dh_row", ctypes.c_int64), ("w", ctypes.c_void_p), ("mean", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("dx", ctypes.c_void_p), ("dw", ctypes.c_void_p), ("db", ctypes.c_void_p)]
+
+
 class ConvArgs(ctypes.Structure):
     """seq_conv_args_t."""
     _fields_ = [("tokens", _Tokens), ("channels", ctypes.c_int64), ("width", ctypes.c_int32),
@@ -103,9 +121,9 @@ def _format(struct_type):
     return "".join(codes[t] if t in codes else _format(t) for _, t in struct_type._fields_)
 
 
-_NORM, _NORM_GRAD, _CONV, _CONV_GRAD, _SCAN, _SCAN_GRAD = (
+_NORM, _NORM_GRAD, _LAYER, _LAYER_GRAD, _CONV, _CONV_GRAD, _SCAN, _SCAN_GRAD = (
     struct.Struct("@" + _format(t)).pack
-    for t in (NormArgs, NormGradArgs, ConvArgs, ConvGradArgs, ScanArgs, ScanGradArgs))
+    for t in (NormArgs, NormGradArgs, LayerNormArgs, LayerNormGradArgs, ConvArgs, ConvGradArgs, ScanArgs, ScanGradArgs))
 
 _CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _f32 = torch.float32
@@ -118,12 +136,14 @@ def _lib():
     """The library with the argument types of the sequence entries."""
     lib = load()
     ptr, size = ctypes.c_void_p, ctypes.c_size_t
-    for name in ("seq_rms_norm", "seq_rms_norm_e4m3", "seq_causal_conv", "seq_causal_conv_step",
+    for name in ("seq_rms_norm", "seq_rms_norm_e4m3", "seq_layer_norm", "seq_causal_conv", "seq_causal_conv_step",
                  "seq_selective_scan_step"):
         getattr(lib, name).argtypes = [ptr, ptr]
-    for name in ("seq_rms_norm_grad", "seq_causal_conv_grad", "seq_selective_scan", "seq_selective_scan_grad"):
+    for name in ("seq_rms_norm_grad", "seq_layer_norm_grad", "seq_causal_conv_grad", "seq_selective_scan",
+                 "seq_selective_scan_grad"):
         getattr(lib, name).argtypes = [ptr, ptr, size, ptr]
-    for name in ("seq_rms_norm_grad_workspace", "seq_causal_conv_grad_workspace", "seq_selective_scan_save",
+    for name in ("seq_rms_norm_grad_workspace", "seq_layer_norm_grad_workspace", "seq_causal_conv_grad_workspace",
+                 "seq_selective_scan_save",
                  "seq_selective_scan_workspace", "seq_selective_scan_grad_workspace"):
         getattr(lib, name).argtypes = [ptr, ctypes.POINTER(size)]
     return lib
@@ -345,6 +365,57 @@ def rms_norm_grad(dy, h, w, r, dh=None, stream=None):
     if status:
         raise ConvWgradError(status, "rms_norm_grad")
     return dx, dw
+
+
+def layer_norm(x, w, b=None, residual=None, eps=1e-5, stream=None):
+    """y = (h - m) r w + b with h = x + residual, m = mean(h) and r = 1 / sqrt(mean((h - m)^2) + eps) over the last axis
+    of x [..., C]; returns (y, h, m, r).  h is rounded to the element type before the norm reads it and is x itself
+    without a residual; w, b [C] and m, r [...] are float32."""
+    on = _here(x, stream)
+    if on is None:
+        return _there(x, stream, layer_norm, x, w, b, residual, eps)
+    shape, index, code = x.shape, x.get_device(), _code(x)
+    rows, x_row = _rows(x, "x")
+    res, res_row, h_ptr, h = _residual(residual, x, index)
+    y, m, r = _same(x), _empty(shape[:-1], _f32, x), _empty(shape[:-1], _f32, x)
+    status = _lib().seq_layer_norm(
+        _LAYER(rows, shape[-1], code, eps, x.data_ptr(), x_row, res, res_row, _dense(w, "w", shape[-1:], _f32, index),
+               _dense(b, "b", shape[-1:], _f32, index), y.data_ptr(), h_ptr, m.data_ptr(), r.data_ptr()), on)
+    if status:
+        raise ConvWgradError(status, "layer_norm")
+    return y, h, m, r
+
+
+@functools.lru_cache(4096)
+def _layer_norm_grad_space(rows, C, code):
+    return _bytes("seq_layer_norm_grad_workspace", _LAYER_GRAD(rows, C, code, *[0] * 13))
+
+
+def layer_norm_grad(dy, h, w, m, r, dh=None, bias=True, stream=None):
+    """Gradients of layer_norm, from its h, m and r: (dx, dw, db), db None with bias false.  dx is the gradient of x and
+    of the residual alike; dh is the gradient that reaches h by another way (the residual stream behind it)."""
+    on = _here(h, stream)
+    if on is None:
+        return _there(h, stream, layer_norm_grad, dy, h, w, m, r, dh, bias)
+    shape, dtype, index, code = h.shape, h.dtype, h.get_device(), _code(h)
+    rows, h_row = _rows(h, "h")
+    C = shape[-1]
+    _like(dy, "dy", shape, dtype, index)
+    if dh is not None:
+        _like(dh, "dh", shape, dtype, index)
+    dx, dw = _same(h), _empty((C,), _f32, h)
+    db = _empty((C,), _f32, h) if bias else None
+    n = _layer_norm_grad_space(rows, C, code)
+    ws = _empty(n, torch.uint8, h)
+    status = _lib().seq_layer_norm_grad(
+        _LAYER_GRAD(rows, C, code, 0, dy.data_ptr(), _rows(dy, "dy")[1], h.data_ptr(), h_row,
+                    dh.data_ptr() if dh is not None else 0, _rows(dh, "dh")[1] if dh is not None else 0,
+                    _dense(w, "w", (C,), _f32, index), _dense(m, "m", shape[:-1], _f32, index),
+                    _dense(r, "r", shape[:-1], _f32, index), dx.data_ptr(), dw.data_ptr(),
+                    db.data_ptr() if bias else 0), ws.data_ptr(), n, on)
+    if status:
+        raise ConvWgradError(status, "layer_norm_grad")
+    return dx, dw, db
 
 
 # --------------------------------------------------------------------------------------------------- convolution

@@ -499,6 +499,62 @@ conv_wgrad_status_t seq_rms_norm_grad_workspace(const seq_norm_grad_args_t* args
 conv_wgrad_status_t seq_rms_norm_grad(const seq_norm_grad_args_t* args, void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * Layer norm:  y = (h - m) r w + b,  h = x + residual rounded to the element type,  m = mean(h),
+ * r = 1 / sqrt(mean((h - m)^2) + eps), per row.
+ *   x, residual : rows x channels (residual NULL: h = x); row strides in elements
+ *   w, b        : fp32 [channels]; b may be NULL (zeros)
+ *   y, h        : dense outputs; h may be NULL (not needed)
+ *   mean, rstd  : fp32 [rows] or NULL: m and r, which the gradient reads
+ * 1 <= channels <= 16384, rows >= 0.
+ */
+typedef struct seq_layer_norm_args {
+  int64_t rows, channels;
+  int32_t dtype;
+  float eps;
+  const void* x;
+  int64_t x_row;
+  const void* residual;
+  int64_t residual_row;
+  const float* w;
+  const float* b;
+  void* y;
+  void* h;
+  float* mean;
+  float* rstd;
+} seq_layer_norm_args_t;
+
+conv_wgrad_status_t seq_layer_norm(const seq_layer_norm_args_t* args, void* stream);
+
+/*
+ * Gradients of seq_layer_norm, with n = (h - m) r and g = dy w:
+ *   dx = r (g - mean(g) - n mean(g n)) + dh  (also the residual's gradient),  dw = sum over rows of dy n,
+ *   db = sum over rows of dy (NULL: not needed).  h, mean and rstd are the forward's (h = x without a residual).
+ *   dh : gradient that reaches h by another way, or NULL
+ *   workspace : 16-byte aligned, seq_layer_norm_grad_workspace bytes
+ */
+typedef struct seq_layer_norm_grad_args {
+  int64_t rows, channels;
+  int32_t dtype;
+  int32_t reserved;
+  const void* dy;
+  int64_t dy_row;
+  const void* h;
+  int64_t h_row;
+  const void* dh;
+  int64_t dh_row;
+  const float* w;
+  const float* mean;
+  const float* rstd;
+  void* dx;               /* [rows][channels] */
+  float* dw;              /* [channels] */
+  float* db;              /* [channels] */
+} seq_layer_norm_grad_args_t;
+
+conv_wgrad_status_t seq_layer_norm_grad_workspace(const seq_layer_norm_grad_args_t* args, size_t* bytes);
+conv_wgrad_status_t seq_layer_norm_grad(const seq_layer_norm_grad_args_t* args, void* workspace, size_t ws_bytes,
+                                        void* stream);
+
+/*
  * Short causal convolution, one filter of `width` taps per channel:
  *   p[t, d] = bias[d] + sum_k w[d, k] x[t - (width - 1) + k, d],   y = p  or, with silu, p / (1 + e^-p).
  * Before a sequence's first token x is its state: [pool][width - 1][channels], the last width - 1 inputs, oldest first
