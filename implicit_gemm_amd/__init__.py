@@ -447,7 +447,7 @@ def wgrad(x, dy, R, S, pad=0, stride=1, dilation=1, groups=1, split_k=-1, dw=Non
 
 _SEQUENCE = ("rms_norm", "rms_norm_e4m3", "rms_norm_grad", "layer_norm", "layer_norm_grad", "causal_conv",
              "causal_conv_step", "causal_conv_grad", "selective_scan", "selective_scan_step", "selective_scan_grad",
-             "ScanGrads")
+             "ScanGrads", "gated_delta", "gated_delta_step", "gated_delta_grad", "DeltaGrads")
 
 
 def __getattr__(name):

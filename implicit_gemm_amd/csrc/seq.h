@@ -75,4 +75,15 @@ int64_t scan_step_lanes(const seq_scan_args_t& a);
 int64_t scan_grad_lanes(const seq_scan_grad_args_t& g);
 hipError_t launch_scan_grad(const seq_scan_grad_args_t& a, float* ws, hipStream_t stream);
 
+int64_t delta_save_floats(const seq_delta_args_t& a);
+int64_t delta_chunk_floats(const seq_delta_args_t& a);
+hipError_t launch_delta(const seq_delta_args_t& a, float* ws, hipStream_t stream);
+hipError_t launch_delta_step(const seq_delta_args_t& a, hipStream_t stream);
+int64_t delta_grad_ws_floats(const seq_delta_grad_args_t& g);
+// Lanes of the largest launch of a call.
+int64_t delta_lanes(const seq_delta_args_t& a);
+int64_t delta_step_lanes(const seq_delta_args_t& a);
+int64_t delta_grad_lanes(const seq_delta_grad_args_t& g);
+hipError_t launch_delta_grad(const seq_delta_grad_args_t& g, float* ws, hipStream_t stream);
+
 }  // namespace cw

@@ -190,6 +190,61 @@ Status check_scan_grad(const seq_scan_grad_args_t* g) {
   return cw::scan_grad_lanes(*g) <= kMaxLanes ? CONV_WGRAD_OK : CONV_WGRAD_ERR_UNSUPPORTED;
 }
 
+// ---- gated delta rule -----------------------------------------------------------------------------------------------
+// The sizes and strides that every entry reads.
+Status check_delta_shape(const seq_delta_args_t& a, bool step) {
+  const Status st = check_tokens(a.tokens);
+  if (st != CONV_WGRAD_OK) return st;
+  if (bad_dtype(a.dtype)) return CONV_WGRAD_ERR_BAD_DTYPE;
+  if (a.heads < 1 || a.key_heads < 1 || a.heads % a.key_heads || a.key_dim < 1 || a.value_dim < 1 || negative(a.q) ||
+      negative(a.k) || negative(a.v) || negative(a.g) || negative(a.beta) || a.q_head < 0 || a.k_head < 0 || a.v_head < 0 ||
+      a.state_stride < 0 || a.state_out_stride < 0)
+    return CONV_WGRAD_ERR_BAD_SHAPE;
+  if (step && (a.tokens.offsets || a.tokens.rows != 1)) return CONV_WGRAD_ERR_BAD_SHAPE;
+  if (a.heads > 65536 || a.key_dim > 256 || a.value_dim > 1024 || !pieces_fit(a.tokens)) return CONV_WGRAD_ERR_UNSUPPORTED;
+  // the offsets of a chunk's 64 rows are 32 bits in the kernels, in bytes, for inputs and for dense outputs
+  const int64_t most = (int64_t)1 << 24;
+  for (const seq_view_t* v : {&a.q, &a.k, &a.v})
+    if (v->row >= most) return CONV_WGRAD_ERR_UNSUPPORTED;
+  if (a.heads * a.value_dim >= most || a.key_heads * a.key_dim >= most) return CONV_WGRAD_ERR_UNSUPPORTED;
+  // a state's heads start at 64-bit offsets; the workspace's sizes have to stay far from overflowing 64 bits
+  if (seq_rows(a.tokens) > kMaxAll / 64 || seq_pieces(cw::seq_map(a.tokens, 6)) > ((int64_t)1 << 31) / a.heads)
+    return CONV_WGRAD_ERR_UNSUPPORTED;
+  return (step ? cw::delta_step_lanes(a) : cw::delta_lanes(a)) <= kMaxLanes ? CONV_WGRAD_OK : CONV_WGRAD_ERR_UNSUPPORTED;
+}
+
+Status check_delta_inputs(const seq_delta_args_t& a) {
+  if (seq_rows(a.tokens) && (!a.q.ptr || !a.k.ptr || !a.v.ptr || !a.g.ptr || !a.beta.ptr)) return CONV_WGRAD_ERR_NULL_ARG;
+  const int64_t e = elem(a.dtype);
+  if (off(a.q.ptr, e) || off(a.k.ptr, e) || off(a.v.ptr, e) || off(a.g.ptr, 4) || off(a.beta.ptr, 4) || off(a.save, 16))
+    return CONV_WGRAD_ERR_MISALIGNED;
+  return CONV_WGRAD_OK;
+}
+
+Status check_delta_forward(const seq_delta_args_t* a, bool step) {
+  if (!a) return CONV_WGRAD_ERR_NULL_ARG;
+  Status st = check_delta_shape(*a, step);
+  if (st == CONV_WGRAD_OK) st = check_delta_inputs(*a);
+  if (st != CONV_WGRAD_OK) return st;
+  if (negative(a->o)) return CONV_WGRAD_ERR_BAD_SHAPE;
+  if (a->o.row >= (int64_t)1 << 24) return CONV_WGRAD_ERR_UNSUPPORTED;
+  if (a->state_out && a->tokens.pool > 1 && a->state_out_stride < a->heads * a->key_dim * a->value_dim)
+    return CONV_WGRAD_ERR_BAD_SHAPE;
+  if (a->state && a->state == a->state_out && a->state_stride != a->state_out_stride) return CONV_WGRAD_ERR_BAD_SHAPE;
+  if (seq_rows(a->tokens) && !a->o.ptr) return CONV_WGRAD_ERR_NULL_ARG;
+  if (off(a->o.ptr, elem(a->dtype)) || off(a->state, 4) || off(a->state_out, 4)) return CONV_WGRAD_ERR_MISALIGNED;
+  return CONV_WGRAD_OK;
+}
+
+Status check_delta_grad(const seq_delta_grad_args_t* g) {
+  if (!g) return CONV_WGRAD_ERR_NULL_ARG;
+  const Status st = check_delta_shape(g->fwd, false);
+  if (st != CONV_WGRAD_OK) return st;
+  if (negative(g->dout) || g->dout_head < 0) return CONV_WGRAD_ERR_BAD_SHAPE;
+  if (g->dout.row >= (int64_t)1 << 24) return CONV_WGRAD_ERR_UNSUPPORTED;
+  return cw::delta_grad_lanes(*g) <= kMaxLanes ? CONV_WGRAD_OK : CONV_WGRAD_ERR_UNSUPPORTED;
+}
+
 Status check_space(const void* ws, size_t have, uint64_t floats) {
   if (floats == 0) return CONV_WGRAD_OK;
   if (!ws) return CONV_WGRAD_ERR_NULL_ARG;
@@ -339,6 +394,53 @@ conv_wgrad_status_t seq_selective_scan_grad(const seq_scan_grad_args_t* args, vo
   st = check_space(workspace, ws_bytes, (uint64_t)cw::scan_grad_ws_floats(g));
   if (st != CONV_WGRAD_OK) return st;
   return of(cw::launch_scan_grad(g, static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+conv_wgrad_status_t seq_gated_delta_save(const seq_delta_args_t* args, size_t* bytes) {
+  if (!args || !bytes) return CONV_WGRAD_ERR_NULL_ARG;
+  const Status st = check_delta_shape(*args, false);
+  return size_of(st, st == CONV_WGRAD_OK ? (uint64_t)cw::delta_save_floats(*args) : 0, bytes);
+}
+
+conv_wgrad_status_t seq_gated_delta_workspace(const seq_delta_args_t* args, size_t* bytes) {
+  if (!args || !bytes) return CONV_WGRAD_ERR_NULL_ARG;
+  const Status st = check_delta_shape(*args, false);
+  return size_of(st, st == CONV_WGRAD_OK ? (uint64_t)cw::delta_chunk_floats(*args) : 0, bytes);
+}
+
+conv_wgrad_status_t seq_gated_delta(const seq_delta_args_t* args, void* workspace, size_t ws_bytes, void* stream) {
+  Status st = check_delta_forward(args, false);
+  if (st == CONV_WGRAD_OK) st = check_space(workspace, ws_bytes, (uint64_t)cw::delta_chunk_floats(*args));
+  if (st != CONV_WGRAD_OK) return st;
+  return of(cw::launch_delta(*args, static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
+}
+
+conv_wgrad_status_t seq_gated_delta_step(const seq_delta_args_t* args, void* stream) {
+  const Status st = check_delta_forward(args, true);
+  return st != CONV_WGRAD_OK ? st : of(cw::launch_delta_step(*args, static_cast<hipStream_t>(stream)));
+}
+
+conv_wgrad_status_t seq_gated_delta_grad_workspace(const seq_delta_grad_args_t* args, size_t* bytes) {
+  if (!bytes) return CONV_WGRAD_ERR_NULL_ARG;
+  const Status st = check_delta_grad(args);
+  return size_of(st, st == CONV_WGRAD_OK ? (uint64_t)cw::delta_grad_ws_floats(*args) : 0, bytes);
+}
+
+conv_wgrad_status_t seq_gated_delta_grad(const seq_delta_grad_args_t* args, void* workspace, size_t ws_bytes,
+                                         void* stream) {
+  Status st = check_delta_grad(args);
+  if (st == CONV_WGRAD_OK) st = check_delta_inputs(args->fwd);
+  if (st != CONV_WGRAD_OK) return st;
+  const seq_delta_grad_args_t& g = *args;
+  if (seq_rows(g.fwd.tokens) && (!g.dout.ptr || !g.fwd.save || !g.dq || !g.dk || !g.dv || !g.dg || !g.dbeta))
+    return CONV_WGRAD_ERR_NULL_ARG;
+  const int64_t e = elem(g.fwd.dtype);
+  if (off(g.dout.ptr, e) || off(g.dq, e) || off(g.dk, e) || off(g.dv, e) || off(g.dg, 4) || off(g.dbeta, 4) ||
+      off(g.dstate, 4) || off(g.dstate_out, 4))
+    return CONV_WGRAD_ERR_MISALIGNED;
+  st = check_space(workspace, ws_bytes, (uint64_t)cw::delta_grad_ws_floats(g));
+  if (st != CONV_WGRAD_OK) return st;
+  return of(cw::launch_delta_grad(g, static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -108,8 +108,26 @@ class ScanGradArgs(ctypes.Structure):
                [(n, ctypes.c_void_p) for n in ("du", "ddelta", "dz", "dB", "dC", "dA", "dskip", "ddelta_bias", "dstate")]
 
 
+class DeltaArgs(ctypes.Structure):
+    """seq_delta_args_t."""
+    _fields_ = [("tokens", _Tokens), ("heads", ctypes.c_int64), ("key_heads", ctypes.c_int64),
+                ("key_dim", ctypes.c_int32), ("value_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("q", _View), ("k", _View), ("v", _View), ("q_head", ctypes.c_int64),
+                ("k_head", ctypes.c_int64), ("v_head", ctypes.c_int64), ("g", _View), ("beta", _View),
+                ("state", ctypes.c_void_p), ("state_stride", ctypes.c_int64), ("state_out", ctypes.c_void_p),
+                ("state_out_stride", ctypes.c_int64), ("save", ctypes.c_void_p), ("o", _View)]
+
+
+class DeltaGradArgs(ctypes.Structure):
+    """seq_delta_grad_args_t."""
+    _fields_ = [("fwd", DeltaArgs), ("dout", _View), ("dout_head", ctypes.c_int64), ("dstate_out", ctypes.c_void_p)] + \
+               [(n, ctypes.c_void_p) for n in ("dq", "dk", "dv", "dg", "dbeta", "dstate")]
+
+
 ScanGrads = namedtuple("ScanGrads", "du ddelta dA dB dC dskip dz ddelta_bias dstate")
 ScanGrads.__doc__ = """Gradients of selective_scan; None where the input was not given."""
+DeltaGrads = namedtuple("DeltaGrads", "dq dk dv dg dbeta dstate")
+DeltaGrads.__doc__ = """Gradients of gated_delta; dstate None without a state."""
 
 # A call on a few tokens takes a few microseconds on the GPU, so what the host does for it counts: arguments are packed
 # by one struct.pack, checks take one comparison of each property (a second function words the error), and workspace
@@ -121,9 +139,10 @@ def _format(struct_type):
     return "".join(codes[t] if t in codes else _format(t) for _, t in struct_type._fields_)
 
 
-_NORM, _NORM_GRAD, _LAYER, _LAYER_GRAD, _CONV, _CONV_GRAD, _SCAN, _SCAN_GRAD = (
+_NORM, _NORM_GRAD, _LAYER, _LAYER_GRAD, _CONV, _CONV_GRAD, _SCAN, _SCAN_GRAD, _DELTA, _DELTA_GRAD = (
     struct.Struct("@" + _format(t)).pack
-    for t in (NormArgs, NormGradArgs, LayerNormArgs, LayerNormGradArgs, ConvArgs, ConvGradArgs, ScanArgs, ScanGradArgs))
+    for t in (NormArgs, NormGradArgs, LayerNormArgs, LayerNormGradArgs, ConvArgs, ConvGradArgs, ScanArgs, ScanGradArgs,
+              DeltaArgs, DeltaGradArgs))
 
 _CODES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _f32 = torch.float32
@@ -137,14 +156,15 @@ def _lib():
     lib = load()
     ptr, size = ctypes.c_void_p, ctypes.c_size_t
     for name in ("seq_rms_norm", "seq_rms_norm_e4m3", "seq_layer_norm", "seq_causal_conv", "seq_causal_conv_step",
-                 "seq_selective_scan_step"):
+                 "seq_selective_scan_step", "seq_gated_delta_step"):
         getattr(lib, name).argtypes = [ptr, ptr]
     for name in ("seq_rms_norm_grad", "seq_layer_norm_grad", "seq_causal_conv_grad", "seq_selective_scan",
-                 "seq_selective_scan_grad"):
+                 "seq_selective_scan_grad", "seq_gated_delta", "seq_gated_delta_grad"):
         getattr(lib, name).argtypes = [ptr, ptr, size, ptr]
     for name in ("seq_rms_norm_grad_workspace", "seq_layer_norm_grad_workspace", "seq_causal_conv_grad_workspace",
                  "seq_selective_scan_save",
-                 "seq_selective_scan_workspace", "seq_selective_scan_grad_workspace"):
+                 "seq_selective_scan_workspace", "seq_selective_scan_grad_workspace", "seq_gated_delta_save",
+                 "seq_gated_delta_workspace", "seq_gated_delta_grad_workspace"):
         getattr(lib, name).argtypes = [ptr, ctypes.POINTER(size)]
     return lib
 
@@ -660,3 +680,163 @@ def selective_scan_grad(dy, u, delta, A, B, C, saved, skip=None, z=None, delta_b
     if status:
         raise ConvWgradError(status, "selective_scan_grad")
     return ScanGrads(du, ddelta, dA, dB, dC, dskip, dz, dbias, dstate)
+
+
+# --------------------------------------------------------------------------------------------------- gated delta rule
+
+def _delta_rows(v, offsets):
+    """(sequences, rows of each or in all) of [S, L, H, Dv], or of [T, H, Dv] with offsets."""
+    shape = v.shape
+    if offsets is None:
+        if len(shape) != 4:
+            raise ValueError("v must be [S, L, H, Dv] without offsets, got shape %s" % (tuple(shape),))
+        return shape[0], shape[1]
+    if len(shape) != 3:
+        raise ValueError("v must be [T, H, Dv] with offsets, got shape %s" % (tuple(shape),))
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must hold S + 1 >= 2 row numbers")
+    return offsets.shape[0] - 1, shape[0]
+
+
+def _delta_place(t, name, P, each, index):
+    """(pointer, stride between states) of a pool of P dense states [H, Dk, Dv]."""
+    if t.shape != (P,) + each or t.dtype is not _f32 or t.get_device() != index:
+        _refuse(t, name, (P,) + each, _f32, index)
+    outer, heads, rows, one = t.stride()
+    if (one != 1 and each[2] > 1) or (rows != each[2] and each[1] > 1) or (heads != each[1] * each[2] and each[0] > 1):
+        raise ValueError("each state of %s must be contiguous" % name)
+    return t.data_ptr(), outer
+
+
+def _delta_pool(state, state_out, slots, S, each, index):
+    """_pool for states of three axes."""
+    given = state if state is not None else state_out
+    P = S if given is None else given.shape[0] if given.dim() else 0
+    if P < 1:
+        raise ValueError("there must be at least one sequence and one state")
+    at = (0, 0) if state is None else _delta_place(state, "state", P, each, index)
+    to = at if state_out is state else (0, 0) if state_out is None else _delta_place(state_out, "state_out", P, each, index)
+    if slots is None:
+        if P != S:
+            raise ValueError("%d states for %d sequences: slots must say which" % (P, S))
+        return 0, P, at + to
+    return _dense(slots, "slots", (S,), torch.int32, index), P, at + to
+
+
+def _delta_args(q, k, v, g, beta, scale, offsets, slots, state, state_out, S, L, step, index):
+    """The arguments of seq_delta_args_t up to save."""
+    shape, dtype = v.shape, v.dtype
+    H, Dv = shape[-2:]
+    if q.dim() != len(shape) or q.shape[-2] < 1 or H % q.shape[-2]:
+        raise ValueError("q and k must be [..., key heads, Dk] with key heads dividing %d, got %s" % (H, tuple(q.shape)))
+    Hk, Dk = q.shape[-2:]
+    keys, flat = shape[:-2] + (Hk, Dk), shape[:-1]
+    qs, ks, vs = _like(q, "q", keys, dtype, index), _like(k, "k", keys, dtype, index), _like(v, "v", shape, dtype, index)
+    gs, bs = _like(g, "g", flat, _f32, index), _like(beta, "beta", flat, _f32, index)
+    slot_ptr, P, states = _delta_pool(state, state_out, slots, S, (H, Dk, Dv), index)
+    if step:
+        q_at, k_at, v_at, g_at, b_at = ((t.data_ptr(), n[0], 0) for t, n in ((q, qs), (k, ks), (v, vs), (g, gs), (beta, bs)))
+    elif offsets is None:
+        q_at, k_at, v_at, g_at, b_at = ((t.data_ptr(), n[0], n[1])
+                                        for t, n in ((q, qs), (k, ks), (v, vs), (g, gs), (beta, bs)))
+    else:
+        q_at, k_at, v_at, g_at, b_at = ((t.data_ptr(), 0, n[0]) for t, n in ((q, qs), (k, ks), (v, vs), (g, gs), (beta, bs)))
+    return (S, L, _dense(offsets, "offsets", (S + 1,), torch.int32, index), slot_ptr, P, H, Hk, Dk, Dv, _code(v),
+            Dk ** -0.5 if scale is None else scale, *q_at, *k_at, *v_at, qs[-2], ks[-2], vs[-2], *g_at, *b_at, *states)
+
+
+def _delta_sizes(S, L, packed, H, Hk, Dk, Dv, code):
+    """The arguments that space depends on."""
+    return (S, L, 16 if packed else 0, 0, S, H, Hk, Dk, Dv, code, 0.0, *[0] * 9, 0, 0, 0, *[0] * 6, 0, 0, 0, 0, 0, 0, 0, 0)
+
+
+@functools.lru_cache(4096)
+def _delta_space(*sizes):
+    """Bytes of (saved, the forward's workspace)."""
+    a = _DELTA(*_delta_sizes(*sizes))
+    return _bytes("seq_gated_delta_save", a), _bytes("seq_gated_delta_workspace", a)
+
+
+@functools.lru_cache(4096)
+def _delta_grad_space(*sizes):
+    """Bytes of (saved, the gradient's workspace)."""
+    return _delta_space(*sizes)[0], _bytes("seq_gated_delta_grad_workspace", _DELTA_GRAD(*_delta_sizes(*sizes), *[0] * 11))
+
+
+def gated_delta(q, k, v, g, beta, scale=None, offsets=None, slots=None, state=None, state_out=None, save=False,
+                stream=None):
+    """Gated delta rule over q, k [S, L, Hk, Dk], v [S, L, H, Dv] and float32 g, beta [S, L, H], or the same without S
+    with offsets; heads of v share those of q and k, head h having key head h // (H / Hk):
+
+        S = e^g S;  S = S + beta k (v - S^T k)^T;  o = scale S^T q        (scale: Dk ** -0.5 by default)
+
+    per token and head with a state S [Dk, Dv].  g is the logarithm of a decay (<= 0 as a rule), keys have unit length
+    as a rule.  Dk <= 256, Dv <= 1024.  Returns (o, state_out, saved).  `state` float32 [P, H, Dk, Dv] is where the
+    sequences begin (None: zeros) and state_out where their final states go: a new tensor by default or, with slots,
+    `state` itself; the two may be the same.  saved is for gated_delta_grad (None without save)."""
+    on = _here(v, stream)
+    if on is None:
+        return _there(v, stream, gated_delta, q, k, v, g, beta, scale, offsets, slots, state, state_out, save)
+    index = v.get_device()
+    S, L = _delta_rows(v, offsets)
+    shape = v.shape
+    H, Dv = shape[-2:]
+    state_out = _default_out(state_out, slots, state, S, (H, q.shape[-1], Dv), _f32, v)
+    args = _delta_args(q, k, v, g, beta, scale, offsets, slots, state, state_out, S, L, False, index)
+    keep, n = _delta_space(S, L, offsets is not None, H, *args[6:10])
+    o = _same(v)
+    saved = _empty(keep // 4, _f32, v) if save else None
+    ws = _empty(n, torch.uint8, v)
+    status = _lib().seq_gated_delta(
+        _DELTA(*args, saved.data_ptr() if save else 0, o.data_ptr(), L * H * Dv if offsets is None else 0, H * Dv),
+        ws.data_ptr(), n, on)
+    if status:
+        raise ConvWgradError(status, "gated_delta")
+    return o, state_out, saved
+
+
+def gated_delta_step(q, k, v, g, beta, state, scale=None, slots=None, state_out=None, stream=None):
+    """gated_delta for one token of each sequence: q, k [S, Hk, Dk], v [S, H, Dv], g, beta [S, H] -> o [S, H, Dv].  The
+    new states go to state_out, by default `state` itself."""
+    on = _here(v, stream)
+    if on is None:
+        return _there(v, stream, gated_delta_step, q, k, v, g, beta, state, scale, slots, state_out)
+    shape = v.shape
+    if len(shape) != 3:
+        raise ValueError("v must be [S, H, Dv], got shape %s" % (tuple(shape),))
+    args = _delta_args(q, k, v, g, beta, scale, None, slots, state, state if state_out is None else state_out, shape[0], 1,
+                       True, v.get_device())
+    o = _same(v)
+    status = _lib().seq_gated_delta_step(_DELTA(*args, 0, o.data_ptr(), shape[1] * shape[2], 0), on)
+    if status:
+        raise ConvWgradError(status, "gated_delta_step")
+    return o
+
+
+def gated_delta_grad(do, q, k, v, g, beta, saved, scale=None, offsets=None, slots=None, state=None, dstate_out=None,
+                     stream=None):
+    """Gradients of gated_delta, from do, its inputs and its `saved`: a DeltaGrads tuple.  dstate_out float32 [S, H, Dk,
+    Dv]: the gradient of the final states; dstate is that of the first ones, in the order of the sequences."""
+    on = _here(v, stream)
+    if on is None:
+        return _there(v, stream, gated_delta_grad, do, q, k, v, g, beta, saved, scale, offsets, slots, state, dstate_out)
+    shape, dtype, index = v.shape, v.dtype, v.get_device()
+    S, L = _delta_rows(v, offsets)
+    H, Dv = shape[-2:]
+    args = _delta_args(q, k, v, g, beta, scale, offsets, slots, state, None, S, L, False, index)
+    Dk = args[7]
+    keep, n = _delta_grad_space(S, L, offsets is not None, H, *args[6:10])
+    dos = _like(do, "do", shape, dtype, index)
+    saved_ptr = _dense(saved, "saved", (keep // 4,), _f32, index)
+    dq, dk, dv = _empty(q.shape, dtype, v), _empty(q.shape, dtype, v), _same(v)
+    dg, dbeta = _empty(shape[:-1], _f32, v), _empty(shape[:-1], _f32, v)
+    dstate = _empty((S, H, Dk, Dv), _f32, v) if state is not None else None
+    ws = _empty(n, torch.uint8, v)
+    status = _lib().seq_gated_delta_grad(
+        _DELTA_GRAD(*args, saved_ptr, 0, 0, 0, do.data_ptr(), *(dos[:2] if offsets is None else (0, dos[0])), dos[-2],
+                    _dense(dstate_out, "dstate_out", (S, H, Dk, Dv), _f32, index), dq.data_ptr(), dk.data_ptr(),
+                    dv.data_ptr(), dg.data_ptr(), dbeta.data_ptr(), dstate.data_ptr() if state is not None else 0),
+        ws.data_ptr(), n, on)
+    if status:
+        raise ConvWgradError(status, "gated_delta_grad")
+    return DeltaGrads(dq, dk, dv, dg, dbeta, dstate)

@@ -660,6 +660,65 @@ conv_wgrad_status_t seq_selective_scan_grad_workspace(const seq_scan_grad_args_t
 conv_wgrad_status_t seq_selective_scan_grad(const seq_scan_grad_args_t* args, void* workspace, size_t ws_bytes,
                                             void* stream);
 
+/*
+ * Gated delta rule.  Per sequence and head h, with a state S [key_dim][value_dim] and the queries and keys of head
+ * h / (heads / key_heads):
+ *   a = e^g[t, h],   S[t] = a S[t - 1] + beta[t, h] k[t] (v[t, h] - (a S[t - 1])^T k[t])^T,   o[t, h] = scale S[t]^T q[t]
+ * q, k: element (b, t, h, d) at ptr + b * batch + t * row + h * q_head + d; v likewise; o likewise with value_dim
+ * elements between heads.  g, beta: fp32, element (b, t, h) at ptr + b * batch + t * row + h.  g is a logarithm, as a rule
+ * <= 0 (-inf forgets); keys are as a rule of unit length (with beta |k|^2 > 2 the recurrence itself grows).
+ * state, state_out: fp32 [pool][heads][key_dim][value_dim] (stride elements apart), NULL: zeros / not needed; they may be
+ * the same.  save: NULL, or what seq_gated_delta_grad needs, seq_gated_delta_save bytes, 16-byte aligned.
+ * 1 <= key_dim <= 256, 1 <= value_dim <= 1024, heads a multiple of key_heads and at most 65536.
+ * Products and sums keep 32-bit accuracy for every element type.  A chunk of 64 tokens of a sequence is one system: an
+ * infinite or NaN element makes its sequence's later outputs NaN, and may those of the up to 63 tokens before it in its
+ * chunk; other sequences and heads are not touched.
+ */
+typedef struct seq_delta_args {
+  seq_tokens_t tokens;
+  int64_t heads, key_heads;
+  int32_t key_dim, value_dim;
+  int32_t dtype;
+  float scale;
+  seq_view_t q, k, v;
+  int64_t q_head, k_head, v_head;
+  seq_view_t g, beta;
+  const float* state;
+  int64_t state_stride;
+  float* state_out;
+  int64_t state_out_stride;
+  float* save;
+  seq_view_t o;
+} seq_delta_args_t;
+
+conv_wgrad_status_t seq_gated_delta_save(const seq_delta_args_t* args, size_t* bytes);
+conv_wgrad_status_t seq_gated_delta_workspace(const seq_delta_args_t* args, size_t* bytes);
+conv_wgrad_status_t seq_gated_delta(const seq_delta_args_t* args, void* workspace, size_t ws_bytes, void* stream);
+
+/* The same for one token of each sequence (tokens.offsets NULL, tokens.rows 1); save is not written. */
+conv_wgrad_status_t seq_gated_delta_step(const seq_delta_args_t* args, void* stream);
+
+/* Gradients, from dout (strided as v, dout_head elements between heads), dstate_out (dense fp32 [sequences][heads]
+ * [key_dim][value_dim], gradient of the final states, NULL: zero) and fwd.save as the forward filled it.  Outputs dense:
+ * dq, dk rows x key_heads x key_dim, dv rows x heads x value_dim, dg and dbeta fp32 rows x heads, dstate fp32 [sequences]
+ * [heads][key_dim][value_dim] or NULL.  fwd.o, fwd.state and fwd.state_out are not read. */
+typedef struct seq_delta_grad_args {
+  seq_delta_args_t fwd;
+  seq_view_t dout;
+  int64_t dout_head;
+  const float* dstate_out;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* dg;
+  float* dbeta;
+  float* dstate;
+} seq_delta_grad_args_t;
+
+conv_wgrad_status_t seq_gated_delta_grad_workspace(const seq_delta_grad_args_t* args, size_t* bytes);
+conv_wgrad_status_t seq_gated_delta_grad(const seq_delta_grad_args_t* args, void* workspace, size_t ws_bytes,
+                                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif
