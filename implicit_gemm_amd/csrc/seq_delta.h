@@ -146,19 +146,37 @@ __device__ __forceinline__ int opaque(int v) {
 __device__ __forceinline__ f32x4 mfma(s16x8 a, s16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
-// The products of pieces above 2^-8N of the whole, the leading one apart from the others so that two chains run.
+// The products of pieces above 2^-8N of the whole, each order of magnitude in a sum of its own, so that N chains run.
 template <int N, int NA, int NB>
-__device__ __forceinline__ void mfma_pieces(const s16x8 (&a)[NA], const s16x8 (&b)[NB], f32x4& lead, f32x4& rest) {
+__device__ __forceinline__ void mfma_pieces(const s16x8 (&a)[NA], const s16x8 (&b)[NB], f32x4 (&sum)[N]) {
 #pragma unroll
   for (int i = 0; i < NA; ++i)
 #pragma unroll
     for (int j = 0; j < NB; ++j)
-      if (i + j < N) {
-        if (i + j == 0) lead = mfma(a[0], b[0], lead);
-        else rest = mfma(a[i], b[j], rest);
-      }
+      if (i + j < N) sum[i + j] = mfma(a[i], b[j], sum[i + j]);
+}
+// The same into one sum, where there are enough others to fill the time between two steps of a chain.
+template <int N, int NA, int NB>
+__device__ __forceinline__ void mfma_pieces(const s16x8 (&a)[NA], const s16x8 (&b)[NB], f32x4& sum) {
+#pragma unroll
+  for (int i = NA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = NB - 1; j >= 0; --j)
+      if (i + j < N) sum = mfma(a[i], b[j], sum);
 }
 __device__ __forceinline__ f32x4 zero4() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+template <int N>
+__device__ __forceinline__ void clear(f32x4 (&sum)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) sum[i] = zero4();
+}
+template <int N>
+__device__ __forceinline__ f32x4 total(const f32x4 (&sum)[N]) {
+  f32x4 t = sum[N - 1];
+#pragma unroll
+  for (int i = N - 2; i >= 0; --i) t += sum[i];
+  return t;
+}
 
 // Eight 16-bit elements of LDS at p; and a transposed operand: terms are LDS rows of `pitch` elements, p is lane's place
 // as trans_place gives it.
@@ -240,6 +258,47 @@ __device__ __forceinline__ Share share_of(unsigned b, int slices) {
   return Share{(int)(i / slices * 8 + (b & 7)), (int)(i % slices)};
 }
 inline int64_t shares(int64_t units, int64_t slices) { return (units + 7) / 8 * 8 * slices; }
+
+// What a workgroup that walks along a sequence has: COLS columns of one head's state.
+struct Walk {
+  int seq, head, col0, chunks;
+  int64_t key_head, number;      // number: chunk_head of the sequence's first chunk
+  Piece p;
+};
+// False for a workgroup past the last one.
+template <int COLS>
+__device__ __forceinline__ bool find_walk(const DeltaArgs& k, Walk& w) {
+  const int heads = (int)k.a.heads;
+  const Share share = share_of(blockIdx.x, k.slices);
+  if (share.unit >= k.m.S * heads) return false;
+  w.seq = uniform(share.unit / heads);
+  w.head = uniform(share.unit % heads);
+  w.col0 = share.slice * COLS;
+  w.key_head = w.head / (heads / (int)k.a.key_heads);
+  w.p.seq = w.seq;
+  if (k.m.offsets) {
+    const int start = uniform(seq_start(k.m, w.seq)), stop = uniform(seq_start(k.m, w.seq + 1));
+    w.p.batch = 0;
+    w.p.first = start;
+    w.p.len = max(stop - start, 0);
+  } else {
+    w.p.batch = w.seq;
+    w.p.first = 0;
+    w.p.len = k.m.rows;
+  }
+  w.chunks = (w.p.len + kChunk - 1) >> kChunkShift;
+  w.number = chunk_head(k, chunk_number(k.m, w.seq, (int)w.p.first, 0), w.head);
+  return true;
+}
+
+// A wave's 16 rows of K or Q in a chunk as loaded, lane by lane: row 16 r + l % 16, dimensions 32 c + 8 (l / 16) .. + 7.
+// Rows past the sequence's end are its last one: what they meet is zero or thrown away.  WHOLE: Dk is KP.
+template <typename T, int KP, bool WHOLE>
+__device__ __forceinline__ void load_row(const ChunkRows<const T>& from, int n, int row, int lg, int Dk, int c, Eight<T>& to) {
+  const int d = 32 * c + 8 * lg;
+  if constexpr (WHOLE) to.raw.load(&from.at(min(row, n - 1), d));
+  else to.load(&from.at(min(row, n - 1), d), Dk - d);
+}
 
 DeltaArgs delta_args(const seq_delta_args_t& a, float* ws);
 hipError_t launch_delta_chunks(const DeltaArgs& k, bool gradient, hipStream_t stream);

@@ -27,54 +27,99 @@ __device__ __forceinline__ void block_store(float (*c)[kSquarePitch], int r, int
   for (int x = 0; x < 4; ++x) c[r + 4 * (lane >> 4) + x][col + (lane & 15)] = sign * v[x];
 }
 
-template <typename T, bool GRAD>
-__global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs k) {
+constexpr int kPanel = 128;                // dimensions of K and Q that are staged at a time
+
+template <typename T>
+union ChunkLds {
+  static constexpr int kPitch = kPanel + 16 / (int)sizeof(T);
+  struct Panel {
+    T key[kChunk][kPitch], query[kChunk][kPitch];
+  } panel;
+  struct Squares {
+    float M[kChunk][kSquarePitch], I[kChunk][kSquarePitch];
+  } squares;
+};
+
+// EIGHTS: Dk is a multiple of 8.
+template <typename T, bool GRAD, bool EIGHTS>
+__global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void delta_chunk_kernel(DeltaArgs k) {
   constexpr int N = ElemPieces<T>::n;
-  __shared__ __attribute__((aligned(16))) float M[kChunk][kSquarePitch], P[kChunk][kSquarePitch], I[kChunk][kSquarePitch];
+  __shared__ __attribute__((aligned(16))) char bytes[sizeof(ChunkLds<T>)];
   __shared__ ChunkDecay d;
+  ChunkLds<T>& L = *reinterpret_cast<ChunkLds<T>*>(bytes);
+  auto& M = L.squares.M;
+  auto& I = L.squares.I;
   const seq_delta_args_t& a = k.a;
-  const int lane = threadIdx.x & 63, r = uniform(threadIdx.x >> 6), lr = lane & 15, lg = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, r = uniform(tid >> 6), lr = lane & 15, lg = lane >> 4;
   const int heads = (int)a.heads, piece = blockIdx.x / heads, head = blockIdx.x % heads;
   Piece p;
   if (!find_piece(k.m, piece, p)) return;
+  const int n = p.end - p.t0, Dk = a.key_dim;
   if (p.seq == k.m.S) {            // padding behind the last sequence
     if constexpr (!GRAD) {
       const int Dv = a.value_dim;
-      for (int i = threadIdx.x; i < (p.end - p.t0) * Dv; i += 256)
+      for (int i = tid; i < n * Dv; i += 256)
         from_f32(0.f, row_at<T>(a.o, p, p.t0 + i / Dv)[(int64_t)head * Dv + i % Dv]);
     }
     return;
   }
-  const int n = p.end - p.t0, Dk = a.key_dim;
   if (n <= 0) return;                // an empty sequence has a number too
   const int64_t at = chunk_head(k, piece, head);
-  if (r == 0) {
-    chunk_decay(a, p, head, lane, d);
-    k.decay[at * 2 * kChunk + lane] = d.first[lane];
-    k.decay[(at * 2 + 1) * kChunk + lane] = d.last[lane] * d.beta[lane];
-  }
   const int64_t kh = head / (heads / (int)a.key_heads);
-  const int row = 16 * r + lr;
-  // Rows past the chunk's end read its last one: what they give is multiplied by zero or thrown away below.
   const ChunkRows<const T> key(a.k, kh * a.k_head, p, p.t0), query(a.q, kh * a.q_head, p, p.t0);
-  f32x4 kk[4][2], qk[4][2];
+  f32x4 kk[4], qk[4];
+  clear(kk);
+  clear(qk);
+  for (int c0 = 0; c0 < Dk; c0 += kPanel) {
+    // 64 rows of 16 groups of 8 dimensions, four groups a lane.  Rows past the chunk's end read its last one: what they
+    // give is thrown away below.
+    Eight<T> ek[4], eq[4];
 #pragma unroll
-  for (int t = 0; t < 4; ++t) kk[t][0] = kk[t][1] = qk[t][0] = qk[t][1] = zero4();
-  for (int c = 8 * lg; c - 8 * lg < Dk; c += 32) {
-    Eight<T> e;
-    s16x8 ka[N], qa[N];
-    e.load(&key.at(min(row, n - 1), c), Dk - c);
-    e.pieces(ka);
-    e.load(&query.at(min(row, n - 1), c), Dk - c);
-    e.pieces(qa);
+    for (int i = 0; i < 4; ++i) {
+      const int row = min(tid / 16 + 16 * i, n - 1), c = c0 + 8 * (tid & 15);
+      if constexpr (EIGHTS) {
+        ek[i].raw.load(&key.at(row, c < Dk ? c : 0));
+        eq[i].raw.load(&query.at(row, c < Dk ? c : 0));
+      } else {
+        ek[i].load(&key.at(row, c), Dk - c);
+        eq[i].load(&query.at(row, c), Dk - c);
+      }
+    }
+    if (c0 == 0 && r == 0) {
+      chunk_decay(a, p, head, lane, d);
+      k.decay[at * 2 * kChunk + lane] = d.first[lane];
+      k.decay[(at * 2 + 1) * kChunk + lane] = d.last[lane] * d.beta[lane];
+    }
+    if (c0) __syncthreads();         // the last panel's reads are done
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-      if (t <= r) {
-        s16x8 kb[N];
-        e.load(&key.at(min(16 * t + lr, n - 1), c), Dk - c);
-        e.pieces(kb);
-        mfma_pieces<kPieces>(ka, kb, kk[t][0], kk[t][1]);
-        mfma_pieces<kPieces>(qa, kb, qk[t][0], qk[t][1]);
+    for (int i = 0; i < 4; ++i) {
+      const int row = tid / 16 + 16 * i, c = 8 * (tid & 15);
+      if (EIGHTS && c0 + c >= Dk) {
+        ek[i].raw.clear();
+        eq[i].raw.clear();
+      }
+      ek[i].raw.store(&L.panel.key[row][c]);
+      eq[i].raw.store(&L.panel.query[row][c]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < kPanel / 32; ++c)
+      if (c0 + 32 * c < Dk) {
+        Eight<T> e;
+        s16x8 ka[N], qa[N];
+        e.raw.load(&L.panel.key[16 * r + lr][32 * c + 8 * lg]);
+        e.pieces(ka);
+        e.raw.load(&L.panel.query[16 * r + lr][32 * c + 8 * lg]);
+        e.pieces(qa);
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (t <= r) {
+            s16x8 kb[N];
+            e.raw.load(&L.panel.key[16 * t + lr][32 * c + 8 * lg]);
+            e.pieces(kb);
+            mfma_pieces<kPieces>(ka, kb, kk[t]);
+            mfma_pieces<kPieces>(qa, kb, qk[t]);
+          }
       }
   }
   __syncthreads();
@@ -84,11 +129,11 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs k) {
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const int i = 16 * r + 4 * lg + x;
-      const bool live = i < n && j <= i;
+      const bool live = t <= r && i < n && j <= i;
       const float e = live ? decay_between(d, i, j) * d.beta[j] : 0.f;
-      M[i][j] = live && j < i ? e * (kk[t][0][x] + kk[t][1][x]) : 0.f;
-      P[i][j] = live ? e * (qk[t][0][x] + qk[t][1][x]) * a.scale : 0.f;
+      M[i][j] = live && j < i ? e * kk[t][x] : 0.f;
       I[i][j] = 0.f;
+      qk[t][x] = live ? e * qk[t][x] * a.scale : 0.f;
     }
   }
   wave_sync();                       // a diagonal block is read by the wave that wrote it
@@ -123,6 +168,12 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs k) {
     block_store(I, 32 + u, v, lane, z, -1.f);
   }
   __syncthreads();
+  // M has served: P takes its place.
+#pragma unroll
+  for (int t = 0; t < 4; ++t) block_store(M, 16 * r, 16 * t, lane, qk[t], 1.f);
+  if (GRAD) __syncthreads();         // columns are read, of all waves' rows
+  else wave_sync();
+  const int row = 16 * r + lr;
   uint16_t* inv = k.inverse + at * kMatrix;
   uint16_t* inn = k.inner + at * kMatrix;
 #pragma unroll
@@ -134,7 +185,7 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs k) {
     for (int i = 0; i < 8; ++i) {
       const int c = 32 * s + 8 * lg + i;
       fi[i] = GRAD ? I[c][row] : I[row][c];
-      fp[i] = GRAD ? P[c][row] : P[row][c];
+      fp[i] = GRAD ? M[c][row] : M[row][c];
     }
     s16x8 pi[kPieces], pp[kPieces];
     split8<kPieces>(fi, pi);
@@ -152,55 +203,39 @@ __global__ __launch_bounds__(256) void delta_chunk_kernel(DeltaArgs k) {
 // chunk's tokens 16 r .. and the state's rows r KP / 4 .., in registers; the state's pieces go to all waves through LDS.
 // Waves 4 .. 7 make the outputs of the same tokens beside them.  Three exchanges a chunk: the state, X, and Z; global
 // loads are one chunk ahead.
-template <typename T, int KP, int NT, bool SAVE>
-__global__ __launch_bounds__(512) void delta_kernel(DeltaArgs k) {
-  constexpr int N = ElemPieces<T>::n, NO = OutPieces<T>::n, KS = KP / 32, MT = KP / 64;
-  constexpr int kKeyPitch = KP + 8;
-  constexpr bool kStage = N == 1 || KP <= 128;     // K's pieces fit the LDS beside the rest
-  constexpr int kCols = 16 * NT;
-  constexpr bool kAhead = N == 1 || KP <= 128;     // K's and Q's rows of the next chunk fit the registers
-  __shared__ __attribute__((aligned(16))) uint16_t sS[kPieces][kCols][kKeyPitch], sX[kPieces][kCols][kTokenPitch],
-      sW[kPieces][kCols][kTokenPitch], sZ[NO][kCols][kTokenPitch], sK[kStage ? N : 1][kStage ? kChunk : 1][kKeyPitch];
-  const seq_delta_args_t& a = k.a;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = wave & 3, lr = lane & 15, lg = lane >> 4;
-  const bool chain = wave < 4;
-  const int heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
-  const Share share = share_of(blockIdx.x, k.slices);
-  if (share.unit >= k.m.S * heads) return;
-  const int s = uniform(share.unit / heads), head = uniform(share.unit % heads), col0 = share.slice * kCols;
-  const int64_t kh = head / (heads / (int)a.key_heads);
-  Piece p;
-  p.seq = s;
-  if (k.m.offsets) {
-    const int start = uniform(seq_start(k.m, s)), stop = uniform(seq_start(k.m, s + 1));
-    p.batch = 0;
-    p.first = start;
-    p.len = max(stop - start, 0);
-  } else {
-    p.batch = s;
-    p.first = 0;
-    p.len = k.m.rows;
-  }
-  const int chunks = (p.len + kChunk - 1) >> kChunkShift;
-  const int64_t number = chunk_head(k, chunk_number(k.m, s, (int)p.first, 0), head);
-  const int64_t slot = pool_slot(a.tokens.slots, a.tokens.pool, s);
+template <typename T, int KP, int NT>
+struct WalkLds {
+  static constexpr int N = ElemPieces<T>::n, NO = OutPieces<T>::n;
+  static constexpr bool kStage = N == 1 || KP <= 128;     // K's pieces fit beside the rest
+  uint16_t S[kPieces][16 * NT][KP + 8], X[kPieces][16 * NT][kTokenPitch], W[kPieces][16 * NT][kTokenPitch],
+      Z[NO][16 * NT][kTokenPitch], K[kStage ? N : 1][kStage ? kChunk : 1][KP + 8];
+};
+// Two workgroups a CU (four waves a SIMD) where their LDS and registers allow it.
+template <class Lds, int KP>
+constexpr int walk_waves() { return sizeof(Lds) <= 80 * 1024 && KP <= 128 ? 4 : 2; }
 
-  // ---- the state
+template <typename T, int KP, int NT, bool SAVE, bool WHOLE>
+__device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, WalkLds<T, KP, NT>& L, int r, int lane) {
+  typedef WalkLds<T, KP, NT> Lds;
+  constexpr int N = Lds::N, NO = Lds::NO, KS = KP / 32, MT = KP / 64;
+  constexpr bool kAhead = N == 1 || KP <= 128;     // the next chunk's rows fit the registers
+  const seq_delta_args_t& a = k.a;
+  const int lr = lane & 15, lg = lane >> 4, heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
+  const int64_t slot = pool_slot(a.tokens.slots, a.tokens.pool, w.seq);
+  const int64_t place = (int64_t)w.head * Dk * Dv;
   f32x4 S[MT][NT];
-  const int64_t place = (int64_t)head * Dk * Dv;
-  if (chain) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int c = col0 + 16 * t + lr;
+    for (int t = 0; t < NT; ++t) {
+      const int c = w.col0 + 16 * t + lr;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = 16 * (r * MT + m) + 4 * lg + x;
-          S[m][t][x] = a.state && slot >= 0 && row < Dk && c < Dv ? a.state[slot * a.state_stride + place + (int64_t)row * Dv + c] : 0.f;
-        }
+      for (int x = 0; x < 4; ++x) {
+        const int row = 16 * (r * MT + m) + 4 * lg + x;
+        S[m][t][x] = a.state && slot >= 0 && (WHOLE || row < Dk) && c < Dv
+                         ? at_lane(a.state + slot * a.state_stride + place, row * Dv + c) : 0.f;
       }
-  }
+    }
   auto share_state = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -209,39 +244,35 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs k) {
         uint2 u[kPieces];
         split4<kPieces>(S[m][t], u);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          *reinterpret_cast<uint2*>(&sS[i][16 * t + lr][16 * (r * MT + m) + 4 * lg]) = u[i];
+        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.S[i][16 * t + lr][16 * (r * MT + m) + 4 * lg]) = u[i];
       }
   };
   auto keep_state = [&](float* to) __attribute__((always_inline)) {
+    const int row0 = opaque(16 * MT * r + 4 * lg);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int t = 0; t < NT; ++t) {
+      const int c = w.col0 + 16 * t + lr;
+      if (c < Dv) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int c = col0 + 16 * t + lr;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = 16 * (r * MT + m) + 4 * lg + x;
-          if (row < Dk && c < Dv) at_lane(to, row * Dv + c) = S[m][t][x];
-        }
+          for (int x = 0; x < 4; ++x)
+            if (WHOLE || row0 + 16 * m + x < Dk) at_lane(to, (row0 + 16 * m + x) * Dv + c) = S[m][t][x];
       }
+    }
   };
-
-  // ---- what is loaded a chunk ahead
-  Eight<T> rows[kAhead ? KS : 1];                 // chain: K, outputs: Q
-  T v[NT][4];                        // chain: V
-  s16x8 square[2][kPieces];          // chain: (1 + M)^-1, outputs: P
+  Eight<T> rows[kAhead ? KS : 1];
+  T v[NT][4];
+  s16x8 square[2][kPieces];
   float4 first, last;
   float whole;
-  auto load_row = [&](int j, int c, Eight<T>& to) __attribute__((always_inline)) {
-    const int n = p.len - kChunk * j, t = 16 * r + lr;
-    const ChunkRows<const T> from(chain ? a.k : a.q, kh * (chain ? a.k_head : a.q_head), p, kChunk * j);
-    to.load(&from.at(min(t, n - 1), 32 * c + 8 * lg), t < n ? Dk - 32 * c - 8 * lg : 0);
+  auto keys = [&](int j) __attribute__((always_inline)) {
+    return ChunkRows<const T>(a.k, w.key_head * a.k_head, w.p, kChunk * j);
   };
   auto load_rows = [&](int j) __attribute__((always_inline)) {
     if constexpr (kAhead) {
 #pragma unroll
-      for (int c = 0; c < KS; ++c) load_row(j, c, rows[c]);
+      for (int c = 0; c < KS; ++c) load_row<T, KP, WHOLE>(keys(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, rows[c]);
     }
   };
   auto row_pieces = [&](int j, int c, s16x8 (&e)[N]) __attribute__((always_inline)) {
@@ -249,205 +280,292 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs k) {
       rows[c].pieces(e);
     } else {
       Eight<T> row;
-      load_row(j, c, row);
+      load_row<T, KP, WHOLE>(keys(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, row);
       row.pieces(e);
     }
   };
   auto load_values = [&](int j) __attribute__((always_inline)) {
-    const int n = p.len - kChunk * j;
-    const ChunkRows<const T> from(a.v, head * a.v_head, p, kChunk * j);
+    const int n = w.p.len - kChunk * j;
+    const ChunkRows<const T> from(a.v, w.head * a.v_head, w.p, kChunk * j);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int t = 16 * r + 4 * lg + x;
+    for (int x = 0; x < 4; ++x)
 #pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        const int col = col0 + 16 * c + lr;
-        if (t < n && col < Dv) v[c][x] = from.at(t, col);
-        else from_f32(0.f, v[c][x]);
-      }
-    }
+      for (int t = 0; t < NT; ++t) v[t][x] = from.at(min(16 * r + 4 * lg + x, n - 1), min(w.col0 + 16 * t + lr, Dv - 1));
   };
   auto load_square = [&](int j) __attribute__((always_inline)) {
-    const uint16_t* from = (chain ? k.inverse : k.inner) + (number + (int64_t)j * heads) * kMatrix + lane * 8;
+    const uint16_t* from = k.inverse + (w.number + (int64_t)j * heads) * kMatrix;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      if (c <= r / 2) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          if (i < (NO > 2 ? kPieces : 2) || chain)
-            square[c][i] = *reinterpret_cast<const s16x8*>(from + (lower_frag(r, c) * kPieces + i) * kFragElems);
-      }
+      for (int i = 0; i < kPieces; ++i)
+        square[c][i] = *reinterpret_cast<const s16x8*>(&at_lane(from + (lower_frag(r, min(c, r / 2)) * kPieces + i) * kFragElems, lane * 8));
   };
   auto load_decay = [&](int j) __attribute__((always_inline)) {
-    const float* from = k.decay + (number + (int64_t)j * heads) * 2 * kChunk;
+    const float* from = k.decay + (w.number + (int64_t)j * heads) * 2 * kChunk;
     first = *reinterpret_cast<const float4*>(from + 16 * r + 4 * lg);
     last = *reinterpret_cast<const float4*>(from + kChunk + 16 * r + 4 * lg);
     whole = from[kChunk - 1];
   };
-  if (chunks > 0) {
+  if (w.chunks > 0) {
     load_rows(0);
-    if (chain) load_values(0);
-    load_square(0);
+    load_values(0);
     load_decay(0);
+    load_square(0);
   }
-  if (chain) share_state();
+  share_state();
   lds_barrier();
-
-  for (int j = 0; j < chunks; ++j) {
-    const int n = p.len - kChunk * j;      // tokens that are left
-    const bool more = j + 1 < chunks;
+#pragma unroll 1
+  for (int j = 0; j < w.chunks; ++j) {
+    const int n = w.p.len - kChunk * j;      // tokens that are left
+    const int next = min(j + 1, w.chunks - 1);
     const float f[4] = {first.x, first.y, first.z, first.w}, l[4] = {last.x, last.y, last.z, last.w};
     const float keep = whole;
-    f32x4 lead[NT], rest[NT];
+    if (SAVE) keep_state(k.states + (w.number + (int64_t)j * heads) * Dk * Dv);
+    // X = V - e^G (K S)
+    {
+      f32x4 sum[NT][kPieces];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) lead[t] = rest[t] = zero4();
-    // K S or Q S
-    if (SAVE && chain) keep_state(k.states + (number + (int64_t)j * heads) * Dk * Dv);
+      for (int t = 0; t < NT; ++t) clear(sum[t]);
 #pragma unroll
-    for (int c = 0; c < KS; ++c) {
-      s16x8 e[N];
-      row_pieces(j, c, e);
-      if (kStage && chain) {
+      for (int c = 0; c < KS; ++c) {
+        s16x8 e[N];
+        row_pieces(j, c, e);
+        if (Lds::kStage && N > 1) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<s16x8*>(&sK[i][kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[i];
+          for (int i = 0; i < N; ++i) *reinterpret_cast<s16x8*>(&L.K[i][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[i];
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          s16x8 b[kPieces];
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.S[i][16 * t + lr][32 * c + 8 * lg]);
+          mfma_pieces<kPieces>(e, b, sum[t]);
+        }
+        if (c & 1) __builtin_amdgcn_sched_barrier(0);     // two blocks' operands in registers at a time
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        s16x8 b[kPieces];
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          if (chain || i < NO) b[i] = lds8(&sS[i][16 * t + lr][32 * c + 8 * lg]);
-        if (chain) mfma_pieces<kPieces>(e, b, lead[t], rest[t]);
-        else mfma_pieces<NO>(e, b, lead[t], rest[t]);
-      }
-    }
-    if (more) load_rows(j + 1);
-    if (chain) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
+        const f32x4 kS = total(sum[t]);
         f32x4 x;
         uint2 u[kPieces];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = __builtin_fmaf(-f[i], lead[t][i] + rest[t][i], to_f32(v[t][i]));
+        for (int i = 0; i < 4; ++i) {
+          const float d = __builtin_fmaf(-f[i], kS[i], to_f32(v[t][i]));
+          x[i] = 16 * r + 4 * lg + i < n && w.col0 + 16 * t + lr < Dv ? d : 0.f;
+        }
         split4<kPieces>(x, u);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&sX[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
+        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.X[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
       }
-      if (more) load_values(j + 1);
     }
     lds_barrier();
-    if (chain) {
-      // Z
-      f32x4 z[NT];
+    if (Lds::kStage && N == 1) {
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        s16x8 e[N];
+        row_pieces(j, c, e);
+        *reinterpret_cast<s16x8*>(&L.K[0][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[0];
+      }
+    }
+    // Z = (1 + M)^-1 X
+    f32x4 z[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      f32x4 sum[kPieces];
+      clear(sum);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (c <= r / 2) {
+          s16x8 b[kPieces];
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.X[i][16 * t + lr][32 * c + 8 * lg]);
+          mfma_pieces<kPieces>(square[c], b, sum);
+        }
+      z[t] = total(sum);
+      uint2 u[kPieces];
+      f32x4 x;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = l[i] * z[t][i];
+      split4<kPieces>(x, u);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.W[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
+      uint2 uz[NO];
+      split4<NO>(z[t], uz);
+#pragma unroll
+      for (int i = 0; i < NO; ++i) *reinterpret_cast<uint2*>(&L.Z[i][16 * t + lr][16 * r + 4 * lg]) = uz[i];
+    }
+    lds_barrier();
+    if (SAVE) {
+      float* to = k.errors + ((w.p.batch * k.m.rows + w.p.first + kChunk * j) * heads + w.head) * Dv + w.col0;
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+        if (w.col0 + 16 * c + lr < Dv) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = opaque(16 * r + 4 * lg) + i;
+            if (t < n) at_lane(to, t * heads * Dv + 16 * c + lr) = z[c][i];
+          }
+        }
+    }
+    load_rows(next);
+    load_values(next);
+    load_decay(next);
+    // S' = e^G_C S + K^T W
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      f32x4 sum[NT][kPieces];
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        lead[t] = rest[t] = zero4();
+        clear(sum[t]);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (c <= r / 2) {
-            s16x8 b[kPieces];
+        for (int x = 0; x < 4; ++x) sum[t][0][x] = keep * S[m][t][x];
+      }
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i) b[i] = lds8(&sX[i][16 * t + lr][32 * c + 8 * lg]);
-            mfma_pieces<kPieces>(square[c], b, lead[t], rest[t]);
+      for (int c = 0; c < 2; ++c) {
+        s16x8 e[N];
+        if constexpr (Lds::kStage) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) e[i] = lds8_trans(&L.K[i][32 * c][16 * (r * MT + m)] + trans_place(lane, KP + 8), KP + 8);
+        } else {
+          const ChunkRows<const T> key = keys(j);
+          float g[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int t = opaque(32 * c + 8 * lg) + i, row = 16 * (r * MT + m) + lr;
+            g[i] = t < n && row < Dk ? to_f32(key.at(t, row)) : 0.f;
           }
-        z[t] = lead[t] + rest[t];
-        uint2 u[kPieces], w[kPieces];
-        split4<kPieces>(z[t], u);
-#pragma unroll
-        for (int i = 0; i < NO; ++i) *reinterpret_cast<uint2*>(&sZ[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
-        f32x4 x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = l[i] * z[t][i];
-        split4<kPieces>(x, w);
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&sW[i][16 * t + lr][16 * r + 4 * lg]) = w[i];
-      }
-      if (SAVE) {
-        float* to = k.errors + ((p.batch * k.m.rows + p.first + kChunk * j) * heads + head) * Dv + col0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = 16 * r + 4 * lg + i;
-#pragma unroll
-          for (int c = 0; c < NT; ++c)
-            if (t < n && col0 + 16 * c + lr < Dv) at_lane(to, t * heads * Dv + 16 * c + lr) = z[c][i];
+          split8<N>(g, e);
         }
-      }
-      if (more) {
-        load_square(j + 1);
-        load_decay(j + 1);
-      }
-    }
-    lds_barrier();
-    if (chain) {
-      // S' = e^G_C S + K^T W
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        f32x4 low[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          low[t] = zero4();
+          s16x8 b[kPieces];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) S[m][t][x] *= keep;
+          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.W[i][16 * t + lr][32 * c + 8 * lg]);
+          mfma_pieces<kPieces>(e, b, sum[t]);
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          s16x8 e[N];
-          if constexpr (kStage) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-              e[i] = lds8_trans(&sK[i][32 * c][16 * (r * MT + m)] + trans_place(lane, kKeyPitch), kKeyPitch);
-          } else {
-            const ChunkRows<const T> key(a.k, kh * a.k_head, p, kChunk * j);
-            float g[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int t = opaque(32 * c + 8 * lg) + i, row = 16 * (r * MT + m) + lr;
-              g[i] = t < n && row < Dk ? to_f32(key.at(t, row)) : 0.f;
-            }
-            split8<N>(g, e);
-          }
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            s16x8 b[kPieces];
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) b[i] = lds8(&sW[i][16 * t + lr][32 * c + 8 * lg]);
-            mfma_pieces<kPieces>(e, b, S[m][t], low[t]);
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) S[m][t] += low[t];
       }
-      share_state();
-    } else {
-      // O
-      const ChunkRows<T> out(a.o, (int64_t)head * Dv, p, kChunk * j);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) S[m][t] = total(sum[t]);
+    }
+    __builtin_amdgcn_sched_barrier(0);       // the sums' registers are free by now
+    load_square(next);
+    share_state();
+    lds_barrier();
+  }
+  if (a.state_out && slot >= 0) keep_state(a.state_out + slot * a.state_out_stride + place);
+}
+
+template <typename T, int KP, int NT, bool WHOLE>
+__device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, WalkLds<T, KP, NT>& L, int r, int lane) {
+  typedef WalkLds<T, KP, NT> Lds;
+  constexpr int N = Lds::N, NO = Lds::NO, KS = KP / 32;
+  constexpr bool kAhead = N == 1 || KP <= 128;
+  const seq_delta_args_t& a = k.a;
+  const int lr = lane & 15, lg = lane >> 4, heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
+  Eight<T> rows[kAhead ? KS : 1];
+  s16x8 square[2][NO];
+  float4 first;
+  auto queries = [&](int j) __attribute__((always_inline)) {
+    return ChunkRows<const T>(a.q, w.key_head * a.q_head, w.p, kChunk * j);
+  };
+  auto load_rows = [&](int j) __attribute__((always_inline)) {
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int c = 0; c < KS; ++c) load_row<T, KP, WHOLE>(queries(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, rows[c]);
+    }
+  };
+  auto load_square = [&](int j) __attribute__((always_inline)) {
+    const uint16_t* from = k.inner + (w.number + (int64_t)j * heads) * kMatrix;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < NO; ++i)
+        square[c][i] = *reinterpret_cast<const s16x8*>(&at_lane(from + (lower_frag(r, min(c, r / 2)) * kPieces + i) * kFragElems, lane * 8));
+  };
+  auto load_decay = [&](int j) __attribute__((always_inline)) {
+    first = *reinterpret_cast<const float4*>(k.decay + (w.number + (int64_t)j * heads) * 2 * kChunk + 16 * r + 4 * lg);
+  };
+  if (w.chunks > 0) {
+    load_rows(0);
+    load_decay(0);
+    load_square(0);
+  }
+  lds_barrier();
+#pragma unroll 1
+  for (int j = 0; j < w.chunks; ++j) {
+    const int n = w.p.len - kChunk * j;
+    const int next = min(j + 1, w.chunks - 1);
+    f32x4 o[NT][NO];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) clear(o[t]);
+#pragma unroll
+    for (int c = 0; c < KS; ++c) {
+      s16x8 e[N];
+      if constexpr (kAhead) {
+        rows[c].pieces(e);
+      } else {
+        Eight<T> row;
+        load_row<T, KP, WHOLE>(queries(j), n, 16 * r + lr, lg, Dk, c, row);
+        row.pieces(e);
+      }
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        f32x4 o, low = zero4();
+        s16x8 b[NO];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = a.scale * f[i] * (lead[t][i] + rest[t][i]);
+        for (int i = 0; i < NO; ++i) b[i] = lds8(&L.S[i][16 * t + lr][32 * c + 8 * lg]);
+        mfma_pieces<NO>(e, b, o[t]);
+      }
+    }
+    lds_barrier();
+    const float f[4] = {first.x, first.y, first.z, first.w};
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (c <= r / 2) {
-            s16x8 b[NO];
+    for (int t = 0; t < NT; ++t) {
+      const f32x4 qS = total(o[t]);
+      clear(o[t]);
 #pragma unroll
-            for (int i = 0; i < NO; ++i) b[i] = lds8(&sZ[i][16 * t + lr][32 * c + 8 * lg]);
-            mfma_pieces<NO>(square[c], b, o, low);
-          }
+      for (int i = 0; i < 4; ++i) o[t][0][i] = a.scale * f[i] * qS[i];
+    }
+    load_rows(next);
+    load_decay(next);
+    lds_barrier();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (c <= r / 2) {
+          s16x8 b[NO];
+#pragma unroll
+          for (int i = 0; i < NO; ++i) b[i] = lds8(&L.Z[i][16 * t + lr][32 * c + 8 * lg]);
+          mfma_pieces<NO>(square[c], b, o[t]);
+        }
+    load_square(next);
+    const ChunkRows<T> out(a.o, (int64_t)w.head * Dv, w.p, kChunk * j);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const f32x4 v = total(o[t]);
+      const int col = w.col0 + 16 * t + lr;
+      if (col < Dv) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int row = 16 * r + 4 * lg + i, col = col0 + 16 * t + lr;
-          if (row < n && col < Dv) from_f32(o[i] + low[i], out.at(row, col));
+          const int row = 16 * r + 4 * lg + i;
+          if (row < n) from_f32(v[i], out.at(row, col));
         }
-      }
-      if (more) {
-        load_square(j + 1);
-        load_decay(j + 1);
       }
     }
     lds_barrier();
   }
-  if (chain && a.state_out && slot >= 0) keep_state(a.state_out + slot * a.state_out_stride + place);
+}
+
+template <typename T, int KP, int NT, bool SAVE, bool WHOLE>
+__global__ __launch_bounds__(512, (walk_waves<WalkLds<T, KP, NT>, KP>())) void delta_kernel(DeltaArgs k) {
+  typedef WalkLds<T, KP, NT> Lds;
+  __shared__ __attribute__((aligned(16))) char bytes[sizeof(Lds)];
+  Lds& L = *reinterpret_cast<Lds*>(bytes);
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  Walk w;
+  if (!find_walk<16 * NT>(k, w)) return;
+  if (wave < 4) walk_chain<T, KP, NT, SAVE, WHOLE>(k, w, L, wave, lane);
+  else walk_outputs<T, KP, NT, WHOLE>(k, w, L, wave - 4, lane);
 }
 
 // ---- one token ----------------------------------------------------------------------------------------------------------
@@ -540,24 +658,32 @@ hipError_t step_t(const DeltaArgs& k, hipStream_t stream) {
   return launch_kernel(delta_step_kernel<T, 32, 32>, grid, block, k, stream);
 }
 
-template <typename T, int KP, int NT>
+template <typename T, int KP, int NT, bool WHOLE>
 hipError_t delta_n(const DeltaArgs& k, hipStream_t stream) {
   const dim3 grid((unsigned)shares(k.a.tokens.sequences * k.a.heads, k.slices)), block(512);
-  if (k.states) return launch_kernel(delta_kernel<T, KP, NT, true>, grid, block, k, stream);
-  return launch_kernel(delta_kernel<T, KP, NT, false>, grid, block, k, stream);
+  if (k.states) return launch_kernel(delta_kernel<T, KP, NT, true, WHOLE>, grid, block, k, stream);
+  return launch_kernel(delta_kernel<T, KP, NT, false, WHOLE>, grid, block, k, stream);
+}
+template <typename T, int KP>
+hipError_t delta_k(const DeltaArgs& k, hipStream_t stream) {
+  if (k.a.key_dim == KP) return delta_n<T, KP, 1, true>(k, stream);
+  return delta_n<T, KP, 1, false>(k, stream);
 }
 template <typename T>
 hipError_t delta_t(const DeltaArgs& k, hipStream_t stream) {
-  if (k.a.key_dim <= 64) return delta_n<T, 64, 1>(k, stream);
-  if (k.a.key_dim <= 128) return delta_n<T, 128, 1>(k, stream);
-  return delta_n<T, 256, 1>(k, stream);
+  if (k.a.key_dim <= 64) return delta_k<T, 64>(k, stream);
+  if (k.a.key_dim <= 128) return delta_k<T, 128>(k, stream);
+  return delta_k<T, 256>(k, stream);
 }
 
 template <typename T>
 hipError_t chunks_t(const DeltaArgs& k, bool gradient, hipStream_t stream) {
   const dim3 grid((unsigned)(k.pieces * k.a.heads)), block(256);
-  if (gradient) return launch_kernel(delta_chunk_kernel<T, true>, grid, block, k, stream);
-  return launch_kernel(delta_chunk_kernel<T, false>, grid, block, k, stream);
+  if (k.a.key_dim % 8 == 0)
+    return gradient ? launch_kernel(delta_chunk_kernel<T, true, true>, grid, block, k, stream)
+                    : launch_kernel(delta_chunk_kernel<T, false, true>, grid, block, k, stream);
+  return gradient ? launch_kernel(delta_chunk_kernel<T, true, false>, grid, block, k, stream)
+                  : launch_kernel(delta_chunk_kernel<T, false, false>, grid, block, k, stream);
 }
 
 int64_t round16(int64_t floats) { return (floats + 15) / 16 * 16; }

@@ -21,54 +21,62 @@ namespace {
 // The mirror of the forward's walk: 16 NT columns of one sequence's and head's dS a workgroup, waves 0 .. 3 the chain
 // (K dS', dX, K^T dX), waves 4 .. 7 what does not wait for it: P^T do of the chunk to come and Q^T do' of this one.
 template <typename T, int KP, int NT>
-__global__ __launch_bounds__(512) void delta_back_kernel(DeltaArgs k) {
-  constexpr int N = ElemPieces<T>::n, KS = KP / 32, MT = KP / 64;
-  constexpr int kKeyPitch = KP + 8;
-  constexpr bool kStage = N == 1 || KP * N <= 256;     // K's and Q's pieces fit the LDS beside the rest
-  constexpr int kCols = 16 * NT;
-  constexpr bool kAhead = N == 1 || KP <= 128;     // K's and Q's rows of the next chunk fit the registers
-  __shared__ __attribute__((aligned(16))) uint16_t sS[kPieces][kCols][kKeyPitch], sX[kPieces][kCols][kTokenPitch],
-      sW[kPieces][kCols][kTokenPitch], sD[kPieces][kCols][kTokenPitch], sO[N][kCols][kTokenPitch],
-      sK[2][kStage ? N : 1][kStage ? kChunk : 1][kKeyPitch];
-  __shared__ f32x4 sR[4][NT][64], sQ[KP / 16][NT][64];
-  const seq_delta_args_t& a = k.a;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), r = wave & 3, lr = lane & 15, lg = lane >> 4;
-  const bool chain = wave < 4;
-  const int heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
-  const Share share = share_of(blockIdx.x, k.slices);
-  if (share.unit >= k.m.S * heads) return;
-  const int s = uniform(share.unit / heads), head = uniform(share.unit % heads), col0 = share.slice * kCols;
-  const int64_t kh = head / (heads / (int)a.key_heads);
-  Piece p;
-  p.seq = s;
-  if (k.m.offsets) {
-    const int start = uniform(seq_start(k.m, s)), stop = uniform(seq_start(k.m, s + 1));
-    p.batch = 0;
-    p.first = start;
-    p.len = max(stop - start, 0);
-  } else {
-    p.batch = s;
-    p.first = 0;
-    p.len = k.m.rows;
+struct BackLds {
+  static constexpr int N = ElemPieces<T>::n;
+  static constexpr bool kStage = N == 1 || KP * N <= 256;     // K's and Q's pieces fit beside the rest
+  uint16_t S[kPieces][16 * NT][KP + 8], X[kPieces][16 * NT][kTokenPitch], W[kPieces][16 * NT][kTokenPitch],
+      D[kPieces][16 * NT][kTokenPitch], O[N][16 * NT][kTokenPitch], K[kStage ? N : 1][kStage ? kChunk : 1][KP + 8],
+      Q[kStage ? N : 1][kStage ? kChunk : 1][KP + 8];
+  f32x4 back[KP / 16][NT][64];       // Q^T do', each lane's as the chain's lane takes it
+  // P^T do of the chunk to come, where the chain's wave r is to put its part of dZ: in X, free from the one exchange to
+  // the other.
+  __device__ __forceinline__ f32x4& inner(int r, int t, int lane) {
+    return *reinterpret_cast<f32x4*>(&X[lane >> 5][16 * t + (lane & 15)][16 * r + 8 * ((lane >> 4) & 1)]);
   }
-  const int chunks = (p.len + kChunk - 1) >> kChunkShift;
-  const int64_t number = chunk_head(k, chunk_number(k.m, s, (int)p.first, 0), head);
-  const int64_t place = ((int64_t)s * heads + head) * Dk * Dv;
+};
+template <class Lds, int KP>
+constexpr int back_waves() { return sizeof(Lds) <= 80 * 1024 && KP <= 128 ? 4 : 2; }
 
-  f32x4 S[MT][NT];
-  if (chain) {
+// Operand of K^T or Q^T: rows are the state's, terms are tokens.
+template <typename T, int KP, bool STAGED>
+__device__ __forceinline__ void transposed(const uint16_t* staged, int plane, const ChunkRows<const T>& from, int n, int Dk, int m,
+                                           int c, int lane, s16x8 (&e)[ElemPieces<T>::n]) {
+  constexpr int N = ElemPieces<T>::n;
+  if constexpr (STAGED) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int i = 0; i < N; ++i)
+      e[i] = lds8_trans(staged + i * plane + 32 * c * (KP + 8) + 16 * m + trans_place(lane, KP + 8), KP + 8);
+  } else {
+    float g[8];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int c = col0 + 16 * t + lr;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = 16 * (r * MT + m) + 4 * lg + x;
-          S[m][t][x] = k.last && row < Dk && c < Dv ? at_lane(k.last + place, row * Dv + c) : 0.f;
-        }
-      }
+    for (int i = 0; i < 8; ++i) {
+      const int t = opaque(32 * c + 8 * (lane >> 4)) + i, row = 16 * m + (lane & 15);
+      g[i] = t < n && row < Dk ? to_f32(from.at(t, row)) : 0.f;
+    }
+    split8<N>(g, e);
   }
+}
+
+template <typename T, int KP, int NT, bool WHOLE>
+__device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, BackLds<T, KP, NT>& L, int r, int lane) {
+  typedef BackLds<T, KP, NT> Lds;
+  constexpr int N = Lds::N, KS = KP / 32, MT = KP / 64;
+  constexpr bool kAhead = N == 1 || KP <= 128;
+  const seq_delta_args_t& a = k.a;
+  const int lr = lane & 15, lg = lane >> 4, heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
+  const int64_t place = ((int64_t)w.seq * heads + w.head) * Dk * Dv;
+  f32x4 S[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int c = w.col0 + 16 * t + lr;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int row = 16 * (r * MT + m) + 4 * lg + x;
+        S[m][t][x] = k.last && (WHOLE || row < Dk) && c < Dv ? at_lane(k.last + place, row * Dv + c) : 0.f;
+      }
+    }
   auto share_state = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -77,38 +85,34 @@ __global__ __launch_bounds__(512) void delta_back_kernel(DeltaArgs k) {
         uint2 u[kPieces];
         split4<kPieces>(S[m][t], u);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          *reinterpret_cast<uint2*>(&sS[i][16 * t + lr][16 * (r * MT + m) + 4 * lg]) = u[i];
+        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.S[i][16 * t + lr][16 * (r * MT + m) + 4 * lg]) = u[i];
       }
   };
   auto keep_state = [&](float* to) __attribute__((always_inline)) {
+    const int row0 = opaque(16 * MT * r + 4 * lg);
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int t = 0; t < NT; ++t) {
+      const int c = w.col0 + 16 * t + lr;
+      if (c < Dv) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int c = col0 + 16 * t + lr;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = 16 * (r * MT + m) + 4 * lg + x;
-          if (row < Dk && c < Dv) at_lane(to, row * Dv + c) = S[m][t][x];
-        }
+          for (int x = 0; x < 4; ++x)
+            if (WHOLE || row0 + 16 * m + x < Dk) at_lane(to, (row0 + 16 * m + x) * Dv + c) = S[m][t][x];
       }
+    }
   };
-
-  Eight<T> rows[kAhead ? KS : 1];                 // chain: K, beside: Q
-  T now[NT][4], next[NT][4];         // beside: do of this chunk and of the one to come
-  s16x8 square[2][kPieces];          // chain: (1 + M)^-T, beside: P^T of the chunk to come
+  Eight<T> rows[kAhead ? KS : 1];
+  s16x8 square[2][kPieces];
   float4 first, last;
   float whole;
-  auto load_row = [&](int j, int c, Eight<T>& to) __attribute__((always_inline)) {
-    const int n = p.len - kChunk * j, t = 16 * r + lr;
-    const ChunkRows<const T> from(chain ? a.k : a.q, kh * (chain ? a.k_head : a.q_head), p, kChunk * j);
-    to.load(&from.at(min(t, n - 1), 32 * c + 8 * lg), t < n ? Dk - 32 * c - 8 * lg : 0);
+  auto keys = [&](int j) __attribute__((always_inline)) {
+    return ChunkRows<const T>(a.k, w.key_head * a.k_head, w.p, kChunk * j);
   };
   auto load_rows = [&](int j) __attribute__((always_inline)) {
     if constexpr (kAhead) {
 #pragma unroll
-      for (int c = 0; c < KS; ++c) load_row(j, c, rows[c]);
+      for (int c = 0; c < KS; ++c) load_row<T, KP, WHOLE>(keys(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, rows[c]);
     }
   };
   auto row_pieces = [&](int j, int c, s16x8 (&e)[N]) __attribute__((always_inline)) {
@@ -116,263 +120,313 @@ __global__ __launch_bounds__(512) void delta_back_kernel(DeltaArgs k) {
       rows[c].pieces(e);
     } else {
       Eight<T> row;
-      load_row(j, c, row);
+      load_row<T, KP, WHOLE>(keys(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, row);
       row.pieces(e);
     }
   };
-  auto load_do = [&](int j, T (&v)[NT][4]) __attribute__((always_inline)) {
-    const int n = p.len - kChunk * j;
-    const ChunkRows<const T> from(k.dout, head * k.dout_head, p, kChunk * j);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int t = 16 * r + 4 * lg + x;
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        const int col = col0 + 16 * c + lr;
-        if (t < n && col < Dv) v[c][x] = from.at(t, col);
-        else from_f32(0.f, v[c][x]);
-      }
-    }
-  };
   auto load_square = [&](int j) __attribute__((always_inline)) {
-    const uint16_t* from = (chain ? k.inverse : k.inner) + (number + (int64_t)j * heads) * kMatrix + lane * 8;
+    const uint16_t* from = k.inverse + (w.number + (int64_t)j * heads) * kMatrix;
 #pragma unroll
     for (int c = 0; c < 2; ++c)
-      if (c >= r / 2) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i)
-          square[c][i] = *reinterpret_cast<const s16x8*>(from + (upper_frag(r, c) * kPieces + i) * kFragElems);
-      }
+      for (int i = 0; i < kPieces; ++i)
+        square[c][i] = *reinterpret_cast<const s16x8*>(&at_lane(from + (upper_frag(r, max(c, r / 2)) * kPieces + i) * kFragElems, lane * 8));
   };
   auto load_decay = [&](int j) __attribute__((always_inline)) {
-    const float* from = k.decay + (number + (int64_t)j * heads) * 2 * kChunk;
+    const float* from = k.decay + (w.number + (int64_t)j * heads) * 2 * kChunk;
     first = *reinterpret_cast<const float4*>(from + 16 * r + 4 * lg);
     last = *reinterpret_cast<const float4*>(from + kChunk + 16 * r + 4 * lg);
     whole = from[kChunk - 1];
   };
-  // beside: do as an operand
-  auto share_do = [&](const T (&v)[NT][4]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      uint2 u[N];
-      split4<N>(f32x4{to_f32(v[t][0]), to_f32(v[t][1]), to_f32(v[t][2]), to_f32(v[t][3])}, u);
-#pragma unroll
-      for (int i = 0; i < N; ++i) *reinterpret_cast<uint2*>(&sO[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
-    }
-  };
-  // beside: P^T do
-  auto inner_part = [&]() __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      f32x4 lead = zero4(), rest = zero4();
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        if (c >= r / 2) {
-          s16x8 b[N];
-#pragma unroll
-          for (int i = 0; i < N; ++i) b[i] = lds8(&sO[i][16 * t + lr][32 * c + 8 * lg]);
-          mfma_pieces<kPieces>(square[c], b, lead, rest);
-        }
-      sR[r][t][lane] = lead + rest;
-    }
-  };
-  // Operand of K^T or Q^T: rows of the state, terms are tokens.
-  auto transposed = [&](int which, const seq_view_t& view, int64_t at, int j, int m, int c, s16x8 (&e)[N]) __attribute__((always_inline)) {
-    if constexpr (kStage) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) e[i] = lds8_trans(&sK[which][i][32 * c][16 * m] + trans_place(lane, kKeyPitch), kKeyPitch);
-    } else {
-      const ChunkRows<const T> from(view, at, p, kChunk * j);
-      float g[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int t = opaque(32 * c + 8 * lg) + i, row = 16 * m + lr;
-        g[i] = kChunk * j + t < p.len && row < Dk ? to_f32(from.at(t, row)) : 0.f;
-      }
-      split8<N>(g, e);
-    }
-  };
-
-  if (chunks > 0) {
-    load_rows(chunks - 1);
-    load_square(chunks - 1);
-    load_decay(chunks - 1);
-    if (!chain) {
-      load_do(chunks - 1, now);
-      share_do(now);
-      if (chunks > 1) load_do(chunks - 2, next);
-    }
+  if (w.chunks > 0) {
+    load_rows(w.chunks - 1);
+    load_decay(w.chunks - 1);
+    load_square(w.chunks - 1);
   }
-  if (chain) share_state();
+  share_state();
   lds_barrier();
-  if (chunks > 0 && !chain) {
-    inner_part();
-    if (chunks > 1) load_square(chunks - 2);
-  }
   lds_barrier();
-
-  for (int j = chunks - 1; j >= 0; --j) {
-    const int n = p.len - kChunk * j;
-    const bool more = j > 0;
+#pragma unroll 1
+  for (int j = w.chunks - 1; j >= 0; --j) {
+    const int n = w.p.len - kChunk * j, next = max(j - 1, 0);
     const float f[4] = {first.x, first.y, first.z, first.w}, l[4] = {last.x, last.y, last.z, last.w};
     const float keep = whole;
-    if (chain) {
-      keep_state(k.dstates + (number + (int64_t)j * heads) * Dk * Dv);
-      f32x4 lead[NT], rest[NT];
+    keep_state(k.dstates + (w.number + (int64_t)j * heads) * Dk * Dv);
+    // dZ
+    {
+      f32x4 sum[NT][kPieces];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) lead[t] = rest[t] = zero4();
+      for (int t = 0; t < NT; ++t) clear(sum[t]);
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
         s16x8 e[N];
         row_pieces(j, c, e);
-        if (kStage) {
+        if (Lds::kStage && N > 1) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) *reinterpret_cast<s16x8*>(&sK[0][i][kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[i];
+          for (int i = 0; i < N; ++i) *reinterpret_cast<s16x8*>(&L.K[i][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[i];
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           s16x8 b[kPieces];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&sS[i][16 * t + lr][32 * c + 8 * lg]);
-          mfma_pieces<kPieces>(e, b, lead[t], rest[t]);
+          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.S[i][16 * t + lr][32 * c + 8 * lg]);
+          mfma_pieces<kPieces>(e, b, sum[t]);
         }
+        if (c & 1) __builtin_amdgcn_sched_barrier(0);
       }
-      if (more) load_rows(j - 1);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        f32x4 z = sR[r][t][lane];
+        const f32x4 kS = total(sum[t]);
+        f32x4 z = L.inner(r, t, lane);
         uint2 u[kPieces];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = __builtin_fmaf(l[i], lead[t][i] + rest[t][i], z[i]);
+        for (int i = 0; i < 4; ++i) z[i] = 16 * r + 4 * lg + i < n ? __builtin_fmaf(l[i], kS[i], z[i]) : 0.f;
         split4<kPieces>(z, u);
+        wave_sync();                 // what `inner` holds is read by then
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&sX[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
-      }
-    } else {
-      if (kStage) {
-#pragma unroll
-        for (int c = 0; c < KS; ++c) {
-          s16x8 e[N];
-          row_pieces(j, c, e);
-#pragma unroll
-          for (int i = 0; i < N; ++i) *reinterpret_cast<s16x8*>(&sK[1][i][kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[i];
-        }
-        if (more) load_rows(j - 1);
-      }
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        f32x4 x;
-        uint2 u[kPieces];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = a.scale * f[i] * to_f32(now[t][i]);
-        split4<kPieces>(x, u);
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&sD[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
-      }
-      if (more) {
-        share_do(next);
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) now[t][i] = next[t][i];
-        if (j > 1) load_do(j - 2, next);
-        load_decay(j - 1);
+        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.X[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
       }
     }
     lds_barrier();
-    if (chain) {
-      f32x4 dx[NT];
+    if (Lds::kStage && N == 1) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        f32x4 lead = zero4(), rest = zero4();
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          if (c >= r / 2) {
-            s16x8 b[kPieces];
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) b[i] = lds8(&sX[i][16 * t + lr][32 * c + 8 * lg]);
-            mfma_pieces<kPieces>(square[c], b, lead, rest);
-          }
-        dx[t] = lead + rest;
-        f32x4 x;
-        uint2 u[kPieces];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = -f[i] * dx[t][i];
-        split4<kPieces>(x, u);
-#pragma unroll
-        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&sW[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
-      }
-      if (more) {
-        load_square(j - 1);
-        load_decay(j - 1);
-      }
-      const int64_t at = ((p.batch * k.m.rows + p.first + kChunk * j) * heads + head) * Dv + col0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * r + 4 * lg + i;
-#pragma unroll
-        for (int c = 0; c < NT; ++c)
-          if (t < n && col0 + 16 * c + lr < Dv) {
-            at_lane(k.dx + at, t * heads * Dv + 16 * c + lr) = dx[c][i];
-            from_f32(dx[c][i], at_lane(static_cast<T*>(k.dv) + at, t * heads * Dv + 16 * c + lr));
-          }
-      }
-    } else {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        f32x4 lead[NT], rest[NT];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) lead[t] = rest[t] = zero4();
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          s16x8 e[N];
-          transposed(1, a.q, kh * a.q_head, j, r * MT + m, c, e);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            s16x8 b[kPieces];
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) b[i] = lds8(&sD[i][16 * t + lr][32 * c + 8 * lg]);
-            mfma_pieces<kPieces>(e, b, lead[t], rest[t]);
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) sQ[r * MT + m][t][lane] = lead[t] + rest[t];
+      for (int c = 0; c < KS; ++c) {
+        s16x8 e[N];
+        row_pieces(j, c, e);
+        *reinterpret_cast<s16x8*>(&L.K[0][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[0];
       }
     }
-    lds_barrier();
-    if (chain) {
+    // dX
+    f32x4 dx[NT];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        f32x4 low[NT];
+    for (int t = 0; t < NT; ++t) {
+      f32x4 sum[kPieces];
+      clear(sum);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (c >= r / 2) {
+          s16x8 b[kPieces];
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.X[i][16 * t + lr][32 * c + 8 * lg]);
+          mfma_pieces<kPieces>(square[c], b, sum);
+        }
+      dx[t] = total(sum);
+      f32x4 x;
+      uint2 u[kPieces];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = -f[i] * dx[t][i];
+      split4<kPieces>(x, u);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.W[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
+    }
+    lds_barrier();
+    {
+      const int64_t at = ((w.p.batch * k.m.rows + w.p.first + kChunk * j) * heads + w.head) * Dv + w.col0;
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+        if (w.col0 + 16 * c + lr < Dv) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = opaque(16 * r + 4 * lg) + i;
+            if (t < n) {
+              at_lane(k.dx + at, t * heads * Dv + 16 * c + lr) = dx[c][i];
+              from_f32(dx[c][i], at_lane(static_cast<T*>(k.dv) + at, t * heads * Dv + 16 * c + lr));
+            }
+          }
+        }
+    }
+    load_rows(next);
+    load_decay(next);
+    // dS
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      f32x4 sum[NT][kPieces];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        clear(sum[t]);
+        sum[t][1] = L.back[r * MT + m][t][lane];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sum[t][0][x] = keep * S[m][t][x];
+      }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        s16x8 e[N];
+        transposed<T, KP, Lds::kStage>(&L.K[0][0][0], sizeof(L.K[0]) / 2, keys(j), n, Dk, r * MT + m, c, lane, e);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          low[t] = sQ[r * MT + m][t][lane];
+          s16x8 b[kPieces];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) S[m][t][x] *= keep;
+          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.W[i][16 * t + lr][32 * c + 8 * lg]);
+          mfma_pieces<kPieces>(e, b, sum[t]);
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          s16x8 e[N];
-          transposed(0, a.k, kh * a.k_head, j, r * MT + m, c, e);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            s16x8 b[kPieces];
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) b[i] = lds8(&sW[i][16 * t + lr][32 * c + 8 * lg]);
-            mfma_pieces<kPieces>(e, b, S[m][t], low[t]);
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) S[m][t] += low[t];
       }
-      share_state();
-    } else if (more) {
-      inner_part();
-      if (j > 1) load_square(j - 2);
+#pragma unroll
+      for (int t = 0; t < NT; ++t) S[m][t] = total(sum[t]);
     }
+    __builtin_amdgcn_sched_barrier(0);       // the sums' registers are free by now
+    load_square(next);
+    share_state();
     lds_barrier();
   }
-  if (chain && k.dstate) keep_state(k.dstate + place);
+  if (k.dstate) keep_state(k.dstate + place);
+}
+
+template <typename T, int KP, int NT, bool WHOLE>
+__device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, BackLds<T, KP, NT>& L, int r, int lane) {
+  typedef BackLds<T, KP, NT> Lds;
+  constexpr int N = Lds::N, KS = KP / 32, MT = KP / 64;
+  constexpr bool kAhead = N == 1 || KP <= 128;
+  const seq_delta_args_t& a = k.a;
+  const int lr = lane & 15, lg = lane >> 4, heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
+  Eight<T> rows[kAhead ? KS : 1];
+  T now[NT][4], next[NT][4];         // do of this chunk and of the one to come
+  s16x8 square[2][kPieces];
+  float4 first;
+  auto queries = [&](int j) __attribute__((always_inline)) {
+    return ChunkRows<const T>(a.q, w.key_head * a.q_head, w.p, kChunk * j);
+  };
+  auto load_rows = [&](int j) __attribute__((always_inline)) {
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int c = 0; c < KS; ++c) load_row<T, KP, WHOLE>(queries(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, rows[c]);
+    }
+  };
+  auto load_do = [&](int j, T (&v)[NT][4]) __attribute__((always_inline)) {
+    const int n = w.p.len - kChunk * j;
+    const ChunkRows<const T> from(k.dout, w.head * k.dout_head, w.p, kChunk * j);
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) v[t][x] = from.at(min(16 * r + 4 * lg + x, n - 1), min(w.col0 + 16 * t + lr, Dv - 1));
+  };
+  auto load_square = [&](int j) __attribute__((always_inline)) {
+    const uint16_t* from = k.inner + (w.number + (int64_t)j * heads) * kMatrix;
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i)
+        square[c][i] = *reinterpret_cast<const s16x8*>(&at_lane(from + (upper_frag(r, max(c, r / 2)) * kPieces + i) * kFragElems, lane * 8));
+  };
+  auto load_decay = [&](int j) __attribute__((always_inline)) {
+    first = *reinterpret_cast<const float4*>(k.decay + (w.number + (int64_t)j * heads) * 2 * kChunk + 16 * r + 4 * lg);
+  };
+  // do of chunk j times a number per token, zeros past the sequence's end
+  auto values = [&](int j, const T (&v)[NT][4], int t, float (&by)[4]) __attribute__((always_inline)) {
+    f32x4 x;
+    const int n = w.p.len - kChunk * j;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = 16 * r + 4 * lg + i < n && w.col0 + 16 * t + lr < Dv ? by[i] * to_f32(v[t][i]) : 0.f;
+    return x;
+  };
+  auto share_do = [&](int j, const T (&v)[NT][4]) __attribute__((always_inline)) {
+    float one[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      uint2 u[N];
+      split4<N>(values(j, v, t, one), u);
+#pragma unroll
+      for (int i = 0; i < N; ++i) *reinterpret_cast<uint2*>(&L.O[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
+    }
+  };
+  auto inner_part = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      f32x4 sum[kPieces];
+      clear(sum);
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        if (c >= r / 2) {
+          s16x8 b[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) b[i] = lds8(&L.O[i][16 * t + lr][32 * c + 8 * lg]);
+          mfma_pieces<kPieces>(square[c], b, sum);
+        }
+      L.inner(r, t, lane) = total(sum);
+    }
+  };
+  if (w.chunks > 0) {
+    load_do(w.chunks - 1, now);
+    load_square(w.chunks - 1);
+    load_rows(w.chunks - 1);
+    load_decay(w.chunks - 1);
+    load_do(max(w.chunks - 2, 0), next);
+    share_do(w.chunks - 1, now);
+  }
+  lds_barrier();
+  if (w.chunks > 0) {
+    inner_part();
+    load_square(max(w.chunks - 2, 0));
+  }
+  lds_barrier();
+#pragma unroll 1
+  for (int j = w.chunks - 1; j >= 0; --j) {
+    const int n = w.p.len - kChunk * j, after = max(j - 1, 0);
+    if (Lds::kStage) {
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        s16x8 e[N];
+        rows[kAhead ? c : 0].pieces(e);
+#pragma unroll
+        for (int i = 0; i < N; ++i) *reinterpret_cast<s16x8*>(&L.Q[i][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[i];
+      }
+    }
+    {
+      float by[4] = {a.scale * first.x, a.scale * first.y, a.scale * first.z, a.scale * first.w};
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        uint2 u[kPieces];
+        split4<kPieces>(values(j, now, t, by), u);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.D[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
+      }
+    }
+    share_do(after, next);
+    lds_barrier();
+    load_rows(after);
+    load_decay(after);
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) now[t][i] = next[t][i];
+    load_do(max(j - 2, 0), next);
+    // Q^T do'
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      f32x4 sum[NT][kPieces];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) clear(sum[t]);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        s16x8 e[N];
+        transposed<T, KP, Lds::kStage>(&L.Q[0][0][0], sizeof(L.Q[0]) / 2, queries(j), n, Dk, r * MT + m, c, lane, e);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          s16x8 b[kPieces];
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.D[i][16 * t + lr][32 * c + 8 * lg]);
+          mfma_pieces<kPieces>(e, b, sum[t]);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) L.back[r * MT + m][t][lane] = total(sum[t]);
+    }
+    lds_barrier();
+    inner_part();                    // of the chunk to come; after the first chunk nobody takes it
+    load_square(max(j - 2, 0));
+    lds_barrier();
+  }
+}
+
+template <typename T, int KP, int NT, bool WHOLE>
+__global__ __launch_bounds__(512, (back_waves<BackLds<T, KP, NT>, KP>())) void delta_back_kernel(DeltaArgs k) {
+  typedef BackLds<T, KP, NT> Lds;
+  __shared__ __attribute__((aligned(16))) char bytes[sizeof(Lds)];
+  Lds& L = *reinterpret_cast<Lds*>(bytes);
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  Walk w;
+  if (!find_walk<16 * NT>(k, w)) return;
+  if (wave < 4) back_chain<T, KP, NT, WHOLE>(k, w, L, wave, lane);
+  else back_beside<T, KP, NT, WHOLE>(k, w, L, wave - 4, lane);
 }
 
 // ---- queries, keys and decays -----------------------------------------------------------------------------------------
@@ -538,11 +592,11 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
         s16x8 b[kPieces];
 #pragma unroll
         for (int e = 0; e < kPieces; ++e) b[e] = lds8(&L.panels.S[e][16 * (tile0 + t) + lr][8 * lg]);
-        mfma_pieces<kPieces>(o, b, Q[t], Q[t]);
-        mfma_pieces<kPieces>(x, b, R[t], R[t]);
+        mfma_pieces<kPieces>(o, b, Q[t]);
+        mfma_pieces<kPieces>(x, b, R[t]);
 #pragma unroll
         for (int e = 0; e < kPieces; ++e) b[e] = lds8(&L.panels.D[e][16 * (tile0 + t) + lr][8 * lg]);
-        mfma_pieces<kPieces>(z, b, W[t], W[t]);
+        mfma_pieces<kPieces>(z, b, W[t]);
         if (t & 1) __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -551,8 +605,8 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
           s16x8 b[kPieces];
 #pragma unroll
           for (int e = 0; e < kPieces; ++e) b[e] = lds8(&L.panels.Z[e][16 * t + lr][8 * lg]);
-          if (part == 0) mfma_pieces<kPieces>(o, b, oz[t], oz[t]);
-          if (part == kParts - 1) mfma_pieces<kPieces>(x, b, xz[t], xz[t]);
+          if (part == 0) mfma_pieces<kPieces>(o, b, oz[t]);
+          if (part == kParts - 1) mfma_pieces<kPieces>(x, b, xz[t]);
         }
       __syncthreads();
     }
@@ -629,8 +683,8 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
         for (int t = 0; t < KT; ++t) {
           s16x8 b[N];
           transposed(staged_key, key, t, c, b);
-          mfma_pieces<kPieces>(e, b, Q[t], Q[t]);
-          mfma_pieces<kPieces>(x, b, R[t], R[t]);
+          mfma_pieces<kPieces>(e, b, Q[t]);
+          mfma_pieces<kPieces>(x, b, R[t]);
           if (!Lds::kStage) __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -662,9 +716,9 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
         for (int t = 0; t < KT; ++t) {
           s16x8 b[N];
           transposed(staged_query, query, t, c, b);
-          mfma_pieces<kPieces>(e, b, W[t], W[t]);
+          mfma_pieces<kPieces>(e, b, W[t]);
           transposed(staged_key, key, t, c, b);
-          mfma_pieces<kPieces>(x, b, W[t], W[t]);
+          mfma_pieces<kPieces>(x, b, W[t]);
           if (!Lds::kStage) __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -747,7 +801,8 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
 template <typename T, int KP>
 hipError_t grad_n(const DeltaArgs& k, hipStream_t stream) {
   const dim3 order((unsigned)shares(k.a.tokens.sequences * k.a.heads, k.slices));
-  const hipError_t err = launch_kernel(delta_back_kernel<T, KP, 1>, order, dim3(512), k, stream);
+  const hipError_t err = k.a.key_dim == KP ? launch_kernel(delta_back_kernel<T, KP, 1, true>, order, dim3(512), k, stream)
+                                           : launch_kernel(delta_back_kernel<T, KP, 1, false>, order, dim3(512), k, stream);
   if (err != hipSuccess || seq_rows(k.a.tokens) == 0) return err;
   const dim3 grid((unsigned)(k.pieces * k.a.key_heads)), block(KP > 64 ? 512 : 256);
   const int group = (int)(k.a.heads / k.a.key_heads);
