@@ -123,18 +123,24 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void delta_chunk_kerne
       }
   }
   __syncthreads();
+  {
+    const f32x4 hi = *reinterpret_cast<const f32x4*>(&d.hi[16 * r + 4 * lg]), lo = *reinterpret_cast<const f32x4*>(&d.lo[16 * r + 4 * lg]);
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int j = 16 * t + lr;
+    for (int t = 0; t < 4; ++t) {
+      if (t > r) continue;
+      const int j = 16 * t + lr;
+      const float hj = d.hi[j], lj = d.lo[j], beta = d.beta[j], scaled = a.scale * beta;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int i = 16 * r + 4 * lg + x;
-      const bool live = t <= r && i < n && j <= i;
-      const float e = live ? decay_between(d, i, j) * d.beta[j] : 0.f;
-      M[i][j] = live && j < i ? e * kk[t][x] : 0.f;
-      I[i][j] = 0.f;
-      qk[t][x] = live ? e * qk[t][x] * a.scale : 0.f;
+      for (int x = 0; x < 4; ++x) {
+        const int i = 16 * r + 4 * lg + x;
+        const bool live = i < n && j <= i;
+        const float e = exp_of(hi[x] - hj, lo[x] - lj);
+        M[i][j] = live && j < i ? e * beta * kk[t][x] : 0.f;
+        qk[t][x] = live ? e * scaled * qk[t][x] : 0.f;
+      }
     }
+    // The blocks beside the diagonal's that share an operand block with it.
+    if ((r & 1) == 0) block_store(I, 16 * r, 16 * r + 16, lane, zero4(), 1.f);
   }
   wave_sync();                       // a diagonal block is read by the wave that wrote it
   {
@@ -159,18 +165,20 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void delta_chunk_kerne
   __syncthreads();
   {
     const int u = 16 * (r >> 1), v = 16 * (r & 1);
-    f32x4 y = block_product(M, 32 + u, 0, I, 0, v, lane, zero4());
+    f32x4 y = zero4();
+    if (v == 0) y = block_product(M, 32 + u, 0, I, 0, 0, lane, y);
     y = block_product(M, 32 + u, 16, I, 16, v, lane, y);
     block_store(M, u, 32 + v, lane, y, 1.f);
     __syncthreads();
     f32x4 z = block_product(I, 32 + u, 32, M, 0, 32 + v, lane, zero4());
-    z = block_product(I, 32 + u, 48, M, 16, 32 + v, lane, z);
+    if (u == 16) z = block_product(I, 48, 48, M, 16, 32 + v, lane, z);
     block_store(I, 32 + u, v, lane, z, -1.f);
   }
   __syncthreads();
   // M has served: P takes its place.
 #pragma unroll
-  for (int t = 0; t < 4; ++t) block_store(M, 16 * r, 16 * t, lane, qk[t], 1.f);
+  for (int t = 0; t < 4; ++t)
+    if (t <= (r | 1)) block_store(M, 16 * r, 16 * t, lane, qk[t], 1.f);      // zero past the diagonal
   if (GRAD) __syncthreads();         // columns are read, of all waves' rows
   else wave_sync();
   const int row = 16 * r + lr;
@@ -187,14 +195,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void delta_chunk_kerne
       fi[i] = GRAD ? I[c][row] : I[row][c];
       fp[i] = GRAD ? M[c][row] : M[row][c];
     }
-    s16x8 pi[kPieces], pp[kPieces];
+    constexpr int NP = GRAD ? kPieces : OutPieces<T>::n;
+    s16x8 pi[kPieces], pp[NP];
     split8<kPieces>(fi, pi);
-    split8<kPieces>(fp, pp);
+    split8<NP>(fp, pp);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
-      *reinterpret_cast<s16x8*>(inv + (b * kPieces + i) * kFragElems + lane * 8) = pi[i];
-      *reinterpret_cast<s16x8*>(inn + (b * kPieces + i) * kFragElems + lane * 8) = pp[i];
-    }
+    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<s16x8*>(&at_lane(inv + (b * kPieces + i) * kFragElems, lane * 8)) = pi[i];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) *reinterpret_cast<s16x8*>(&at_lane(inn + (b * kPieces + i) * kFragElems, lane * 8)) = pp[i];
   }
 }
 
@@ -343,6 +351,15 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
         }
         if (c & 1) __builtin_amdgcn_sched_barrier(0);     // two blocks' operands in registers at a time
       }
+      if (Lds::kStage && N == 1) {
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          s16x8 e[N];
+          row_pieces(j, c, e);
+          *reinterpret_cast<s16x8*>(&L.K[0][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[0];
+        }
+      }
+      load_rows(next);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const f32x4 kS = total(sum[t]);
@@ -358,15 +375,8 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
         for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.X[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
       }
     }
+    load_values(next);
     lds_barrier();
-    if (Lds::kStage && N == 1) {
-#pragma unroll
-      for (int c = 0; c < KS; ++c) {
-        s16x8 e[N];
-        row_pieces(j, c, e);
-        *reinterpret_cast<s16x8*>(&L.K[0][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[0];
-      }
-    }
     // Z = (1 + M)^-1 X
     f32x4 z[NT];
 #pragma unroll
@@ -407,9 +417,8 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
           }
         }
     }
-    load_rows(next);
-    load_values(next);
     load_decay(next);
+    if (N == 1) load_square(next);
     // S' = e^G_C S + K^T W
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -447,8 +456,10 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
 #pragma unroll
       for (int t = 0; t < NT; ++t) S[m][t] = total(sum[t]);
     }
-    __builtin_amdgcn_sched_barrier(0);       // the sums' registers are free by now
-    load_square(next);
+    if (N > 1) {                             // the sums' registers are free by now
+      __builtin_amdgcn_sched_barrier(0);
+      load_square(next);
+    }
     share_state();
     lds_barrier();
   }

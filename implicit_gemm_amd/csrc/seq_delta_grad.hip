@@ -35,7 +35,7 @@ struct BackLds {
   }
 };
 template <class Lds, int KP>
-constexpr int back_waves() { return sizeof(Lds) <= 80 * 1024 && KP <= 128 ? 4 : 2; }
+constexpr int back_waves() { return sizeof(Lds) <= 80 * 1024 && KP <= 128 && Lds::kStage ? 4 : 2; }
 
 // Operand of K^T or Q^T: rows are the state's, terms are tokens.
 template <typename T, int KP, bool STAGED>
@@ -174,6 +174,15 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
         }
         if (c & 1) __builtin_amdgcn_sched_barrier(0);
       }
+      if (Lds::kStage && N == 1) {
+#pragma unroll
+        for (int c = 0; c < KS; ++c) {
+          s16x8 e[N];
+          row_pieces(j, c, e);
+          *reinterpret_cast<s16x8*>(&L.K[0][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[0];
+        }
+      }
+      load_rows(next);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const f32x4 kS = total(sum[t]);
@@ -188,14 +197,6 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
       }
     }
     lds_barrier();
-    if (Lds::kStage && N == 1) {
-#pragma unroll
-      for (int c = 0; c < KS; ++c) {
-        s16x8 e[N];
-        row_pieces(j, c, e);
-        *reinterpret_cast<s16x8*>(&L.K[0][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[0];
-      }
-    }
     // dX
     f32x4 dx[NT];
 #pragma unroll
@@ -235,8 +236,8 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
           }
         }
     }
-    load_rows(next);
     load_decay(next);
+    load_square(next);
     // dS
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -263,8 +264,6 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
 #pragma unroll
       for (int t = 0; t < NT; ++t) S[m][t] = total(sum[t]);
     }
-    __builtin_amdgcn_sched_barrier(0);       // the sums' registers are free by now
-    load_square(next);
     share_state();
     lds_barrier();
   }
