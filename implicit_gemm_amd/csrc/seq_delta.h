@@ -112,6 +112,10 @@ struct Eight {
     if (n > 0) raw.load_n(p, n);
     else raw.clear();
   }
+  __device__ __forceinline__ void put(T* p) const {           // 16-byte aligned
+    *reinterpret_cast<uint4*>(p) = uint4{raw.u[0], raw.u[1], raw.u[2], raw.u[3]};
+    if constexpr (sizeof(T) == 4) reinterpret_cast<uint4*>(p)[1] = uint4{raw.u[4], raw.u[5], raw.u[6], raw.u[7]};
+  }
   __device__ __forceinline__ void pieces(s16x8 (&out)[ElemPieces<T>::n]) const {
     if constexpr (__is_same(T, Bf16)) {
       out[0] = __builtin_bit_cast(s16x8, uint4{raw.u[0], raw.u[1], raw.u[2], raw.u[3]});
@@ -191,6 +195,43 @@ __device__ __forceinline__ s16x8 lds8_trans(const uint16_t* p, int pitch) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
+// K or Q of a chunk in LDS as it lies in memory, a few elements' padding a row.
+template <typename T, int KP>
+struct Staged {
+  static constexpr int kPitch = KP + 16 / (int)sizeof(T);
+  alignas(16) T at[kChunk][kPitch];
+  // Its transpose as an operand: rows (columns) are dimensions 16 m .., terms are tokens 32 c ...
+  __device__ __forceinline__ void transposed(int m, int c, int lane, s16x8 (&e)[ElemPieces<T>::n]) const {
+    if constexpr (sizeof(T) == 2) {
+      const s16x8 raw = lds8_trans(reinterpret_cast<const uint16_t*>(&at[32 * c][16 * m]) + trans_place(lane, kPitch), kPitch);
+      if constexpr (__is_same(T, Bf16)) {
+        e[0] = raw;
+      } else {
+        Eight<T> v;
+        __builtin_memcpy(v.raw.u, &raw, sizeof(raw));
+        v.pieces(e);
+      }
+    } else {
+      float f[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = to_f32(at[32 * c + 8 * (lane >> 4) + i][16 * m + (lane & 15)]);
+      split8<ElemPieces<T>::n>(f, e);
+    }
+  }
+};
+// The same from memory, where the LDS is full; n tokens are the chunk's.
+template <typename T>
+__device__ __forceinline__ void transposed_rows(const ChunkRows<const T>& from, int n, int Dk, int m, int c, int lane,
+                                                s16x8 (&e)[ElemPieces<T>::n]) {
+  float f[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int t = opaque(32 * c + 8 * (lane >> 4)) + i, d = 16 * m + (lane & 15);
+    f[i] = t < n && d < Dk ? to_f32(from.at(t, d)) : 0.f;
+  }
+  split8<ElemPieces<T>::n>(f, e);
+}
+
 // Block (row tile r of 16, terms 32 s ..) of a lower triangular matrix, and of an upper one.
 __host__ __device__ constexpr int lower_frag(int r, int s) { return r < 2 ? r : 2 * r - 2 + s; }
 __host__ __device__ constexpr int upper_frag(int r, int s) { return r < 2 ? 2 * r + s : r + 2; }
@@ -210,7 +251,7 @@ __device__ __forceinline__ float exp_of(float hi, float lo) {
 __device__ __forceinline__ float log_decay(float g) { return g < -200.f ? -200.f : g; }
 // The running sum of g as two floats (48 bits: differences of it are good to 32 bits however far it has run), e^G, e^(G_C
 // - G) and beta of a chunk's tokens, zeros behind its end.
-struct ChunkDecay {
+struct alignas(16) ChunkDecay {
   float hi[kChunk], lo[kChunk], first[kChunk], last[kChunk], beta[kChunk];
 };
 // By one wave, lane = token; n of them are the chunk's.

@@ -98,8 +98,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void delta_chunk_kerne
         ek[i].raw.clear();
         eq[i].raw.clear();
       }
-      ek[i].raw.store(&L.panel.key[row][c]);
-      eq[i].raw.store(&L.panel.query[row][c]);
+      ek[i].put(&L.panel.key[row][c]);
+      eq[i].put(&L.panel.query[row][c]);
     }
     __syncthreads();
 #pragma unroll
@@ -214,19 +214,18 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void delta_chunk_kerne
 template <typename T, int KP, int NT>
 struct WalkLds {
   static constexpr int N = ElemPieces<T>::n, NO = OutPieces<T>::n;
-  static constexpr bool kStage = N == 1 || KP <= 128;     // K's pieces fit beside the rest
   uint16_t S[kPieces][16 * NT][KP + 8], X[kPieces][16 * NT][kTokenPitch], W[kPieces][16 * NT][kTokenPitch],
-      Z[NO][16 * NT][kTokenPitch], K[kStage ? N : 1][kStage ? kChunk : 1][KP + 8];
+      Z[NO][16 * NT][kTokenPitch];
+  Staged<T, KP> K;
 };
 // Two workgroups a CU (four waves a SIMD) where their LDS and registers allow it.
 template <class Lds, int KP>
-constexpr int walk_waves() { return sizeof(Lds) <= 80 * 1024 && KP <= 128 ? 4 : 2; }
+constexpr int walk_waves() { return sizeof(Lds) <= 80 * 1024 && KP <= 128 && KP * Lds::N <= 256 ? 4 : 2; }
 
 template <typename T, int KP, int NT, bool SAVE, bool WHOLE>
 __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, WalkLds<T, KP, NT>& L, int r, int lane) {
   typedef WalkLds<T, KP, NT> Lds;
   constexpr int N = Lds::N, NO = Lds::NO, KS = KP / 32, MT = KP / 64;
-  constexpr bool kAhead = N == 1 || KP <= 128;     // the next chunk's rows fit the registers
   const seq_delta_args_t& a = k.a;
   const int lr = lane & 15, lg = lane >> 4, heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
   const int64_t slot = pool_slot(a.tokens.slots, a.tokens.pool, w.seq);
@@ -269,7 +268,7 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
       }
     }
   };
-  Eight<T> rows[kAhead ? KS : 1];
+  Eight<T> rows[KS];
   T v[NT][4];
   s16x8 square[2][kPieces];
   float4 first, last;
@@ -278,19 +277,8 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
     return ChunkRows<const T>(a.k, w.key_head * a.k_head, w.p, kChunk * j);
   };
   auto load_rows = [&](int j) __attribute__((always_inline)) {
-    if constexpr (kAhead) {
 #pragma unroll
-      for (int c = 0; c < KS; ++c) load_row<T, KP, WHOLE>(keys(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, rows[c]);
-    }
-  };
-  auto row_pieces = [&](int j, int c, s16x8 (&e)[N]) __attribute__((always_inline)) {
-    if constexpr (kAhead) {
-      rows[c].pieces(e);
-    } else {
-      Eight<T> row;
-      load_row<T, KP, WHOLE>(keys(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, row);
-      row.pieces(e);
-    }
+    for (int c = 0; c < KS; ++c) load_row<T, KP, WHOLE>(keys(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, rows[c]);
   };
   auto load_values = [&](int j) __attribute__((always_inline)) {
     const int n = w.p.len - kChunk * j;
@@ -337,11 +325,7 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
         s16x8 e[N];
-        row_pieces(j, c, e);
-        if (Lds::kStage && N > 1) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) *reinterpret_cast<s16x8*>(&L.K[i][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[i];
-        }
+        rows[c].pieces(e);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           s16x8 b[kPieces];
@@ -351,14 +335,8 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
         }
         if (c & 1) __builtin_amdgcn_sched_barrier(0);     // two blocks' operands in registers at a time
       }
-      if (Lds::kStage && N == 1) {
 #pragma unroll
-        for (int c = 0; c < KS; ++c) {
-          s16x8 e[N];
-          row_pieces(j, c, e);
-          *reinterpret_cast<s16x8*>(&L.K[0][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[0];
-        }
-      }
+      for (int c = 0; c < KS; ++c) rows[c].put(&L.K.at[16 * r + lr][32 * c + 8 * lg]);
       load_rows(next);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
@@ -432,19 +410,7 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         s16x8 e[N];
-        if constexpr (Lds::kStage) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) e[i] = lds8_trans(&L.K[i][32 * c][16 * (r * MT + m)] + trans_place(lane, KP + 8), KP + 8);
-        } else {
-          const ChunkRows<const T> key = keys(j);
-          float g[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int t = opaque(32 * c + 8 * lg) + i, row = 16 * (r * MT + m) + lr;
-            g[i] = t < n && row < Dk ? to_f32(key.at(t, row)) : 0.f;
-          }
-          split8<N>(g, e);
-        }
+        L.K.transposed(r * MT + m, c, lane, e);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           s16x8 b[kPieces];
@@ -470,20 +436,17 @@ template <typename T, int KP, int NT, bool WHOLE>
 __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, WalkLds<T, KP, NT>& L, int r, int lane) {
   typedef WalkLds<T, KP, NT> Lds;
   constexpr int N = Lds::N, NO = Lds::NO, KS = KP / 32;
-  constexpr bool kAhead = N == 1 || KP <= 128;
   const seq_delta_args_t& a = k.a;
   const int lr = lane & 15, lg = lane >> 4, heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
-  Eight<T> rows[kAhead ? KS : 1];
+  Eight<T> rows[KS];
   s16x8 square[2][NO];
   float4 first;
   auto queries = [&](int j) __attribute__((always_inline)) {
     return ChunkRows<const T>(a.q, w.key_head * a.q_head, w.p, kChunk * j);
   };
   auto load_rows = [&](int j) __attribute__((always_inline)) {
-    if constexpr (kAhead) {
 #pragma unroll
-      for (int c = 0; c < KS; ++c) load_row<T, KP, WHOLE>(queries(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, rows[c]);
-    }
+    for (int c = 0; c < KS; ++c) load_row<T, KP, WHOLE>(queries(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, rows[c]);
   };
   auto load_square = [&](int j) __attribute__((always_inline)) {
     const uint16_t* from = k.inner + (w.number + (int64_t)j * heads) * kMatrix;
@@ -512,13 +475,7 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, 
 #pragma unroll
     for (int c = 0; c < KS; ++c) {
       s16x8 e[N];
-      if constexpr (kAhead) {
-        rows[c].pieces(e);
-      } else {
-        Eight<T> row;
-        load_row<T, KP, WHOLE>(queries(j), n, 16 * r + lr, lg, Dk, c, row);
-        row.pieces(e);
-      }
+      rows[c].pieces(e);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         s16x8 b[NO];

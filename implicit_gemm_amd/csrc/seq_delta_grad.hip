@@ -23,10 +23,10 @@ namespace {
 template <typename T, int KP, int NT>
 struct BackLds {
   static constexpr int N = ElemPieces<T>::n;
-  static constexpr bool kStage = N == 1 || KP * N <= 256;     // K's and Q's pieces fit beside the rest
+  static constexpr bool kStage = sizeof(T) == 2 || KP <= 128;     // K and Q fit beside the rest
   uint16_t S[kPieces][16 * NT][KP + 8], X[kPieces][16 * NT][kTokenPitch], W[kPieces][16 * NT][kTokenPitch],
-      D[kPieces][16 * NT][kTokenPitch], O[N][16 * NT][kTokenPitch], K[kStage ? N : 1][kStage ? kChunk : 1][KP + 8],
-      Q[kStage ? N : 1][kStage ? kChunk : 1][KP + 8];
+      D[kPieces][16 * NT][kTokenPitch], O[N][16 * NT][kTokenPitch];
+  Staged<T, kStage ? KP : 0> K, Q;
   f32x4 back[KP / 16][NT][64];       // Q^T do', each lane's as the chain's lane takes it
   // P^T do of the chunk to come, where the chain's wave r is to put its part of dZ: in X, free from the one exchange to
   // the other.
@@ -34,34 +34,16 @@ struct BackLds {
     return *reinterpret_cast<f32x4*>(&X[lane >> 5][16 * t + (lane & 15)][16 * r + 8 * ((lane >> 4) & 1)]);
   }
 };
-template <class Lds, int KP>
-constexpr int back_waves() { return sizeof(Lds) <= 80 * 1024 && KP <= 128 && Lds::kStage ? 4 : 2; }
-
-// Operand of K^T or Q^T: rows are the state's, terms are tokens.
-template <typename T, int KP, bool STAGED>
-__device__ __forceinline__ void transposed(const uint16_t* staged, int plane, const ChunkRows<const T>& from, int n, int Dk, int m,
-                                           int c, int lane, s16x8 (&e)[ElemPieces<T>::n]) {
-  constexpr int N = ElemPieces<T>::n;
-  if constexpr (STAGED) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      e[i] = lds8_trans(staged + i * plane + 32 * c * (KP + 8) + 16 * m + trans_place(lane, KP + 8), KP + 8);
-  } else {
-    float g[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = opaque(32 * c + 8 * (lane >> 4)) + i, row = 16 * m + (lane & 15);
-      g[i] = t < n && row < Dk ? to_f32(from.at(t, row)) : 0.f;
-    }
-    split8<N>(g, e);
-  }
+// Two workgroups a CU (four waves a SIMD) where their LDS and registers allow it.
+template <class Lds, int KP, bool WHOLE>
+constexpr int back_waves() {
+  return sizeof(Lds) <= 80 * 1024 && KP <= 128 && (KP * Lds::N <= 128 || (KP * Lds::N <= 256 && WHOLE)) ? 4 : 2;
 }
 
 template <typename T, int KP, int NT, bool WHOLE>
 __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, BackLds<T, KP, NT>& L, int r, int lane) {
   typedef BackLds<T, KP, NT> Lds;
   constexpr int N = Lds::N, KS = KP / 32, MT = KP / 64;
-  constexpr bool kAhead = N == 1 || KP <= 128;
   const seq_delta_args_t& a = k.a;
   const int lr = lane & 15, lg = lane >> 4, heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
   const int64_t place = ((int64_t)w.seq * heads + w.head) * Dk * Dv;
@@ -102,7 +84,7 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
       }
     }
   };
-  Eight<T> rows[kAhead ? KS : 1];
+  Eight<T> rows[KS];
   s16x8 square[2][kPieces];
   float4 first, last;
   float whole;
@@ -110,19 +92,8 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
     return ChunkRows<const T>(a.k, w.key_head * a.k_head, w.p, kChunk * j);
   };
   auto load_rows = [&](int j) __attribute__((always_inline)) {
-    if constexpr (kAhead) {
 #pragma unroll
-      for (int c = 0; c < KS; ++c) load_row<T, KP, WHOLE>(keys(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, rows[c]);
-    }
-  };
-  auto row_pieces = [&](int j, int c, s16x8 (&e)[N]) __attribute__((always_inline)) {
-    if constexpr (kAhead) {
-      rows[c].pieces(e);
-    } else {
-      Eight<T> row;
-      load_row<T, KP, WHOLE>(keys(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, row);
-      row.pieces(e);
-    }
+    for (int c = 0; c < KS; ++c) load_row<T, KP, WHOLE>(keys(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, rows[c]);
   };
   auto load_square = [&](int j) __attribute__((always_inline)) {
     const uint16_t* from = k.inverse + (w.number + (int64_t)j * heads) * kMatrix;
@@ -160,11 +131,7 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
 #pragma unroll
       for (int c = 0; c < KS; ++c) {
         s16x8 e[N];
-        row_pieces(j, c, e);
-        if (Lds::kStage && N > 1) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) *reinterpret_cast<s16x8*>(&L.K[i][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[i];
-        }
+        rows[c].pieces(e);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           s16x8 b[kPieces];
@@ -174,13 +141,9 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
         }
         if (c & 1) __builtin_amdgcn_sched_barrier(0);
       }
-      if (Lds::kStage && N == 1) {
+      if constexpr (Lds::kStage) {
 #pragma unroll
-        for (int c = 0; c < KS; ++c) {
-          s16x8 e[N];
-          row_pieces(j, c, e);
-          *reinterpret_cast<s16x8*>(&L.K[0][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[0];
-        }
+        for (int c = 0; c < KS; ++c) rows[c].put(&L.K.at[16 * r + lr][32 * c + 8 * lg]);
       }
       load_rows(next);
 #pragma unroll
@@ -252,7 +215,8 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         s16x8 e[N];
-        transposed<T, KP, Lds::kStage>(&L.K[0][0][0], sizeof(L.K[0]) / 2, keys(j), n, Dk, r * MT + m, c, lane, e);
+        if constexpr (Lds::kStage) L.K.transposed(r * MT + m, c, lane, e);
+        else transposed_rows<T>(keys(j), n, Dk, r * MT + m, c, lane, e);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           s16x8 b[kPieces];
@@ -274,10 +238,9 @@ template <typename T, int KP, int NT, bool WHOLE>
 __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, BackLds<T, KP, NT>& L, int r, int lane) {
   typedef BackLds<T, KP, NT> Lds;
   constexpr int N = Lds::N, KS = KP / 32, MT = KP / 64;
-  constexpr bool kAhead = N == 1 || KP <= 128;
   const seq_delta_args_t& a = k.a;
   const int lr = lane & 15, lg = lane >> 4, heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
-  Eight<T> rows[kAhead ? KS : 1];
+  Eight<T> rows[KS];
   T now[NT][4], next[NT][4];         // do of this chunk and of the one to come
   s16x8 square[2][kPieces];
   float4 first;
@@ -285,7 +248,7 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
     return ChunkRows<const T>(a.q, w.key_head * a.q_head, w.p, kChunk * j);
   };
   auto load_rows = [&](int j) __attribute__((always_inline)) {
-    if constexpr (kAhead) {
+    if constexpr (Lds::kStage) {
 #pragma unroll
       for (int c = 0; c < KS; ++c) load_row<T, KP, WHOLE>(queries(j), w.p.len - kChunk * j, 16 * r + lr, lg, Dk, c, rows[c]);
     }
@@ -360,14 +323,9 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
 #pragma unroll 1
   for (int j = w.chunks - 1; j >= 0; --j) {
     const int n = w.p.len - kChunk * j, after = max(j - 1, 0);
-    if (Lds::kStage) {
+    if constexpr (Lds::kStage) {
 #pragma unroll
-      for (int c = 0; c < KS; ++c) {
-        s16x8 e[N];
-        rows[kAhead ? c : 0].pieces(e);
-#pragma unroll
-        for (int i = 0; i < N; ++i) *reinterpret_cast<s16x8*>(&L.Q[i][Lds::kStage ? 16 * r + lr : 0][32 * c + 8 * lg]) = e[i];
-      }
+      for (int c = 0; c < KS; ++c) rows[c].put(&L.Q.at[16 * r + lr][32 * c + 8 * lg]);
     }
     {
       float by[4] = {a.scale * first.x, a.scale * first.y, a.scale * first.z, a.scale * first.w};
@@ -397,7 +355,8 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         s16x8 e[N];
-        transposed<T, KP, Lds::kStage>(&L.Q[0][0][0], sizeof(L.Q[0]) / 2, queries(j), n, Dk, r * MT + m, c, lane, e);
+        if constexpr (Lds::kStage) L.Q.transposed(r * MT + m, c, lane, e);
+        else transposed_rows<T>(queries(j), n, Dk, r * MT + m, c, lane, e);
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           s16x8 b[kPieces];
@@ -417,7 +376,7 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
 }
 
 template <typename T, int KP, int NT, bool WHOLE>
-__global__ __launch_bounds__(512, (back_waves<BackLds<T, KP, NT>, KP>())) void delta_back_kernel(DeltaArgs k) {
+__global__ __launch_bounds__(512, (back_waves<BackLds<T, KP, NT>, KP, WHOLE>())) void delta_back_kernel(DeltaArgs k) {
   typedef BackLds<T, KP, NT> Lds;
   __shared__ __attribute__((aligned(16))) char bytes[sizeof(Lds)];
   Lds& L = *reinterpret_cast<Lds*>(bytes);
@@ -437,20 +396,30 @@ constexpr int kPanelPitch = 40;      // 16-bit elements of an LDS row of 32 colu
 
 template <typename T, int KP>
 struct InputGradLds {
-  static constexpr bool kStage = ElemPieces<T>::n == 1;
+  // K and Q lie beside the rest, or in its place after the first products, or nowhere (fp32 keys of 256 dimensions).
+  static constexpr bool kBeside = KP <= 128, kStage = kBeside || sizeof(T) == 2;
+  struct Keys {
+    Staged<T, KP> key, query;
+  };
+  struct Nothing {};
   struct Panels {
     uint16_t S[kPieces][KP][kPanelPitch], D[kPieces][KP][kPanelPitch], Z[kPieces][kChunk][kPanelPitch];
   };
   struct Squares {
     uint16_t E[kPieces][kChunk][kTokenPitch], R[kPieces][kChunk][kTokenPitch];     // [j][i]
-    uint16_t key[kStage ? kChunk : 1][KP + 8], query[kStage ? kChunk : 1][KP + 8];
+    typename std::conditional<kStage && !kBeside, Keys, Nothing>::type keys;
   };
   union {
     Panels panels;
     Squares squares;
   };
+  typename std::conditional<kBeside, Keys, Nothing>::type beside;
   ChunkDecay d;
   float dots[2][kChunk], db[2][kChunk], part[8];
+  __device__ __forceinline__ Keys& keys() {
+    if constexpr (kBeside) return beside;
+    else return squares.keys;
+  }
 };
 
 template <bool FIRST, class A, class B>
@@ -460,7 +429,7 @@ __device__ __forceinline__ auto& pick(A& a, B& b) {
 }
 
 // How the value heads of a key head are gone through: there is one, all in one launch with the sums in registers, or a
-// launch each with the sums in the workspace (keys of 256 dimensions leave no registers for them).
+// launch each with the sums in the workspace (keys of 256 dimensions leave no registers for them, one head or more).
 enum Sharing { kAlone, kTogether, kInTurn };
 
 template <typename T, int KP, Sharing SHARING>
@@ -503,30 +472,37 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
   }
   const ChunkRows<const T> key(a.k, kh * a.k_head, p, p.t0), query(a.q, kh * a.q_head, p, p.t0);
   // K or Q as the second operand: columns are the key's dimension, terms are tokens.
-  auto transposed = [&](const uint16_t* staged, const ChunkRows<const T>& from, int t, int c, s16x8 (&e)[N]) __attribute__((always_inline)) {
-    if constexpr (Lds::kStage) {
-      e[0] = lds8_trans(staged + 32 * c * (KP + 8) + 16 * (tile0 + t) + trans_place(lane, KP + 8), KP + 8);
-    } else {
-      float g[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int tok = opaque(32 * c + 8 * lg) + i, col = 16 * (tile0 + t) + lr;
-        g[i] = tok < n && col < Dk ? to_f32(from.at(tok, col)) : 0.f;
-      }
-      split8<N>(g, e);
-    }
+  auto transposed = [&](bool keys, int t, int c, s16x8 (&e)[N]) __attribute__((always_inline)) {
+    if constexpr (Lds::kStage) (keys ? L.keys().key : L.keys().query).transposed(tile0 + t, c, lane, e);
+    else transposed_rows<T>(keys ? key : query, n, Dk, tile0 + t, c, lane, e);
   };
   // Element (token 16 r + 4 lg + i, column 16 t + lr) of K or Q.
-  auto element = [&](const ChunkRows<const T>& from, int t, int i) __attribute__((always_inline)) {
+  auto element = [&](bool keys, int t, int i) __attribute__((always_inline)) {
     const int row = opaque(16 * r + 4 * lg) + i, col = 16 * (tile0 + t) + lr;
-    return row < n && col < Dk ? to_f32(from.at(row, col)) : 0.f;
+    float v;
+    if constexpr (Lds::kStage) v = to_f32((keys ? L.keys().key : L.keys().query).at[row][col]);
+    else v = to_f32((keys ? key : query).at(min(row, n - 1), min(col, Dk - 1)));
+    return row < n && col < Dk ? v : 0.f;
   };
+  auto stage_keys = [&]() __attribute__((always_inline)) {
+    if constexpr (Lds::kStage) {
+      const int row = 16 * r + lr;
+#pragma unroll
+      for (int c = 0; c < KT / 2; ++c) {
+        const int col = 16 * tile0 + 32 * c + 8 * lg;
+        Eight<T> e, f;
+        e.load(&key.at(min(row, n - 1), col), Dk - col);
+        f.load(&query.at(min(row, n - 1), col), Dk - col);
+        e.put(&L.keys().key.at[row][col]);
+        f.put(&L.keys().query.at[row][col]);
+      }
+    }
+  };
+  if constexpr (Lds::kBeside) stage_keys();
   for (int h = 0; h < (kHeld ? group : 1); ++h) {
     const int head = kh * group + (SHARING == kInTurn ? k.turn : h);
-    if constexpr (kHeld) {           // offsets made from these are not kept over the loop
-      lr = opaque(lr);
-      lg = opaque(lg);
-    }
+    lr = opaque(lr);                 // offsets made from these are not kept over the loop, nor from one part to the next
+    lg = opaque(lg);
     const int mine = 16 * r + lr;    // the token whose row this lane loads
     const int64_t at = chunk_head(k, piece, head);
     const float* pS = k.states + at * Dk * Dv;
@@ -539,23 +515,49 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
 #pragma unroll
     for (int t = 0; t < 4; ++t) oz[t] = xz[t] = zero4();
     float inside = 0.f;              // <dS', S>
+    // 32 columns: what this lane brings to the panels, and its own operands.
+    constexpr int kRows = KP * 8 / kThreads, kErrors = kChunk * 8 / kThreads;
+    constexpr bool kAhead = KP <= 128 && !(kHeld && KP * N > 256);         // the next panel's loads fit the registers
+    Raw<float, 4> vS[kRows], vD[kRows], vZ[kErrors];
+    Eight<T> vO;
+    Eight<float> vX;
+    auto load_panel = [&](int c0) __attribute__((always_inline)) {
+      const int lane8 = opaque(tid), c = c0 + 4 * (lane8 & 7), left = Dv - c;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int row = (lane8 + kThreads * i) >> 3;
+        vS[i].clear();
+        vD[i].clear();
+        if (row < Dk && left > 0) {
+          vS[i].load_n(&at_lane(pS, row * Dv + c), left);
+          vD[i].load_n(&at_lane(pD, row * Dv + c), left);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kErrors; ++i) {
+        const int row = (lane8 + kThreads * i) >> 3;
+        vZ[i].clear();
+        if (row < n && left > 0) vZ[i].load_n(&at_lane(k.errors + (row0 * heads + head) * Dv, row * heads * Dv + c), left);
+      }
+      const int own = mine < n ? Dv - c0 - 8 * lg : 0;
+      vO.load(&ChunkRows<const T>(k.dout, head * k.dout_head, p, p.t0).at(min(mine, n - 1), c0 + 8 * lg), own);
+      vX.load(&at_lane(k.dx + (row0 * heads + head) * Dv, min(mine, n - 1) * heads * Dv + c0 + 8 * lg), own);
+    };
+    if (kAhead) load_panel(0);
 #pragma unroll 1
     for (int c0 = 0; c0 < Dv; c0 += 32) {
+      if (!kAhead) load_panel(c0);
+      s16x8 o[N], x[kPieces], z[kPieces];
+      vO.pieces(o);
+      vX.pieces(x);
 #pragma unroll
-      for (int i = 0; i < KP * 8 / kThreads; ++i) {
+      for (int i = 0; i < kRows; ++i) {
         const int row = (tid + kThreads * i) >> 3, c = 4 * (tid & 7);
-        Raw<float, 4> s, d;
-        s.clear();
-        d.clear();
-        if (row < Dk && c0 + c < Dv) {
-          s.load_n(&at_lane(pS, row * Dv + c0 + c), Dv - c0 - c);
-          d.load_n(&at_lane(pD, row * Dv + c0 + c), Dv - c0 - c);
-        }
         uint2 us[kPieces], ud[kPieces];
-        split4<kPieces>(f32x4{s.get(0), s.get(1), s.get(2), s.get(3)}, us);
-        split4<kPieces>(f32x4{d.get(0), d.get(1), d.get(2), d.get(3)}, ud);
+        split4<kPieces>(f32x4{vS[i].get(0), vS[i].get(1), vS[i].get(2), vS[i].get(3)}, us);
+        split4<kPieces>(f32x4{vD[i].get(0), vD[i].get(1), vD[i].get(2), vD[i].get(3)}, ud);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) inside = __builtin_fmaf(s.get(e), d.get(e), inside);
+        for (int e = 0; e < 4; ++e) inside = __builtin_fmaf(vS[i].get(e), vD[i].get(e), inside);
 #pragma unroll
         for (int e = 0; e < kPieces; ++e) {
           *reinterpret_cast<uint2*>(&L.panels.S[e][row][c]) = us[e];
@@ -563,27 +565,15 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
         }
       }
 #pragma unroll
-      for (int i = 0; i < kChunk * 8 / kThreads; ++i) {
+      for (int i = 0; i < kErrors; ++i) {
         const int row = (tid + kThreads * i) >> 3, c = 4 * (tid & 7);
-        Raw<float, 4> z;
-        z.clear();
-        if (row < n && c0 + c < Dv) z.load_n(&at_lane(k.errors + (row0 * heads + head) * Dv, row * heads * Dv + c0 + c), Dv - c0 - c);
         uint2 u[kPieces];
-        split4<kPieces>(f32x4{z.get(0), z.get(1), z.get(2), z.get(3)}, u);
+        split4<kPieces>(f32x4{vZ[i].get(0), vZ[i].get(1), vZ[i].get(2), vZ[i].get(3)}, u);
 #pragma unroll
         for (int e = 0; e < kPieces; ++e) *reinterpret_cast<uint2*>(&L.panels.Z[e][row][c]) = u[e];
       }
-      s16x8 o[N], x[kPieces], z[kPieces];
-      {
-        const int left = mine < n ? Dv - c0 - 8 * lg : 0;
-        Eight<T> eo;
-        Eight<float> ex;
-        eo.load(&ChunkRows<const T>(k.dout, head * k.dout_head, p, p.t0).at(min(mine, n - 1), c0 + 8 * lg), left);
-        ex.load(&at_lane(k.dx + (row0 * heads + head) * Dv, min(mine, n - 1) * heads * Dv + c0 + 8 * lg), left);
-        eo.pieces(o);
-        ex.pieces(x);
-      }
-      __syncthreads();
+      lds_barrier();
+      if (kAhead) load_panel(c0 + 32);         // past the last column: zeros
 #pragma unroll
       for (int e = 0; e < kPieces; ++e) z[e] = lds8(&L.panels.Z[e][mine][8 * lg]);
 #pragma unroll
@@ -596,7 +586,7 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
 #pragma unroll
         for (int e = 0; e < kPieces; ++e) b[e] = lds8(&L.panels.D[e][16 * (tile0 + t) + lr][8 * lg]);
         mfma_pieces<kPieces>(z, b, W[t]);
-        if (t & 1) __builtin_amdgcn_sched_barrier(0);
+        if ((t & 1) || KP * N > 256) __builtin_amdgcn_sched_barrier(0);     // operands in registers at a time
       }
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -607,17 +597,14 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
           if (part == 0) mfma_pieces<kPieces>(o, b, oz[t]);
           if (part == kParts - 1) mfma_pieces<kPieces>(x, b, xz[t]);
         }
-      __syncthreads();
+      lds_barrier();
     }
     // E and R (with the sign that R's products have), and the parts that the states give
-    float first[4], last[4], beta[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 16 * r + 4 * lg + i;
-      first[i] = L.d.first[row];
-      last[i] = L.d.last[row];
-      beta[i] = L.d.beta[row];
-    }
+    lr = opaque(lr);
+    lg = opaque(lg);
+    auto of_rows = [&](const float (&v)[kChunk]) __attribute__((always_inline)) {
+      return *reinterpret_cast<const f32x4*>(&v[opaque(16 * r + 4 * lg)]);
+    };
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -644,20 +631,8 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
       if (part == kParts - 1) share_square(xz, L.squares.R, weighted);
     };
     share_squares(true);
-    if constexpr (Lds::kStage) {
-#pragma unroll
-      for (int c = 0; c < KT / 2; ++c) {
-        const int col = 16 * tile0 + 32 * c + 8 * lg, left = mine < n ? Dk - col : 0;
-        Eight<T> e;
-        s16x8 u[N];
-        e.load(&key.at(min(mine, n - 1), col), left);
-        e.pieces(u);
-        *reinterpret_cast<s16x8*>(&L.squares.key[mine][col]) = u[0];
-        e.load(&query.at(min(mine, n - 1), col), left);
-        e.pieces(u);
-        *reinterpret_cast<s16x8*>(&L.squares.query[mine][col]) = u[0];
-      }
-    }
+    if constexpr (Lds::kStage && !Lds::kBeside) stage_keys();
+    const f32x4 first = of_rows(L.d.first), last = of_rows(L.d.last);
 #pragma unroll
     for (int t = 0; t < KT; ++t)
 #pragma unroll
@@ -667,8 +642,6 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
         W[t][i] *= last[i];
       }
     __syncthreads();
-    const uint16_t* staged_key = &L.squares.key[0][0];
-    const uint16_t* staged_query = &L.squares.query[0][0];
 #pragma unroll
     for (int c = 0; c < 2; ++c)
       if (c <= r / 2) {
@@ -681,21 +654,22 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
           s16x8 b[N];
-          transposed(staged_key, key, t, c, b);
+          transposed(true, t, c, b);
           mfma_pieces<kPieces>(e, b, Q[t]);
           mfma_pieces<kPieces>(x, b, R[t]);
-          if (!Lds::kStage) __builtin_amdgcn_sched_barrier(0);
+          if (!Lds::kStage || KP * N > 256) __builtin_amdgcn_sched_barrier(0);
         }
       }
     __syncthreads();
     share_squares(false);
     // <dS', S'>: e^G_C <dS', S> and what the chunk itself writes, beta k . (e^(G_C - G) Z dS'^T)
+    f32x4 beta = of_rows(L.d.beta);
     float tail = L.d.first[kChunk - 1] * inside, dots[4] = {0.f, 0.f, 0.f, 0.f}, db[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float kv = element(key, t, i), qv = element(query, t, i);
+        const float kv = element(true, t, i), qv = element(false, t, i);
         tail = __builtin_fmaf(beta[i] * kv, W[t][i], tail);
         dots[i] = __builtin_fmaf(qv, Q[t][i], __builtin_fmaf(kv, R[t][i], dots[i]));
       }
@@ -714,17 +688,18 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
 #pragma unroll
         for (int t = 0; t < KT; ++t) {
           s16x8 b[N];
-          transposed(staged_query, query, t, c, b);
+          transposed(false, t, c, b);
           mfma_pieces<kPieces>(e, b, W[t]);
-          transposed(staged_key, key, t, c, b);
+          transposed(true, t, c, b);
           mfma_pieces<kPieces>(x, b, W[t]);
-          if (!Lds::kStage) __builtin_amdgcn_sched_barrier(0);
+          if (!Lds::kStage || KP * N > 256) __builtin_amdgcn_sched_barrier(0);
         }
       }
+    beta = of_rows(L.d.beta);
 #pragma unroll
     for (int t = 0; t < KT; ++t) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) db[i] = __builtin_fmaf(element(key, t, i), W[t][i], db[i]);
+      for (int i = 0; i < 4; ++i) db[i] = __builtin_fmaf(element(true, t, i), W[t][i], db[i]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) R[t][i] = __builtin_fmaf(beta[i], W[t][i], R[t][i]);
       if constexpr (kHeld) {
@@ -776,7 +751,7 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
           if (row < n && col < Dk) {
             const int e = row * key_heads * Dk + col;
             float vq = kHeld ? dq[kHeld ? t : 0][i] : Q[t][i], vk = kHeld ? dk[kHeld ? t : 0][i] : R[t][i];
-            if constexpr (SHARING == kInTurn) {
+            if (SHARING == kInTurn && group > 1) {
               float& sq = at_lane(k.sums + to, e);
               float& sk = at_lane(k.sums + k.sums_stride + to, e);
               if (k.turn > 0) {
@@ -805,8 +780,8 @@ hipError_t grad_n(const DeltaArgs& k, hipStream_t stream) {
   if (err != hipSuccess || seq_rows(k.a.tokens) == 0) return err;
   const dim3 grid((unsigned)(k.pieces * k.a.key_heads)), block(KP > 64 ? 512 : 256);
   const int group = (int)(k.a.heads / k.a.key_heads);
-  if (group == 1) return launch_kernel(delta_input_grad_kernel<T, KP, kAlone>, grid, block, k, stream);
   if constexpr (KP <= 128) {
+    if (group == 1) return launch_kernel(delta_input_grad_kernel<T, KP, kAlone>, grid, block, k, stream);
     return launch_kernel(delta_input_grad_kernel<T, KP, kTogether>, grid, block, k, stream);
   } else {
     DeltaArgs one = k;
