@@ -28,7 +28,7 @@ constexpr int kPieces = 3;             // of a 32-bit number
 constexpr int kFrags = 6;              // 16 x 32 blocks of a triangular 64 x 64 matrix that are not zero
 constexpr int kFragElems = 64 * 8;     // of one piece of one block
 constexpr int kMatrix = kFrags * kPieces * kFragElems;   // 16-bit elements of such a matrix
-constexpr int kTokenPitch = kChunk + 8;                  // 16-bit elements of an LDS row of tokens
+constexpr int kTokenPitch = kChunk + 8;                  // 16-bit elements of an LDS row of tokens (input gradients)
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
@@ -69,11 +69,11 @@ struct DeltaArgs {
 };
 
 // ---- pieces ---------------------------------------------------------------------------------------------------------
+// Two numbers rounded to bf16 in one instruction.
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
-  Bf16 lo, hi;
-  from_f32(a, lo);
-  from_f32(b, hi);
-  return lo.bits | (uint32_t)hi.bits << 16;
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
 }
 // Two numbers as pairs of pieces; what a piece leaves is exact in 32 bits.
 template <int N>
@@ -88,12 +88,12 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t (&out)[N]) {
   }
 }
 template <int N>
-__device__ __forceinline__ void split4(f32x4 v, uint2 (&out)[N]) {
+__device__ __forceinline__ void split4(f32x4 v, u32x2 (&out)[N]) {
   uint32_t lo[N], hi[N];
   split2<N>(v[0], v[1], lo);
   split2<N>(v[2], v[3], hi);
 #pragma unroll
-  for (int i = 0; i < N; ++i) out[i] = uint2{lo[i], hi[i]};
+  for (int i = 0; i < N; ++i) out[i] = u32x2{lo[i], hi[i]};
 }
 template <int N>
 __device__ __forceinline__ void split8(const float (&f)[8], s16x8 (&out)[N]) {
@@ -182,6 +182,18 @@ __device__ __forceinline__ f32x4 total(const f32x4 (&sum)[N]) {
   return t;
 }
 
+// A second operand of D terms and 16 columns in LDS, in the order that a wave reads it: eight terms of a column, column by
+// column.  One read of a wave is 1 KB on end, whatever lanes the LDS serves together.
+template <int D>
+struct Operand {
+  alignas(16) uint16_t at[D / 8][16][8];
+  // Four terms from term d on, and a lane's part of terms 32 c ...
+  __device__ __forceinline__ u32x2& four(int d, int col) { return *reinterpret_cast<u32x2*>(&at[d >> 3][col][d & 4]); }
+  __device__ __forceinline__ s16x8 eight(int c, int lane) const {
+    return *reinterpret_cast<const s16x8*>(&at[4 * c + (lane >> 4)][lane & 15][0]);
+  }
+};
+
 // Eight 16-bit elements of LDS at p; and a transposed operand: terms are LDS rows of `pitch` elements, p is lane's place
 // as trans_place gives it.
 __device__ __forceinline__ s16x8 lds8(const uint16_t* p) { return *reinterpret_cast<const s16x8*>(p); }
@@ -217,6 +229,20 @@ struct Staged {
       for (int i = 0; i < 8; ++i) f[i] = to_f32(at[32 * c + 8 * (lane >> 4) + i][16 * m + (lane & 15)]);
       split8<ElemPieces<T>::n>(f, e);
     }
+  }
+};
+// The same as pieces: no work between the LDS and the matrix instructions, for more of the LDS.
+template <typename T, int KP>
+struct StagedPieces {
+  static constexpr int N = ElemPieces<T>::n;
+  alignas(16) uint16_t at[N][kChunk][KP + 8];
+  __device__ __forceinline__ void put(int row, int d, const s16x8 (&e)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) *reinterpret_cast<s16x8*>(&at[i][row][d]) = e[i];
+  }
+  __device__ __forceinline__ void transposed(int m, int c, int lane, s16x8 (&e)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = lds8_trans(&at[i][32 * c][16 * m] + trans_place(lane, KP + 8), KP + 8);
   }
 };
 // The same from memory, where the LDS is full; n tokens are the chunk's.

@@ -214,8 +214,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void delta_chunk_kerne
 template <typename T, int KP, int NT>
 struct WalkLds {
   static constexpr int N = ElemPieces<T>::n, NO = OutPieces<T>::n;
-  uint16_t S[kPieces][16 * NT][KP + 8], X[kPieces][16 * NT][kTokenPitch], W[kPieces][16 * NT][kTokenPitch],
-      Z[NO][16 * NT][kTokenPitch];
+  Operand<KP> S[kPieces][NT];
+  Operand<kChunk> X[kPieces][NT], W[kPieces][NT], Z[NO][NT];
   Staged<T, KP> K;
 };
 // Two workgroups a CU (four waves a SIMD) where their LDS and registers allow it.
@@ -248,10 +248,10 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        uint2 u[kPieces];
+        u32x2 u[kPieces];
         split4<kPieces>(S[m][t], u);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.S[i][16 * t + lr][16 * (r * MT + m) + 4 * lg]) = u[i];
+        for (int i = 0; i < kPieces; ++i) L.S[i][t].four(16 * (r * MT + m) + 4 * lg, lr) = u[i];
       }
   };
   auto keep_state = [&](float* to) __attribute__((always_inline)) {
@@ -330,7 +330,7 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
         for (int t = 0; t < NT; ++t) {
           s16x8 b[kPieces];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.S[i][16 * t + lr][32 * c + 8 * lg]);
+          for (int i = 0; i < kPieces; ++i) b[i] = L.S[i][t].eight(c, lane);
           mfma_pieces<kPieces>(e, b, sum[t]);
         }
         if (c & 1) __builtin_amdgcn_sched_barrier(0);     // two blocks' operands in registers at a time
@@ -342,7 +342,7 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
       for (int t = 0; t < NT; ++t) {
         const f32x4 kS = total(sum[t]);
         f32x4 x;
-        uint2 u[kPieces];
+        u32x2 u[kPieces];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float d = __builtin_fmaf(-f[i], kS[i], to_f32(v[t][i]));
@@ -350,7 +350,7 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
         }
         split4<kPieces>(x, u);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.X[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
+        for (int i = 0; i < kPieces; ++i) L.X[i][t].four(16 * r + 4 * lg, lr) = u[i];
       }
     }
     load_values(next);
@@ -366,21 +366,21 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
         if (c <= r / 2) {
           s16x8 b[kPieces];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.X[i][16 * t + lr][32 * c + 8 * lg]);
+          for (int i = 0; i < kPieces; ++i) b[i] = L.X[i][t].eight(c, lane);
           mfma_pieces<kPieces>(square[c], b, sum);
         }
       z[t] = total(sum);
-      uint2 u[kPieces];
+      u32x2 u[kPieces];
       f32x4 x;
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = l[i] * z[t][i];
       split4<kPieces>(x, u);
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.W[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
-      uint2 uz[NO];
+      for (int i = 0; i < kPieces; ++i) L.W[i][t].four(16 * r + 4 * lg, lr) = u[i];
+      u32x2 uz[NO];
       split4<NO>(z[t], uz);
 #pragma unroll
-      for (int i = 0; i < NO; ++i) *reinterpret_cast<uint2*>(&L.Z[i][16 * t + lr][16 * r + 4 * lg]) = uz[i];
+      for (int i = 0; i < NO; ++i) L.Z[i][t].four(16 * r + 4 * lg, lr) = uz[i];
     }
     lds_barrier();
     if (SAVE) {
@@ -415,7 +415,7 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
         for (int t = 0; t < NT; ++t) {
           s16x8 b[kPieces];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.W[i][16 * t + lr][32 * c + 8 * lg]);
+          for (int i = 0; i < kPieces; ++i) b[i] = L.W[i][t].eight(c, lane);
           mfma_pieces<kPieces>(e, b, sum[t]);
         }
       }
@@ -480,7 +480,7 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, 
       for (int t = 0; t < NT; ++t) {
         s16x8 b[NO];
 #pragma unroll
-        for (int i = 0; i < NO; ++i) b[i] = lds8(&L.S[i][16 * t + lr][32 * c + 8 * lg]);
+        for (int i = 0; i < NO; ++i) b[i] = L.S[i][t].eight(c, lane);
         mfma_pieces<NO>(e, b, o[t]);
       }
     }
@@ -503,7 +503,7 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, 
         if (c <= r / 2) {
           s16x8 b[NO];
 #pragma unroll
-          for (int i = 0; i < NO; ++i) b[i] = lds8(&L.Z[i][16 * t + lr][32 * c + 8 * lg]);
+          for (int i = 0; i < NO; ++i) b[i] = L.Z[i][t].eight(c, lane);
           mfma_pieces<NO>(square[c], b, o[t]);
         }
     load_square(next);

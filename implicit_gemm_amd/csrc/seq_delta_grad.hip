@@ -24,21 +24,19 @@ template <typename T, int KP, int NT>
 struct BackLds {
   static constexpr int N = ElemPieces<T>::n;
   static constexpr bool kStage = sizeof(T) == 2 || KP <= 128;     // K and Q fit beside the rest
-  uint16_t S[kPieces][16 * NT][KP + 8], X[kPieces][16 * NT][kTokenPitch], W[kPieces][16 * NT][kTokenPitch],
-      D[kPieces][16 * NT][kTokenPitch], O[N][16 * NT][kTokenPitch];
+  Operand<KP> S[kPieces][NT];
+  Operand<kChunk> X[kPieces][NT], W[kPieces][NT], D[kPieces][NT], O[N][NT];
   Staged<T, kStage ? KP : 0> K, Q;
   f32x4 back[KP / 16][NT][64];       // Q^T do', each lane's as the chain's lane takes it
-  // P^T do of the chunk to come, where the chain's wave r is to put its part of dZ: in X, free from the one exchange to
-  // the other.
+  // P^T do of the chunk to come, where the chain's wave r is to put its part of dZ: its tokens' 16 x 16 blocks of two
+  // pieces of X, free from the one exchange to the other.
   __device__ __forceinline__ f32x4& inner(int r, int t, int lane) {
-    return *reinterpret_cast<f32x4*>(&X[lane >> 5][16 * t + (lane & 15)][16 * r + 8 * ((lane >> 4) & 1)]);
+    return *reinterpret_cast<f32x4*>(&X[lane >> 5][t].at[2 * r + ((lane >> 4) & 1)][lane & 15][0]);
   }
 };
 // Two workgroups a CU (four waves a SIMD) where their LDS and registers allow it.
-template <class Lds, int KP, bool WHOLE>
-constexpr int back_waves() {
-  return sizeof(Lds) <= 80 * 1024 && KP <= 128 && (KP * Lds::N <= 128 || (KP * Lds::N <= 256 && WHOLE)) ? 4 : 2;
-}
+template <class Lds, int KP>
+constexpr int back_waves() { return sizeof(Lds) <= 80 * 1024 && KP * Lds::N <= 128 ? 4 : 2; }
 
 template <typename T, int KP, int NT, bool WHOLE>
 __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, BackLds<T, KP, NT>& L, int r, int lane) {
@@ -64,10 +62,10 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        uint2 u[kPieces];
+        u32x2 u[kPieces];
         split4<kPieces>(S[m][t], u);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.S[i][16 * t + lr][16 * (r * MT + m) + 4 * lg]) = u[i];
+        for (int i = 0; i < kPieces; ++i) L.S[i][t].four(16 * (r * MT + m) + 4 * lg, lr) = u[i];
       }
   };
   auto keep_state = [&](float* to) __attribute__((always_inline)) {
@@ -136,7 +134,7 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
         for (int t = 0; t < NT; ++t) {
           s16x8 b[kPieces];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.S[i][16 * t + lr][32 * c + 8 * lg]);
+          for (int i = 0; i < kPieces; ++i) b[i] = L.S[i][t].eight(c, lane);
           mfma_pieces<kPieces>(e, b, sum[t]);
         }
         if (c & 1) __builtin_amdgcn_sched_barrier(0);
@@ -150,13 +148,13 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
       for (int t = 0; t < NT; ++t) {
         const f32x4 kS = total(sum[t]);
         f32x4 z = L.inner(r, t, lane);
-        uint2 u[kPieces];
+        u32x2 u[kPieces];
 #pragma unroll
         for (int i = 0; i < 4; ++i) z[i] = 16 * r + 4 * lg + i < n ? __builtin_fmaf(l[i], kS[i], z[i]) : 0.f;
         split4<kPieces>(z, u);
         wave_sync();                 // what `inner` holds is read by then
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.X[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
+        for (int i = 0; i < kPieces; ++i) L.X[i][t].four(16 * r + 4 * lg, lr) = u[i];
       }
     }
     lds_barrier();
@@ -171,17 +169,17 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
         if (c >= r / 2) {
           s16x8 b[kPieces];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.X[i][16 * t + lr][32 * c + 8 * lg]);
+          for (int i = 0; i < kPieces; ++i) b[i] = L.X[i][t].eight(c, lane);
           mfma_pieces<kPieces>(square[c], b, sum);
         }
       dx[t] = total(sum);
       f32x4 x;
-      uint2 u[kPieces];
+      u32x2 u[kPieces];
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = -f[i] * dx[t][i];
       split4<kPieces>(x, u);
 #pragma unroll
-      for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.W[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
+      for (int i = 0; i < kPieces; ++i) L.W[i][t].four(16 * r + 4 * lg, lr) = u[i];
     }
     lds_barrier();
     {
@@ -221,7 +219,7 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
         for (int t = 0; t < NT; ++t) {
           s16x8 b[kPieces];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.W[i][16 * t + lr][32 * c + 8 * lg]);
+          for (int i = 0; i < kPieces; ++i) b[i] = L.W[i][t].eight(c, lane);
           mfma_pieces<kPieces>(e, b, sum[t]);
         }
       }
@@ -284,10 +282,10 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
     float one[4] = {1.f, 1.f, 1.f, 1.f};
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      uint2 u[N];
+      u32x2 u[N];
       split4<N>(values(j, v, t, one), u);
 #pragma unroll
-      for (int i = 0; i < N; ++i) *reinterpret_cast<uint2*>(&L.O[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
+      for (int i = 0; i < N; ++i) L.O[i][t].four(16 * r + 4 * lg, lr) = u[i];
     }
   };
   auto inner_part = [&]() __attribute__((always_inline)) {
@@ -300,7 +298,7 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
         if (c >= r / 2) {
           s16x8 b[N];
 #pragma unroll
-          for (int i = 0; i < N; ++i) b[i] = lds8(&L.O[i][16 * t + lr][32 * c + 8 * lg]);
+          for (int i = 0; i < N; ++i) b[i] = L.O[i][t].eight(c, lane);
           mfma_pieces<kPieces>(square[c], b, sum);
         }
       L.inner(r, t, lane) = total(sum);
@@ -331,10 +329,10 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
       float by[4] = {a.scale * first.x, a.scale * first.y, a.scale * first.z, a.scale * first.w};
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        uint2 u[kPieces];
+        u32x2 u[kPieces];
         split4<kPieces>(values(j, now, t, by), u);
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) *reinterpret_cast<uint2*>(&L.D[i][16 * t + lr][16 * r + 4 * lg]) = u[i];
+        for (int i = 0; i < kPieces; ++i) L.D[i][t].four(16 * r + 4 * lg, lr) = u[i];
       }
     }
     share_do(after, next);
@@ -361,7 +359,7 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
         for (int t = 0; t < NT; ++t) {
           s16x8 b[kPieces];
 #pragma unroll
-          for (int i = 0; i < kPieces; ++i) b[i] = lds8(&L.D[i][16 * t + lr][32 * c + 8 * lg]);
+          for (int i = 0; i < kPieces; ++i) b[i] = L.D[i][t].eight(c, lane);
           mfma_pieces<kPieces>(e, b, sum[t]);
         }
       }
@@ -376,7 +374,7 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
 }
 
 template <typename T, int KP, int NT, bool WHOLE>
-__global__ __launch_bounds__(512, (back_waves<BackLds<T, KP, NT>, KP, WHOLE>())) void delta_back_kernel(DeltaArgs k) {
+__global__ __launch_bounds__(512, (back_waves<BackLds<T, KP, NT>, KP>())) void delta_back_kernel(DeltaArgs k) {
   typedef BackLds<T, KP, NT> Lds;
   __shared__ __attribute__((aligned(16))) char bytes[sizeof(Lds)];
   Lds& L = *reinterpret_cast<Lds*>(bytes);
@@ -553,24 +551,24 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int row = (tid + kThreads * i) >> 3, c = 4 * (tid & 7);
-        uint2 us[kPieces], ud[kPieces];
+        u32x2 us[kPieces], ud[kPieces];
         split4<kPieces>(f32x4{vS[i].get(0), vS[i].get(1), vS[i].get(2), vS[i].get(3)}, us);
         split4<kPieces>(f32x4{vD[i].get(0), vD[i].get(1), vD[i].get(2), vD[i].get(3)}, ud);
 #pragma unroll
         for (int e = 0; e < 4; ++e) inside = __builtin_fmaf(vS[i].get(e), vD[i].get(e), inside);
 #pragma unroll
         for (int e = 0; e < kPieces; ++e) {
-          *reinterpret_cast<uint2*>(&L.panels.S[e][row][c]) = us[e];
-          *reinterpret_cast<uint2*>(&L.panels.D[e][row][c]) = ud[e];
+          *reinterpret_cast<u32x2*>(&L.panels.S[e][row][c]) = us[e];
+          *reinterpret_cast<u32x2*>(&L.panels.D[e][row][c]) = ud[e];
         }
       }
 #pragma unroll
       for (int i = 0; i < kErrors; ++i) {
         const int row = (tid + kThreads * i) >> 3, c = 4 * (tid & 7);
-        uint2 u[kPieces];
+        u32x2 u[kPieces];
         split4<kPieces>(f32x4{vZ[i].get(0), vZ[i].get(1), vZ[i].get(2), vZ[i].get(3)}, u);
 #pragma unroll
-        for (int e = 0; e < kPieces; ++e) *reinterpret_cast<uint2*>(&L.panels.Z[e][row][c]) = u[e];
+        for (int e = 0; e < kPieces; ++e) *reinterpret_cast<u32x2*>(&L.panels.Z[e][row][c]) = u[e];
       }
       lds_barrier();
       if (kAhead) load_panel(c0 + 32);         // past the last column: zeros
@@ -620,10 +618,10 @@ __global__ __launch_bounds__(KP > 64 ? 512 : 256) void delta_input_grad_kernel(D
       for (int t = 0; t < 4; ++t) {
         const int j = 16 * t + lr;
         const float w = weighted ? L.d.beta[j] : 1.f;
-        uint2 u[kPieces];
+        u32x2 u[kPieces];
         split4<kPieces>(f32x4{w * m[t][0], w * m[t][1], w * m[t][2], w * m[t][3]}, u);
 #pragma unroll
-        for (int e = 0; e < kPieces; ++e) *reinterpret_cast<uint2*>(&to[e][j][16 * r + 4 * lg]) = u[e];
+        for (int e = 0; e < kPieces; ++e) *reinterpret_cast<u32x2*>(&to[e][j][16 * r + 4 * lg]) = u[e];
       }
     };
     auto share_squares = [&](bool weighted) __attribute__((always_inline)) {
