@@ -231,20 +231,6 @@ struct Staged {
     }
   }
 };
-// The same as pieces: no work between the LDS and the matrix instructions, for more of the LDS.
-template <typename T, int KP>
-struct StagedPieces {
-  static constexpr int N = ElemPieces<T>::n;
-  alignas(16) uint16_t at[N][kChunk][KP + 8];
-  __device__ __forceinline__ void put(int row, int d, const s16x8 (&e)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) *reinterpret_cast<s16x8*>(&at[i][row][d]) = e[i];
-  }
-  __device__ __forceinline__ void transposed(int m, int c, int lane, s16x8 (&e)[N]) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) e[i] = lds8_trans(&at[i][32 * c][16 * m] + trans_place(lane, KP + 8), KP + 8);
-  }
-};
 // The same from memory, where the LDS is full; n tokens are the chunk's.
 template <typename T>
 __device__ __forceinline__ void transposed_rows(const ChunkRows<const T>& from, int n, int Dk, int m, int c, int lane,

@@ -218,10 +218,6 @@ struct WalkLds {
   Operand<kChunk> X[kPieces][NT], W[kPieces][NT], Z[NO][NT];
   Staged<T, KP> K;
 };
-// Two workgroups a CU (four waves a SIMD) where their LDS and registers allow it.
-template <class Lds, int KP>
-constexpr int walk_waves() { return sizeof(Lds) <= 80 * 1024 && KP <= 128 && KP * Lds::N <= 256 ? 4 : 2; }
-
 template <typename T, int KP, int NT, bool SAVE, bool WHOLE>
 __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, WalkLds<T, KP, NT>& L, int r, int lane) {
   typedef WalkLds<T, KP, NT> Lds;
@@ -525,7 +521,7 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, 
 }
 
 template <typename T, int KP, int NT, bool SAVE, bool WHOLE>
-__global__ __launch_bounds__(512, (walk_waves<WalkLds<T, KP, NT>, KP>())) void delta_kernel(DeltaArgs k) {
+__global__ __launch_bounds__(512) void delta_kernel(DeltaArgs k) {
   typedef WalkLds<T, KP, NT> Lds;
   __shared__ __attribute__((aligned(16))) char bytes[sizeof(Lds)];
   Lds& L = *reinterpret_cast<Lds*>(bytes);

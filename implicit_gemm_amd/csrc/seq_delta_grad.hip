@@ -34,10 +34,6 @@ struct BackLds {
     return *reinterpret_cast<f32x4*>(&X[lane >> 5][t].at[2 * r + ((lane >> 4) & 1)][lane & 15][0]);
   }
 };
-// Two workgroups a CU (four waves a SIMD) where their LDS and registers allow it.
-template <class Lds, int KP>
-constexpr int back_waves() { return sizeof(Lds) <= 80 * 1024 && KP * Lds::N <= 128 ? 4 : 2; }
-
 template <typename T, int KP, int NT, bool WHOLE>
 __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, BackLds<T, KP, NT>& L, int r, int lane) {
   typedef BackLds<T, KP, NT> Lds;
@@ -374,7 +370,7 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
 }
 
 template <typename T, int KP, int NT, bool WHOLE>
-__global__ __launch_bounds__(512, (back_waves<BackLds<T, KP, NT>, KP>())) void delta_back_kernel(DeltaArgs k) {
+__global__ __launch_bounds__(512) void delta_back_kernel(DeltaArgs k) {
   typedef BackLds<T, KP, NT> Lds;
   __shared__ __attribute__((aligned(16))) char bytes[sizeof(Lds)];
   Lds& L = *reinterpret_cast<Lds*>(bytes);

@@ -201,23 +201,41 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_grad_kerne
   }
 }
 
-constexpr int64_t kNarrow = 512;   // channels of a row that 16 lanes take
+// Which team.  Times of a call in us, forward / gradient, the operands in the last-level cache up to 256 MB:
+//
+// 16 lanes against a wave, bf16        8192 rows            65536 rows           131072 rows
+//   128 channels                     3.6 /  9.3 against    11.4 / 17.8 against
+//                                    4.7 /  9.1            21.2 / 33.5
+//   384                              5.8 / 16.3 against    26.4 / 36.7 against  45.4 / 61.7 against
+//                                    6.0 / 10.2            27.2 / 34.9          50.5 / 84.2
+//   512                              7.0 / 20.2 against    33.4 / 46.9 against  60.3 / 88.7 against
+//                                    6.7 / 10.8            31.0 / 39.8          60.1 / 89.3
+// (fp32 by bytes: 256 channels as bf16's 512.)  Rows of up to 768 bytes go to 16 lanes where there are enough of them.
+//
+// A wave against 256 lanes, bf16        256 rows             1024 rows            8192 rows            65536 rows
+//   512 channels                     3.7 /  6.7 against    3.7 /  7.1 against   6.7 / 10.8 against   32.8 /  38.6 against
+//                                    3.7 /  6.8            4.3 / 10.7          11.3 / 21.6           64.3 / 111.7
+//   2048                             3.9 / 10.3 against    6.1 / 13.0 against  21.7 / 28.9 against  130.3 / 156.5 against
+//                                    3.9 /  9.2            5.2 / 20.3          19.7 / 29.7          138.3 / 166.5
 template <typename T>
-constexpr bool by_wave(int64_t C) { return C * (int64_t)sizeof(T) <= 4096; }
+constexpr bool by_sixteen(int64_t C, int64_t rows, int64_t least) { return C * (int64_t)sizeof(T) <= 768 && rows >= least; }
+template <typename T>
+constexpr bool by_wave(int64_t C, int64_t rows, int64_t least) { return C * (int64_t)sizeof(T) <= 4096 && rows >= least; }
 
 template <typename T>
 hipError_t layer_norm_t(const seq_layer_norm_args_t& a, hipStream_t stream) {
   const int64_t C = a.channels;
-  const bool narrow = C <= kNarrow && a.rows >= 4096, wave = by_wave<T>(C) && a.rows >= 1024;
+  const bool narrow = by_sixteen<T>(C, a.rows, 4096), wave = by_wave<T>(C, a.rows, 1024);
   const int64_t teams = narrow ? 16 : wave ? 4 : 1;
   const int64_t most = 1 << 20;
   const int64_t blocks = (a.rows + teams - 1) / teams;
   const dim3 grid((unsigned)(blocks < most ? blocks : most)), block(256);
   if (narrow) {
     if (C <= 16 * 8) return launch_kernel(layer_norm_kernel<T, 16, 8>, grid, block, a, stream);
-    if (C <= 16 * 16) return launch_kernel(layer_norm_kernel<T, 16, 16>, grid, block, a, stream);
-    if (C <= 16 * 24) return launch_kernel(layer_norm_kernel<T, 16, 24>, grid, block, a, stream);
-    return launch_kernel(layer_norm_kernel<T, 16, 32>, grid, block, a, stream);
+    if constexpr (sizeof(T) == 2) {
+      if (C > 16 * 16) return launch_kernel(layer_norm_kernel<T, 16, 24>, grid, block, a, stream);
+    }
+    return launch_kernel(layer_norm_kernel<T, 16, 16>, grid, block, a, stream);
   }
   if (wave) {
     if (C <= 64 * 8) return launch_kernel(layer_norm_kernel<T, 64, 8>, grid, block, a, stream);
@@ -232,9 +250,10 @@ hipError_t layer_norm_t(const seq_layer_norm_args_t& a, hipStream_t stream) {
   return launch_kernel(layer_norm_kernel<T, 256, 64>, grid, block, a, stream);
 }
 
-bool grad_narrow(const seq_layer_norm_grad_args_t& a) { return a.channels <= kNarrow && a.rows >= 4096; }
-bool grad_by_wave(const seq_layer_norm_grad_args_t& a) {
-  return a.dtype == CONV_WGRAD_F32 ? by_wave<float>(a.channels) : by_wave<Bf16>(a.channels);
+// Lanes of a row's team in the gradient.
+template <typename T>
+int grad_team(const seq_layer_norm_grad_args_t& a) {
+  return by_sixteen<T>(a.channels, a.rows, 32768) ? 16 : by_wave<T>(a.channels, a.rows, 512) ? 64 : 256;
 }
 
 template <typename T>
@@ -242,13 +261,15 @@ hipError_t layer_norm_grad_t(const seq_layer_norm_grad_args_t& a, float* ws, hip
   const int64_t C = a.channels;
   const LayerNormGradArgs k{a, ws};
   const dim3 grid((unsigned)layer_norm_grad_parts(a)), block(256);
-  if (grad_narrow(a)) {
+  const int team = grad_team<T>(a);
+  if (team == 16) {
     if (C <= 16 * 8) return launch_kernel(layer_norm_grad_kernel<T, 16, 8>, grid, block, k, stream);
-    if (C <= 16 * 16) return launch_kernel(layer_norm_grad_kernel<T, 16, 16>, grid, block, k, stream);
-    if (C <= 16 * 24) return launch_kernel(layer_norm_grad_kernel<T, 16, 24>, grid, block, k, stream);
-    return launch_kernel(layer_norm_grad_kernel<T, 16, 32>, grid, block, k, stream);
+    if constexpr (sizeof(T) == 2) {
+      if (C > 16 * 16) return launch_kernel(layer_norm_grad_kernel<T, 16, 24>, grid, block, k, stream);
+    }
+    return launch_kernel(layer_norm_grad_kernel<T, 16, 16>, grid, block, k, stream);
   }
-  if (by_wave<T>(C)) {
+  if (team == 64) {
     if (C <= 64 * 8) return launch_kernel(layer_norm_grad_kernel<T, 64, 8>, grid, block, k, stream);
     if constexpr (sizeof(T) == 2) {
       if (C > 64 * 16) return launch_kernel(layer_norm_grad_kernel<T, 64, 32>, grid, block, k, stream);
@@ -274,13 +295,16 @@ hipError_t launch_layer_norm(const seq_layer_norm_args_t& a, hipStream_t stream)
   }
 }
 
-// Workgroups of the gradient, each with its own partial dw and db: as many as rows need, up to 2048 waves, or 4096 where
-// four share a row.
+// Workgroups of the gradient, each with its own partial dw and db: up to 256 as many as the rows need, then at least four
+// rows a team (1024 rows of 4096 channels in bf16: 18.2 us with 256 workgroups against 30.5 with 1024, whose sums take
+// longer to add than the rows), up to 512, or 1024 where the lanes' registers let more than two share a CU (16384 rows of
+// 1537 channels in fp32 82.3 against 87.9 us with 512; of 4096 in bf16 93.0 against 87.8).
 int layer_norm_grad_parts(const seq_layer_norm_grad_args_t& a) {
-  const int64_t teams = grad_narrow(a) ? 16 : grad_by_wave(a) ? 4 : 1;
-  const int64_t need = (a.rows + teams - 1) / teams;
-  const int64_t most = teams == 1 ? 1024 : 512;
-  return (int)(need < 1 ? 1 : need < most ? need : most);
+  const int teams = 256 / (a.dtype == CONV_WGRAD_F32 ? grad_team<float>(a) : grad_team<Bf16>(a));
+  const int64_t need = (a.rows + teams - 1) / teams, some = (need + 3) / 4;
+  const int64_t most = teams == 1 && a.channels <= 2048 ? 1024 : 512;
+  const int64_t parts = need <= 256 ? need : some < 256 ? 256 : some;
+  return (int)(parts < 1 ? 1 : parts < most ? parts : most);
 }
 
 hipError_t launch_layer_norm_grad(const seq_layer_norm_grad_args_t& a, float* ws, hipStream_t stream) {

@@ -39,7 +39,7 @@ def within(got, want, tol, what):
 # one row to many (teams of 256, 64 and 16 lanes), vectors cut short, the widest rows of each kernel
 SHAPES = [(1, 1), (3, 7), (5, 64), (1, 257), (1100, 300), (1030, 1024), (2, 1537), (1025, 2048), (2, 4100), (3, 8192),
           (2, 16384), (0, 64), (1, 16383), (4096, 1), (4099, 96), (5000, 130), (4111, 255), (4100, 384), (4097, 385),
-          (4098, 512), (4096, 513)]
+          (4098, 512), (4096, 513), (32769, 96), (32770, 130), (32768, 384)]
 
 
 @pytest.mark.parametrize("dtype", TYPES)
