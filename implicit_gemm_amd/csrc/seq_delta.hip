@@ -533,10 +533,25 @@ __global__ __launch_bounds__(512) void delta_kernel(DeltaArgs k) {
 }
 
 // ---- one token ----------------------------------------------------------------------------------------------------------
-// A workgroup has one sequence's head and up to 128 columns of its state, four to a lane; its 256 lanes are 32 / (columns
-// / 4) .. groups that share the state's rows.  The state is read once, held in registers between the two sums over its
-// rows, and written once.
-template <typename T, int LANES, int ROWS>
+// A workgroup has one sequence's head and up to 4 LANES columns of its state, four to a lane; its 256 lanes are groups of
+// LANES that share the state's rows.  The state is read once, held in registers between the two sums over its rows, and
+// written once: bound by HBM.
+//
+// States stream past the caches (64 sequences of 32 heads of 128 x 128, 268 MB a call, four sets in turn: 51.4 us against
+// 59.7 with ordinary loads and stores, a copy of the same size 49.9; 8 sequences of 16 heads 6.7 against 7.6): the next
+// token comes when the model's other layers have gone through the caches.  WHOLE: Dv is a multiple of 4, so that a lane
+// has all of its columns or none (without the branches for that 70.7 us became 59.7).
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ void stream_in(Raw<float, 4>& r, const float* p) {
+  const f32x4_u v = __builtin_nontemporal_load(reinterpret_cast<const f32x4_u*>(p));
+  const float f[4] = {v[0], v[1], v[2], v[3]};
+  r.pack(f);
+}
+__device__ __forceinline__ void stream_out(const Raw<float, 4>& r, float* p) {
+  __builtin_nontemporal_store(f32x4_u{r.get(0), r.get(1), r.get(2), r.get(3)}, reinterpret_cast<f32x4_u*>(p));
+}
+
+template <typename T, int LANES, int ROWS, bool WHOLE>
 __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs k) {
   constexpr int kGroups = 256 / LANES;
   __shared__ float sums[kGroups][LANES * 4 + 1];
@@ -564,8 +579,11 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs k) {
   for (int i = 0; i < ROWS; ++i) {
     const int row = g + i * kGroups;
     S[i].clear();
-    if (a.state && slot >= 0 && row < Dk && left > 0)
-      S[i].load_n(a.state + slot * a.state_stride + place + (int64_t)row * Dv, left);
+    if (a.state && slot >= 0 && row < Dk && left > 0) {
+      const float* from = a.state + slot * a.state_stride + place + (int64_t)row * Dv;
+      if constexpr (WHOLE) stream_in(S[i], from);
+      else S[i].load_n(from, left);
+    }
   }
   __syncthreads();
   // Sum over the rows of x S, in every lane; the groups' sums are added in order.
@@ -601,8 +619,11 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs k) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) t[e] = __builtin_fmaf(x, w[e], decay * S[i].get(e));
     S[i].pack(t);
-    if (a.state_out && slot >= 0 && row < Dk && left > 0)
-      S[i].store_n(a.state_out + slot * a.state_out_stride + place + (int64_t)row * Dv, left);
+    if (a.state_out && slot >= 0 && row < Dk && left > 0) {
+      float* to = a.state_out + slot * a.state_out_stride + place + (int64_t)row * Dv;
+      if constexpr (WHOLE) stream_out(S[i], to);
+      else S[i].store_n(to, left);
+    }
   }
   over_rows(query, o);
   if (g == 0) {
@@ -613,13 +634,20 @@ __global__ __launch_bounds__(256) void delta_step_kernel(DeltaArgs k) {
   }
 }
 
+template <typename T, int LANES, bool WHOLE>
+hipError_t step_n(const DeltaArgs& k, hipStream_t stream) {
+  const dim3 grid((unsigned)(k.a.tokens.sequences * k.a.heads * k.slices)), block(256);
+  constexpr int kGroups = 256 / LANES;
+  if (k.a.key_dim <= 64) return launch_kernel(delta_step_kernel<T, LANES, 64 / kGroups, WHOLE>, grid, block, k, stream);
+  if (k.a.key_dim <= 128) return launch_kernel(delta_step_kernel<T, LANES, 128 / kGroups, WHOLE>, grid, block, k, stream);
+  return launch_kernel(delta_step_kernel<T, LANES, 256 / kGroups, WHOLE>, grid, block, k, stream);
+}
+// 64 columns at most leave half of 32 lanes without work (64 sequences of 16 heads of 128 x 64: 12.6 us against 13.1; of 72 x
+// 41: 10.9 against 12.2).
 template <typename T>
 hipError_t step_t(const DeltaArgs& k, hipStream_t stream) {
-  const dim3 grid((unsigned)(k.a.tokens.sequences * k.a.heads * k.slices)), block(256);
-  // 32 lanes x 4 columns, 8 groups
-  if (k.a.key_dim <= 64) return launch_kernel(delta_step_kernel<T, 32, 8>, grid, block, k, stream);
-  if (k.a.key_dim <= 128) return launch_kernel(delta_step_kernel<T, 32, 16>, grid, block, k, stream);
-  return launch_kernel(delta_step_kernel<T, 32, 32>, grid, block, k, stream);
+  if (k.a.value_dim <= 64) return k.a.value_dim % 4 == 0 ? step_n<T, 16, true>(k, stream) : step_n<T, 16, false>(k, stream);
+  return k.a.value_dim % 4 == 0 ? step_n<T, 32, true>(k, stream) : step_n<T, 32, false>(k, stream);
 }
 
 template <typename T, int KP, int NT, bool WHOLE>
