@@ -322,3 +322,35 @@ def test_refusals(iga):
                 lambda: iga.gated_delta(*(torch.zeros(1, 2, 1, 257).cuda(),) * 2, v[:1, :2, :1], g[:1, :2, :1], beta[:1, :2, :1])):
         with pytest.raises((ValueError, TypeError, iga.ConvWgradError)):
             bad()
+
+
+# ---------------------------------------------------------------------------------------------------- as a model's layer
+
+@pytest.fixture(scope="module")
+def layer_module():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "delta_layer.py")
+    spec = importlib.util.spec_from_file_location("delta_layer", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("sizes", [dict(Hk=2, H=4, Dk=64, Dv=64), dict(Hk=1, H=3, Dk=40, Dv=24)])
+def test_layer_by_tokens_matches_prompts(layer_module, sizes, dtype):
+    """The delta rule's output is linear in queries, keys and values each, which three roundings to the element type
+    precede (projection, convolution, norm), and three follow (the rule's, the heads' norm's, the output's): 3 * 3 + 3
+    half steps on either side, 24 of the largest output in all, and the matrix products between them sum in other
+    orders: thirty-two."""
+    layer = layer_module.Layer(96, dtype=DT[dtype], seed=3, **sizes)
+    off = layer_module.steps_against_prompt(layer, [130, 5, 33, 17])
+    assert off <= max(32 * ref.half_step(DT[dtype]), 1e-5)
+
+
+def test_layer_gradient_against_difference(layer_module):
+    """Central differences of a float32 loss: the step's square and the losses' rounding (2^-24 of their terms over the
+    step) leave about a thousandth."""
+    slope, difference = layer_module.gradient_against_difference()
+    assert abs(slope - difference) <= 1e-2 * abs(difference)
