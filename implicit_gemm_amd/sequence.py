@@ -1,16 +1,22 @@
-"""Sequence operators: the root-mean-square norm, the short causal convolution over tokens and the selective state
-space scan, for prompts, for training (forward and gradients) and for single tokens.
+"""Sequence operators: the root-mean-square norm and the layer norm, the short causal convolution over tokens, the
+selective state space scan and the gated delta rule, for prompts, for training (forward and gradients) and for single
+tokens.
 
     y, h, r = rms_norm(x, w, residual)                     # and rms_norm_e4m3 for an 8-bit product behind it
+    y, h, m, r = layer_norm(x, w, b, residual)
+    dx, dw, db = layer_norm_grad(dy, h, w, m, r)
     y, window = causal_conv(x, w, b, silu=True)
     y, state, saved = selective_scan(u, delta, A, B, C, skip=D, z=z, delta_bias=bias, softplus=True, save=True)
     grads = selective_scan_grad(dy, u, delta, A, B, C, saved, skip=D, z=z, delta_bias=bias, softplus=True)
     y = selective_scan_step(u, delta, A, B, C, state, ...)  # one token of each sequence
+    o, state, saved = gated_delta(q, k, v, g, beta, save=True)
+    grads = gated_delta_grad(do, q, k, v, g, beta, saved)
+    o = gated_delta_step(q, k, v, g, beta, state)
 
-Tokens are rows and channels the contiguous last axis.  Sequences of one length come as [S, L, channels]; sequences of
-uneven lengths as [T, channels] with `offsets` (int32 [S + 1] on the GPU, offsets[0] = 0, not decreasing; rows from
+Tokens are rows and channels the contiguous last axis (of a head, where there are heads).  Sequences of one length come
+as [S, L, channels]; sequences of uneven lengths as [T, channels] with `offsets` (int32 [S + 1] on the GPU, offsets[0] = 0, not decreasing; rows from
 offsets[S] on are padding, whose outputs are zero).  float32, bfloat16 or float16 elements, float32 parameters (w, A,
-biases), float32 scan states; arithmetic and sums in float32.  Rows may be strided (a part of a wider projection).
+biases) and gates (g, beta), float32 states; arithmetic and sums in float32.  Rows may be strided (a part of a wider projection).
 
 States live in pools: `state` [P, ...] with `slots` (int32 [S] on the GPU) naming each sequence's place; without slots
 sequence s has place s.  A slot outside the pool stands for no state: it reads as zeros and is not written, as the rows
@@ -771,9 +777,12 @@ def gated_delta(q, k, v, g, beta, scale=None, offsets=None, slots=None, state=No
         S = e^g S;  S = S + beta k (v - S^T k)^T;  o = scale S^T q        (scale: Dk ** -0.5 by default)
 
     per token and head with a state S [Dk, Dv].  g is the logarithm of a decay (<= 0 as a rule), keys have unit length
-    as a rule.  Dk <= 256, Dv <= 1024.  Returns (o, state_out, saved).  `state` float32 [P, H, Dk, Dv] is where the
-    sequences begin (None: zeros) and state_out where their final states go: a new tensor by default or, with slots,
-    `state` itself; the two may be the same.  saved is for gated_delta_grad (None without save)."""
+    as a rule.  Dk <= 256, Dv <= 1024.  An element that is not finite makes its sequence's and head's later outputs NaN,
+    and may those of the up to 63 tokens before it.
+
+    Returns (o, state_out, saved).  `state` float32 [P, H, Dk, Dv] is where the sequences begin (None: zeros) and
+    state_out where their final states go: a new tensor by default or, with slots, `state` itself; the two may be the
+    same.  saved is for gated_delta_grad (None without save)."""
     on = _here(v, stream)
     if on is None:
         return _there(v, stream, gated_delta, q, k, v, g, beta, scale, offsets, slots, state, state_out, save)

@@ -409,9 +409,10 @@ conv_wgrad_status_t conv_wgrad_noalloc(const conv_wgrad_desc_t* desc, const void
                                        float* dw, float* db, void* stream);
 
 /* ------------------------------------------------------------------------------------------------------------------
- * Sequence operators: the root-mean-square norm, the short causal (depthwise) convolution over tokens and the selective
- * state space scan, which together with two matrix products make a layer of a sequence model.  Tokens are rows,
- * channels the contiguous axis; element types as above (desc dtype), arithmetic and every sum in fp32.
+ * Sequence operators: the root-mean-square norm and the layer norm, the short causal (depthwise) convolution over tokens,
+ * the selective state space scan and the gated delta rule, which together with two matrix products make a layer of a
+ * sequence model.  Tokens are rows, channels the contiguous axis; element types as above (desc dtype), arithmetic and
+ * every sum in fp32.
  *
  * Execution is as for the convolutions: validation is synchronous and comes before anything is enqueued, the kernels
  * go to `stream`, nothing is allocated, and results are bit-identical from run to run.  The one thing validation
