@@ -782,7 +782,7 @@ def gated_delta(q, k, v, g, beta, scale=None, offsets=None, slots=None, state=No
 
     Returns (o, state_out, saved).  `state` float32 [P, H, Dk, Dv] is where the sequences begin (None: zeros) and
     state_out where their final states go: a new tensor by default or, with slots, `state` itself; the two may be the
-    same.  saved is for gated_delta_grad (None without save)."""
+    same, and must not overlap otherwise.  saved is for gated_delta_grad (None without save)."""
     on = _here(v, stream)
     if on is None:
         return _there(v, stream, gated_delta, q, k, v, g, beta, scale, offsets, slots, state, state_out, save)

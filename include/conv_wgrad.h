@@ -669,7 +669,7 @@ conv_wgrad_status_t seq_selective_scan_grad(const seq_scan_grad_args_t* args, vo
  * elements between heads.  g, beta: fp32, element (b, t, h) at ptr + b * batch + t * row + h.  g is a logarithm, as a rule
  * <= 0 (-inf forgets); keys are as a rule of unit length (with beta |k|^2 > 2 the recurrence itself grows).
  * state, state_out: fp32 [pool][heads][key_dim][value_dim] (stride elements apart), NULL: zeros / not needed; they may be
- * the same.  save: NULL, or what seq_gated_delta_grad needs, seq_gated_delta_save bytes, 16-byte aligned.
+ * the same and do not overlap otherwise, nor do outputs and inputs.  save: NULL, or what seq_gated_delta_grad needs, seq_gated_delta_save bytes, 16-byte aligned.
  * 1 <= key_dim <= 256, 1 <= value_dim <= 1024, heads a multiple of key_heads and at most 65536.
  * Products and sums keep 32-bit accuracy for every element type.  A chunk of 64 tokens of a sequence is one system: an
  * infinite or NaN element makes its sequence's later outputs NaN, and may those of the up to 63 tokens before it in its

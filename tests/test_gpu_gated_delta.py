@@ -324,6 +324,67 @@ def test_refusals(iga):
             bad()
 
 
+def test_two_graphs_in_turn(iga):
+    """Two captured calls of other sizes, each with a workspace of its own, replayed in turn with eager calls between."""
+    def case(seed, L, H, Dk, Dv, dt):
+        inputs = [t.cuda() for t in make(seed, (2, L), H, H, Dk, Dv, dt)]
+
+        def call():
+            o, last, saved = iga.gated_delta(*inputs, save=True)
+            return (o, last) + tuple(iga.gated_delta_grad(o, *inputs, saved)[:5])
+        return call
+
+    calls = [case(41, 150, 2, 128, 64, torch.bfloat16), case(42, 70, 3, 72, 41, torch.float32)]
+    want = [[t.clone() for t in c()] for c in calls]
+    graphs, outs = [], []
+    for c in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(c())
+    for _ in range(3):
+        for g, c, o, w in zip(graphs, calls, outs, want):
+            g.replay()
+            again = c()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(w, o)) and all(torch.equal(a, b) for a, b in zip(w, again))
+
+
+def test_the_largest_sizes_against_parts_of_themselves(iga):
+    """Columns of v are independent of each other, and so are heads: calls of the most columns and of the most heads give
+    what calls of a part give."""
+    q, k, v, g, beta = (t.cuda() for t in make(15, (2, 70), 1, 1, 256, 1024, torch.bfloat16))
+    part = slice(992, 1024)
+    o, last, saved = iga.gated_delta(q, k, v, g, beta, save=True)
+    o1, last1, _ = iga.gated_delta(q, k, v[..., part].contiguous(), g, beta)
+    assert torch.equal(o[..., part], o1) and torch.equal(last[..., part], last1)
+    dv = iga.gated_delta_grad(o, q, k, v, g, beta, saved).dv
+    _, _, saved1 = iga.gated_delta(q, k, v[..., part].contiguous(), g, beta, save=True)
+    assert torch.equal(dv[..., part], iga.gated_delta_grad(o1, q, k, v[..., part].contiguous(), g, beta, saved1).dv)
+    one = [t[:, 0].contiguous() for t in (q, k, v, g, beta)]
+    a, b = last.clone(), last[..., part].contiguous()
+    y = iga.gated_delta_step(*one, a)
+    one[2] = one[2][..., part].contiguous()
+    # Up to 64 columns go to other teams of lanes, which add the 256 products of k S in another order: each order is off by
+    # at most 256 half steps of the sum of their sizes, the sums' w then enters the state times k, and the state's own two
+    # operations and w's three leave a half step of what they make each, on both sides.  o is one rounding to bf16 of sums
+    # of 256 such elements: two half steps of the largest and that.
+    y1 = iga.gated_delta_step(*one, b)
+    before, half = last[..., part].double(), 2.0 ** -24
+    k64 = one[1].double().abs()[..., None]                                     # [S, 1, Dk, 1], as the state
+    tol = 512 * half * k64 * (k64 * before.abs()).sum(-2, keepdim=True) + 16 * half * (b.double().abs() + before.abs())
+    assert bool(((a[..., part].double() - b.double()).abs() <= tol).all())
+    assert bool(((y1.double() - y[..., part].double()).abs() <= (2.0 ** -7 + 2.0 ** -12) * y.double().abs().max()).all())
+    H = 65536
+    q, k, v, g, beta = (t.cuda() for t in make(16, (1, 3), H, H, 2, 4, torch.float32))
+    o, last, saved = iga.gated_delta(q, k, v, g, beta, save=True)
+    d = iga.gated_delta_grad(o, q, k, v, g, beta, saved)
+    few = [t[:, :, -5:] for t in (q, k, v, g, beta)]
+    o1, last1, saved1 = iga.gated_delta(*few, save=True)
+    d1 = iga.gated_delta_grad(o1, *few, saved1)
+    assert torch.equal(o[:, :, -5:], o1) and torch.equal(last[:, -5:], last1)
+    assert all(torch.equal(a[:, :, -5:], b) for a, b in zip(d[:5], d1[:5]))
+
+
 # ---------------------------------------------------------------------------------------------------- as a model's layer
 
 @pytest.fixture(scope="module")

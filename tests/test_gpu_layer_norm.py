@@ -174,3 +174,26 @@ def test_runs_repeat_bit_for_bit_on_any_stream_and_in_a_graph(iga):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(eager, out))
+
+
+def test_more_rows_than_workgroups_past_4_gib(iga):
+    """2^20 + 5 rows of 4112 bytes, more than there are workgroups at most, against a part of themselves."""
+    R, C = (1 << 20) + 5, 2056
+    x = torch.randn(R, C, device="cuda", dtype=torch.bfloat16)
+    w, b = torch.randn(C, device="cuda"), torch.randn(C, device="cuda")
+    y, h, m, r = iga.layer_norm(x, w, b)
+    dx, dw, db = iga.layer_norm_grad(y, h, w, m, r)
+    for part in (slice(0, 3), slice(R - 7, R)):
+        y1, _, m1, r1 = iga.layer_norm(x[part], w, b)
+        assert torch.equal(y[part], y1) and torch.equal(m[part], m1) and torch.equal(r[part], r1)
+        dx1 = iga.layer_norm_grad(y[part], x[part], w, m1, r1)[0]
+        # the two calls' teams are of other sizes and add s1 and s2 in another order: a step of dx's type at most
+        top = dx1.float().abs().amax(1, keepdim=True)
+        assert bool(((dx[part].float() - dx1.float()).abs() <= 2 * half_step(torch.bfloat16) * top).all())
+    want = torch.zeros(C, dtype=torch.float64, device="cuda")
+    for i in range(0, R, 1 << 17):
+        want += y[i:i + (1 << 17)].double().sum(0)
+    # random signs: the partial sums' roundings stay below 2^-24 of the largest of them, which is under 8 sqrt(rows) times
+    # the values' deviation, for each of a lane's 1025 additions and the 1024 joins
+    size = 8 * R ** 0.5 * y[:4096].double().std(0) + want.abs()
+    assert bool(((db.double() - want).abs() <= 2050 * EPS32 * size).all())
