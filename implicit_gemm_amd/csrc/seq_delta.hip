@@ -531,8 +531,14 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, 
   }
 }
 
+// Four waves a SIMD, that is two workgroups a CU, wherever they fit without spills: fp16 keys of 65 .. 127 dimensions would
+// take 129 registers when they save (8192 tokens of 16 heads of 100 x 100: 220 us against 288; the others have at most 128
+// by themselves, or, fp32 over 64 and all over 128 dimensions, far more).
+template <class Lds, int KP>
+constexpr int walk_waves() { return KP <= 128 && KP * Lds::N <= 256 ? 4 : 2; }
+
 template <typename T, int KP, int NT, bool SAVE, bool WHOLE>
-__global__ __launch_bounds__(512) void delta_kernel(DeltaArgs k) {
+__global__ __launch_bounds__(512, (walk_waves<WalkLds<T, KP, NT>, KP>())) void delta_kernel(DeltaArgs k) {
   typedef WalkLds<T, KP, NT> Lds;
   __shared__ __attribute__((aligned(16))) char bytes[sizeof(Lds)];
   Lds& L = *reinterpret_cast<Lds*>(bytes);

@@ -197,7 +197,7 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
         }
     }
     load_decay(next);
-    load_square(next);
+    if (N == 1) load_square(next);
     // dS
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -224,6 +224,10 @@ __device__ __forceinline__ void back_chain(const DeltaArgs& k, const Walk& w, Ba
       }
 #pragma unroll
       for (int t = 0; t < NT; ++t) S[m][t] = total(sum[t]);
+    }
+    if (N > 1) {                     // fp32 and fp16 K take their pieces' registers: only now are enough free
+      __builtin_amdgcn_sched_barrier(0);
+      load_square(next);
     }
     share_state();
     lds_barrier();
@@ -372,8 +376,13 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
   }
 }
 
+// Two workgroups a CU where they fit without spills, as in the forward: fp16 keys of 65 .. 128 dimensions would take up to
+// 139 registers (8192 tokens of 16 heads of 100 x 100, the whole gradient: 520 us against 603; of 128 x 128 448 against 480).
+template <class Lds, int KP>
+constexpr int back_waves() { return KP <= 128 && KP * Lds::N <= 256 ? 4 : 2; }
+
 template <typename T, int KP, int NT, bool WHOLE>
-__global__ __launch_bounds__(512) void delta_back_kernel(DeltaArgs k) {
+__global__ __launch_bounds__(512, (back_waves<BackLds<T, KP, NT>, KP>())) void delta_back_kernel(DeltaArgs k) {
   typedef BackLds<T, KP, NT> Lds;
   __shared__ __attribute__((aligned(16))) char bytes[sizeof(Lds)];
   Lds& L = *reinterpret_cast<Lds*>(bytes);
