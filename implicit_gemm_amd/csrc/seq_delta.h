@@ -15,8 +15,8 @@
 //
 // Numbers.  The products run on the bf16 matrix instructions.  A 32-bit number is held as up to three bf16 pieces whose
 // sum it is (24 bits), a product of two such numbers is the six products of pieces above 2^-24 of it, all summed in 32
-// bits; bf16 inputs are one piece, fp16 ones two (exact).  So states, corrections and sums keep 32-bit accuracy from
-// chunk to chunk at a sixth to a third of the bf16 rate, two and a half to five times the fp32 instructions' rate.
+// bits; bf16 inputs are one piece, fp16 ones two (exact).  So states, corrections, outputs and sums keep 32-bit accuracy
+// from chunk to chunk at a sixth to a third of the bf16 rate, two and a half to five times the fp32 instructions' rate.
 #pragma once
 
 #include "seq_common.h"
@@ -38,11 +38,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 template <typename T>
 struct ElemPieces {
   static constexpr int n = __is_same(T, Bf16) ? 1 : __is_same(T, F16) ? 2 : kPieces;
-};
-// Pieces that are enough for a product that is rounded to T: 16 bits of accuracy for 8 or 11.
-template <typename T>
-struct OutPieces {
-  static constexpr int n = sizeof(T) == 4 ? kPieces : 2;
 };
 
 struct DeltaArgs {

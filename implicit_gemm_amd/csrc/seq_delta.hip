@@ -198,14 +198,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void delta_chunk_kerne
       fi[i] = GRAD ? I[c][row] : I[row][c];
       fp[i] = GRAD ? M[c][row] : M[row][c];
     }
-    constexpr int NP = GRAD ? kPieces : OutPieces<T>::n;
-    s16x8 pi[kPieces], pp[NP];
+    s16x8 pi[kPieces], pp[kPieces];
     split8<kPieces>(fi, pi);
-    split8<NP>(fp, pp);
+    split8<kPieces>(fp, pp);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) *reinterpret_cast<s16x8*>(&at_lane(inv + (b * kPieces + i) * kFragElems, lane * 8)) = pi[i];
-#pragma unroll
-    for (int i = 0; i < NP; ++i) *reinterpret_cast<s16x8*>(&at_lane(inn + (b * kPieces + i) * kFragElems, lane * 8)) = pp[i];
+    for (int i = 0; i < kPieces; ++i) {
+      *reinterpret_cast<s16x8*>(&at_lane(inv + (b * kPieces + i) * kFragElems, lane * 8)) = pi[i];
+      *reinterpret_cast<s16x8*>(&at_lane(inn + (b * kPieces + i) * kFragElems, lane * 8)) = pp[i];
+    }
   }
 }
 
@@ -224,15 +224,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void delta_chunk_kerne
 // loads are one chunk ahead.
 template <typename T, int KP, int NT>
 struct WalkLds {
-  static constexpr int N = ElemPieces<T>::n, NO = OutPieces<T>::n;
+  static constexpr int N = ElemPieces<T>::n;
   Operand<KP> S[kPieces][NT];
-  Operand<kChunk> X[kPieces][NT], W[kPieces][NT], Z[NO][NT];
+  Operand<kChunk> X[kPieces][NT], W[kPieces][NT], Z[kPieces][NT];
   Staged<T, KP> K;
 };
 template <typename T, int KP, int NT, bool SAVE, bool WHOLE>
 __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, WalkLds<T, KP, NT>& L, int r, int lane) {
   typedef WalkLds<T, KP, NT> Lds;
-  constexpr int N = Lds::N, NO = Lds::NO, KS = KP / 32, MT = KP / 64;
+  constexpr int N = Lds::N, KS = KP / 32, MT = KP / 64;
   const seq_delta_args_t& a = k.a;
   const int lr = lane & 15, lg = lane >> 4, heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
   const int64_t slot = pool_slot(a.tokens.slots, a.tokens.pool, w.seq);
@@ -384,10 +384,9 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
       split4<kPieces>(x, u);
 #pragma unroll
       for (int i = 0; i < kPieces; ++i) L.W[i][t].four(16 * r + 4 * lg, lr) = u[i];
-      u32x2 uz[NO];
-      split4<NO>(z[t], uz);
+      split4<kPieces>(z[t], u);
 #pragma unroll
-      for (int i = 0; i < NO; ++i) L.Z[i][t].four(16 * r + 4 * lg, lr) = uz[i];
+      for (int i = 0; i < kPieces; ++i) L.Z[i][t].four(16 * r + 4 * lg, lr) = u[i];
     }
     lds_barrier();
     if (SAVE) {
@@ -442,11 +441,11 @@ __device__ __forceinline__ void walk_chain(const DeltaArgs& k, const Walk& w, Wa
 template <typename T, int KP, int NT, bool WHOLE>
 __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, WalkLds<T, KP, NT>& L, int r, int lane) {
   typedef WalkLds<T, KP, NT> Lds;
-  constexpr int N = Lds::N, NO = Lds::NO, KS = KP / 32;
+  constexpr int N = Lds::N, KS = KP / 32;
   const seq_delta_args_t& a = k.a;
   const int lr = lane & 15, lg = lane >> 4, heads = (int)a.heads, Dk = a.key_dim, Dv = a.value_dim;
   Eight<T> rows[KS];
-  s16x8 square[2][NO];
+  s16x8 square[2][kPieces];
   float4 first;
   auto queries = [&](int j) __attribute__((always_inline)) {
     return ChunkRows<const T>(a.q, w.key_head * a.q_head, w.p, kChunk * j);
@@ -460,7 +459,7 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, 
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int i = 0; i < NO; ++i)
+      for (int i = 0; i < kPieces; ++i)
         square[c][i] = *reinterpret_cast<const s16x8*>(&at_lane(from + (lower_frag(r, min(c, r / 2)) * kPieces + i) * kFragElems, lane * 8));
   };
   auto load_decay = [&](int j) __attribute__((always_inline)) {
@@ -476,7 +475,7 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, 
   for (int j = 0; j < w.chunks; ++j) {
     const int n = w.p.len - kChunk * j;
     const int next = min(j + 1, w.chunks - 1);
-    f32x4 o[NT][NO];
+    f32x4 o[NT][kPieces];
 #pragma unroll
     for (int t = 0; t < NT; ++t) clear(o[t]);
 #pragma unroll
@@ -485,10 +484,10 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, 
       rows[c].pieces(e);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        s16x8 b[NO];
+        s16x8 b[kPieces];
 #pragma unroll
-        for (int i = 0; i < NO; ++i) b[i] = L.S[i][t].eight(c, lane);
-        mfma_pieces<NO>(e, b, o[t]);
+        for (int i = 0; i < kPieces; ++i) b[i] = L.S[i][t].eight(c, lane);
+        mfma_pieces<kPieces>(e, b, o[t]);
       }
     }
     lds_barrier();
@@ -508,10 +507,10 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, 
 #pragma unroll
       for (int c = 0; c < 2; ++c)
         if (c <= r / 2) {
-          s16x8 b[NO];
+          s16x8 b[kPieces];
 #pragma unroll
-          for (int i = 0; i < NO; ++i) b[i] = L.Z[i][t].eight(c, lane);
-          mfma_pieces<NO>(square[c], b, o[t]);
+          for (int i = 0; i < kPieces; ++i) b[i] = L.Z[i][t].eight(c, lane);
+          mfma_pieces<kPieces>(square[c], b, o[t]);
         }
     load_square(next);
     const ChunkRows<T> out(a.o, (int64_t)w.head * Dv, w.p, kChunk * j);
