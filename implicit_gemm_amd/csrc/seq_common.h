@@ -163,6 +163,12 @@ __device__ __forceinline__ float team_reduce(float v, float* lds) {
   return v;
 }
 
+// An integer that the compiler cannot see through: keeps what is computed from it inside of a loop.
+__device__ __forceinline__ int opaque(int v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
 // Orders a wave's LDS accesses before and after it.  The LDS serves one wave's accesses in order, so this costs nothing.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

@@ -133,11 +133,6 @@ struct ChunkRows {
       : base(row_at<T>(v, p, t0) + head), row((uint32_t)v.row) {}
   __device__ __forceinline__ T& at(int token, int c) const { return at_lane(base, (int)(token * row + c)); }
 };
-// An integer that the compiler cannot see through: keeps what is computed from it inside of a loop.
-__device__ __forceinline__ int opaque(int v) {
-  asm("" : "+v"(v));
-  return v;
-}
 
 // ---- matrix instructions ----------------------------------------------------------------------------------------------
 // 16 x 16 += 16 x 32 times 32 x 16.  Lane l holds row (column) l % 16 and terms 8 (l / 16) .. + 7 of an operand, column

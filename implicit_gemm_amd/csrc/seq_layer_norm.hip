@@ -7,7 +7,9 @@
 // Both are bound by HBM: a row is read once, kept in registers between its reductions and its outputs, and written once
 // (bf16, 16384 rows of 2048 with a residual: 50.9 us for 268 MB, 5.3 TB/s, the gradient 47.3 + 4.7 for its partial sums;
 // 200704 rows of 384: 60.6 us for 308 MB, the gradient 98.1 + 4.8 for 462).
-// The squares are summed about the mean, from the registers, so that a mean far above the deviation costs no bits.  A
+// The mean is the sum over channels and then, from the registers, the mean of what it leaves: the first sum's rounding is
+// 2^-24 of the values, which may be any number of deviations (a row of 10000.1 throughout: y off by 0.3 with the sum alone).
+// The squares are summed about both.  The gradient finds the rest of the mean, that its 32 bits leave, from h likewise.  A
 // row belongs to a team of 16 lanes (four rows a wave: feature maps of few channels), of 64, of 256, or of 1024 for the
 // widest gradients; each lane holds up to 64 elements in 16-byte vectors, and a team of at most a wave needs no barrier.
 #include "seq_common.h"
@@ -29,6 +31,25 @@ template <bool WHOLE, typename T, int V>
 __device__ __forceinline__ void give(const Raw<T, V>& r, T* p, int n) {
   if constexpr (WHOLE) r.store(p);
   else r.store_n(p, n);
+}
+
+// The sums of N values over a team, with 3 TEAM / 64 floats of lds for a team of more than a wave.
+template <int TEAM, int N>
+__device__ __forceinline__ void team_sums(float (&v)[N], float* lds) {
+  static_assert(N <= 3, "size of lds");
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = lanes_reduce<AddOp>(v[i], TEAM < 64 ? TEAM : 64);
+  if constexpr (TEAM > 64) {
+    constexpr int kWaves = TEAM / 64;
+    __syncthreads();  // the last reduction's reads are done
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) lds[i * kWaves + (threadIdx.x >> 6)] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lanes_reduce<AddOp>(lds[i * kWaves + threadIdx.x % kWaves], kWaves);
+  }
 }
 
 template <typename T, int TEAM, int NE, bool WHOLE>
@@ -77,19 +98,27 @@ __global__ __launch_bounds__(256) void layer_norm_kernel(seq_layer_norm_args_t a
 #pragma unroll
       for (int i = 0; i < V; ++i) sum += raw[v].get(i);
     const float mean = team_reduce<AddOp, TEAM>(sum, lds) / (float)C;
+    float left = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int n = C - (v * TEAM + lane) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) left += (WHOLE ? 0 : i) < n ? raw[v].get(i) - mean : 0.f;
+    }
+    const float rest = team_reduce<AddOp, TEAM>(left, lds) / (float)C;
     float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int n = C - (v * TEAM + lane) * V;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float d = i < n ? raw[v].get(i) - mean : 0.f;
+        const float d = (WHOLE ? 0 : i) < n ? (raw[v].get(i) - mean) - rest : 0.f;
         ss = __builtin_fmaf(d, d, ss);
       }
     }
     const float r = 1.f / sqrtf(team_reduce<AddOp, TEAM>(ss, lds) / (float)C + a.eps);
     if (lane == 0) {
-      if (a.mean) a.mean[row] = mean;
+      if (a.mean) a.mean[row] = mean + rest;
       if (a.rstd) a.rstd[row] = r;
     }
     T* y = static_cast<T*>(a.y) + row * C;
@@ -104,7 +133,7 @@ __global__ __launch_bounds__(256) void layer_norm_kernel(seq_layer_norm_args_t a
         Raw<T, V> o;
         float s[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[i] = __builtin_fmaf((raw[v].get(i) - mean) * r, w.get(i), b.get(i));
+        for (int i = 0; i < V; ++i) s[i] = __builtin_fmaf(((raw[v].get(i) - mean) - rest) * r, w.get(i), b.get(i));
         o.pack(s);
         give<WHOLE>(o, y + c, C - c);
       }
@@ -120,7 +149,7 @@ struct LayerNormGradArgs {
 template <typename T, int TEAM, int NE, bool WHOLE>
 __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_grad_kernel(LayerNormGradArgs args) {
   constexpr int V = 16 / sizeof(T), NV = NE / V, kThreads = TEAM > 256 ? TEAM : 256, kTeams = kThreads / TEAM;
-  __shared__ float lds[TEAM > 64 ? TEAM / 64 : 2 * TEAM * NE];
+  __shared__ float lds[TEAM > 64 ? 3 * TEAM / 64 : 2 * TEAM * NE];
   const seq_layer_norm_grad_args_t& a = args.a;
   const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
   const int C = (int)a.channels;
@@ -156,17 +185,20 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_grad_kerne
     }
     const float mean = a.mean[row], r = a.rstd[row];
     // Channels past the end have dy = w = 0; their n is a number that no output takes.
-    float s1 = 0.f, s2 = 0.f;
+    float sums[3] = {0.f, 0.f, 0.f};       // of g, g (h - mean) and h - mean
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+    for (int v = 0; v < NV; ++v) {
+      const int n = opaque(C - (v * TEAM + lane) * V);     // no masks kept over the rows' loop
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float g = dy[v].get(i) * w[v][i];
-        s1 += g;
-        s2 = __builtin_fmaf(g, h[v].get(i) - mean, s2);
+        const float g = dy[v].get(i) * w[v][i], c = h[v].get(i) - mean;
+        sums[0] += g;
+        sums[1] = __builtin_fmaf(g, c, sums[1]);
+        sums[2] += (WHOLE ? 0 : i) < n ? c : 0.f;
       }
-    s1 = team_reduce<AddOp, TEAM>(s1, lds) / (float)C;
-    s2 = team_reduce<AddOp, TEAM>(s2, lds) * r / (float)C;
+    }
+    team_sums<TEAM>(sums, lds);
+    const float rest = sums[2] / (float)C, s1 = sums[0] / (float)C, s2 = (sums[1] - rest * sums[0]) * r / (float)C;
     T* dx = static_cast<T*>(a.dx) + row * C;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -175,7 +207,7 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_grad_kerne
       float s[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float d = dy[v].get(i), n = (h[v].get(i) - mean) * r;
+        const float d = dy[v].get(i), n = ((h[v].get(i) - mean) - rest) * r;
         s[i] = __builtin_fmaf(r, __builtin_fmaf(d, w[v][i], -s1) - n * s2, dh[v].get(i));
         accw[v][i] = __builtin_fmaf(d, n, accw[v][i]);
         accb[v][i] += d;
