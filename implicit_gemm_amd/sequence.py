@@ -729,13 +729,19 @@ def _delta_pool(state, state_out, slots, S, each, index):
     return _dense(slots, "slots", (S,), torch.int32, index), P, at + to
 
 
+def _delta_keys(q, v):
+    """(key heads, Dk) of q beside v."""
+    H = v.shape[-2]
+    if q.dim() != v.dim() or q.shape[-2] < 1 or H % q.shape[-2]:
+        raise ValueError("q and k must be [..., key heads, Dk] with key heads dividing %d, got %s" % (H, tuple(q.shape)))
+    return q.shape[-2:]
+
+
 def _delta_args(q, k, v, g, beta, scale, offsets, slots, state, state_out, S, L, step, index):
     """The arguments of seq_delta_args_t up to save."""
     shape, dtype = v.shape, v.dtype
     H, Dv = shape[-2:]
-    if q.dim() != len(shape) or q.shape[-2] < 1 or H % q.shape[-2]:
-        raise ValueError("q and k must be [..., key heads, Dk] with key heads dividing %d, got %s" % (H, tuple(q.shape)))
-    Hk, Dk = q.shape[-2:]
+    Hk, Dk = _delta_keys(q, v)
     keys, flat = shape[:-2] + (Hk, Dk), shape[:-1]
     qs, ks, vs = _like(q, "q", keys, dtype, index), _like(k, "k", keys, dtype, index), _like(v, "v", shape, dtype, index)
     gs, bs = _like(g, "g", flat, _f32, index), _like(beta, "beta", flat, _f32, index)
@@ -790,9 +796,10 @@ def gated_delta(q, k, v, g, beta, scale=None, offsets=None, slots=None, state=No
     S, L = _delta_rows(v, offsets)
     shape = v.shape
     H, Dv = shape[-2:]
-    state_out = _default_out(state_out, slots, state, S, (H, q.shape[-1], Dv), _f32, v)
+    Hk, Dk = _delta_keys(q, v)
+    keep, n = _delta_space(S, L, offsets is not None, H, Hk, Dk, Dv, _code(v))     # refuses sizes before they are allocated
+    state_out = _default_out(state_out, slots, state, S, (H, Dk, Dv), _f32, v)
     args = _delta_args(q, k, v, g, beta, scale, offsets, slots, state, state_out, S, L, False, index)
-    keep, n = _delta_space(S, L, offsets is not None, H, *args[6:10])
     o = _same(v)
     saved = _empty(keep // 4, _f32, v) if save else None
     ws = _empty(n, torch.uint8, v)
