@@ -669,11 +669,15 @@ conv_wgrad_status_t seq_selective_scan_grad(const seq_scan_grad_args_t* args, vo
  * elements between heads.  g, beta: fp32, element (b, t, h) at ptr + b * batch + t * row + h.  g is a logarithm, as a rule
  * <= 0 (-inf forgets); keys are as a rule of unit length (with beta |k|^2 > 2 the recurrence itself grows).
  * state, state_out: fp32 [pool][heads][key_dim][value_dim] (stride elements apart), NULL: zeros / not needed; they may be
- * the same and do not overlap otherwise, nor do outputs and inputs.  save: NULL, or what seq_gated_delta_grad needs, seq_gated_delta_save bytes, 16-byte aligned.
+ * the same and do not overlap otherwise, nor do outputs and inputs.  save: NULL, or what seq_gated_delta_grad needs,
+ * seq_gated_delta_save bytes, 16-byte aligned.
  * 1 <= key_dim <= 256, 1 <= value_dim <= 1024, heads a multiple of key_heads and at most 65536.
- * Products and sums keep 32-bit accuracy for every element type.  A chunk of 64 tokens of a sequence is one system: an
- * infinite or NaN element makes its sequence's later outputs NaN, and may those of the up to 63 tokens before it in its
- * chunk; other sequences and heads are not touched.
+ * States, products and sums keep 32-bit accuracy for every element type.  What an infinite or NaN element reaches: of q its
+ * own token's output; of v its column of the head's outputs from its token on, and of the state; of k, beta and g (-inf is
+ * none, it forgets) all of the head's outputs from its token on, and the state; of the state its column of all the
+ * sequence's outputs.  As a chunk of 64 tokens of a sequence is one system, those of v, k, beta and g may reach the up to
+ * 63 tokens before theirs in the chunk as well.  In a gradient each, and those of dout, may reach all tokens of the sequence
+ * and head (dq and dk of the key head).  Other sequences and heads are not touched.
  */
 typedef struct seq_delta_args {
   seq_tokens_t tokens;
