@@ -5,8 +5,11 @@
 //   with n = (h - m) r and g = dy w:  dx = r (g - mean(g) - n mean(g n)) + dh,  dw = sum dy n,  db = sum dy over rows
 //
 // Both are bound by HBM: a row is read once, kept in registers between its reductions and its outputs, and written once
-// (bf16, 16384 rows of 2048 with a residual: 50.9 us for 268 MB, 5.3 TB/s, the gradient 47.3 + 4.7 for its partial sums;
-// 200704 rows of 384: 60.6 us for 308 MB, the gradient 98.1 + 4.8 for 462).
+// (bf16, 16384 rows of 2048 with a residual: 49.5 us for 268 MB, 5.4 TB/s, the gradient 46.3 + 4.7 for its partial sums;
+// 200704 rows of 384: 55.2 us for 308 MB, the gradient 97.3 + 4.8 for 462; calls on 16384 rows of 8192: 118 us for 537 MB,
+// the gradient 162 for 805; on 8192 of 16384: 111 and 178; fp32, 8192 of 8192: 102 and 164).  Not so fp32 rows of more than
+// 8192 channels forward, whose 64 elements a lane leave registers for one wave a SIMD: 4096 of 16384 153 us for 537 MB, of
+// 16383 205.
 // The mean is the sum over channels and then, from the registers, the mean of what it leaves: the first sum's rounding is
 // 2^-24 of the values, which may be any number of deviations (a row of 10000.1 throughout: y off by 0.3 with the sum alone).
 // The squares are summed about both.  The gradient finds the rest of the mean, that its 32 bits leave, from h likewise.  A
@@ -18,10 +21,10 @@ namespace cw {
 
 namespace {
 
-// WHOLE: the channels are a multiple of the vector, so that none is cut short and the branches for that go.  bf16, the
-// operands of three calls in turn, forward and gradient: 6007 rows of 4096 channels with a residual 80.1 us against 87.5,
-// 200704 rows of 384 158.3 against 172.2.  (Non-temporal stores of y and dx bring the latter to 136.8 us, but y then
-// takes its reader longer: forward and an elementwise use of y 112.4 us against 108.1.)
+// WHOLE: the channels are a multiple of the vector, so that none is cut short and the branches for that go.  bf16, forward
+// and gradient in a captured graph: 6007 rows of 4096 channels with a residual 66.3 us against 72.5, 200704 rows of 384 155.8
+// against 176.0.  (Non-temporal stores of y and dx brought the latter from 158 to 137 us, but y then took its reader longer:
+// forward and an elementwise use of y 112.4 us against 108.1.)
 template <bool WHOLE, typename T, int V>
 __device__ __forceinline__ void take(Raw<T, V>& r, const T* p, int n) {
   if constexpr (WHOLE) r.load(p);
@@ -31,6 +34,14 @@ template <bool WHOLE, typename T, int V>
 __device__ __forceinline__ void give(const Raw<T, V>& r, T* p, int n) {
   if constexpr (WHOLE) r.store(p);
   else r.store_n(p, n);
+}
+
+// Channels from a vector on: hidden from the compiler where vectors are cut short, so that it keeps no masks of their
+// elements from one loop over a row to the next (fp32, 4096 rows of 16383 channels: 205 us against 231; the same for whole
+// vectors of 16384 167 against 150).
+template <bool WHOLE>
+__device__ __forceinline__ int left_of(int n) {
+  return WHOLE ? n : opaque(n);
 }
 
 // The sums of N values over a team, with 3 TEAM / 64 floats of lds for a team of more than a wave.
@@ -101,7 +112,7 @@ __global__ __launch_bounds__(256) void layer_norm_kernel(seq_layer_norm_args_t a
     float left = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int n = C - (v * TEAM + lane) * V;
+      const int n = left_of<WHOLE>(C - (v * TEAM + lane) * V);
 #pragma unroll
       for (int i = 0; i < V; ++i) left += (WHOLE ? 0 : i) < n ? raw[v].get(i) - mean : 0.f;
     }
@@ -109,7 +120,7 @@ __global__ __launch_bounds__(256) void layer_norm_kernel(seq_layer_norm_args_t a
     float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int n = C - (v * TEAM + lane) * V;
+      const int n = left_of<WHOLE>(C - (v * TEAM + lane) * V);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float d = (WHOLE ? 0 : i) < n ? (raw[v].get(i) - mean) - rest : 0.f;
@@ -250,31 +261,33 @@ __global__ __launch_bounds__(TEAM > 256 ? TEAM : 256) void layer_norm_grad_kerne
   }
 }
 
-// Which team.  Times of a call in us, forward / gradient, the operands in the last-level cache up to 256 MB:
+// Which team.  Times of a call in us, forward / gradient, in a captured graph, the operands in the last-level cache up to
+// 256 MB:
 //
 // 16 lanes against a wave, bf16        8192 rows            65536 rows           131072 rows
-//   128 channels                     3.6 /  9.3 against    11.4 / 17.8 against
-//                                    4.7 /  9.1            21.2 / 33.5
-//   384                              5.8 / 16.3 against    26.4 / 36.7 against  45.4 / 61.7 against
-//                                    6.0 / 10.2            27.2 / 34.9          50.5 / 84.2
-//   512                              7.0 / 20.2 against    33.4 / 46.9 against  60.3 / 88.7 against
-//                                    6.7 / 10.8            31.0 / 39.8          60.1 / 89.3
-// (fp32 by bytes: 256 channels as bf16's 512.)  Rows of up to 768 bytes go to 16 lanes where there are enough of them.
+//   128 channels                     3.3 /  8.8 against     8.5 / 17.8 against  15.1 / 25.2 against
+//                                    4.9 /  9.3            21.8 / 38.8          39.1 / 71.5
+//   384                              4.7 / 15.2 against    19.6 / 35.6 against  33.5 / 58.9 against
+//                                    5.4 / 10.6            27.0 / 40.9          49.1 / 95.4
+//   512                              5.5 / 18.5 against    24.5 / 45.7 against  44.4 / 88.8 against
+//                                    5.7 / 10.8            27.9 / 42.3          52.8 / 99.5
+// (fp32 by bytes: 256 channels as bf16's 512.)  Rows of up to 768 bytes go to 16 lanes where there are enough of them; of
+// 1024 bytes they would gain forward and lose in the gradient up to 65536 rows.
 //
 // A wave against 256 lanes, bf16        256 rows             1024 rows            8192 rows            65536 rows
-//   512 channels                     3.7 /  6.7 against    3.7 /  7.1 against   6.7 / 10.8 against   32.8 /  38.6 against
-//                                    3.7 /  6.8            4.3 / 10.7          11.3 / 21.6           64.3 / 111.7
-//   2048                             3.9 / 10.3 against    6.1 / 13.0 against  21.7 / 28.9 against  130.3 / 156.5 against
-//                                    3.9 /  9.2            5.2 / 20.3          19.7 / 29.7          138.3 / 166.5
+//   512 channels                     2.9 /  6.0 against    3.0 /  6.4 against   5.7 / 10.9 against   28.5 /  42.4 against
+//                                    3.4 /  6.2            4.0 /  8.6          12.2 / 25.0           74.3 / 174.8
+//   2048                             4.1 /  8.8 against    4.6 / 11.0 against  15.5 / 25.3 against  107.4 / 155.7 against
+//                                    3.5 /  8.0            4.4 / 11.2          16.9 / 31.6          126.8 / 225.6
 template <typename T>
 constexpr bool by_sixteen(int64_t C, int64_t rows, int64_t least) { return C * (int64_t)sizeof(T) <= 768 && rows >= least; }
 template <typename T>
-constexpr bool by_wave(int64_t C, int64_t rows, int64_t least) { return C * (int64_t)sizeof(T) <= 4096 && rows >= least; }
+constexpr bool by_wave(int64_t C, int64_t rows) { return C * (int64_t)sizeof(T) <= 4096 && rows >= 1024; }
 
 template <typename T, bool WHOLE>
 hipError_t layer_norm_t(const seq_layer_norm_args_t& a, hipStream_t stream) {
   const int64_t C = a.channels;
-  const bool narrow = by_sixteen<T>(C, a.rows, 4096), wave = by_wave<T>(C, a.rows, 1024);
+  const bool narrow = by_sixteen<T>(C, a.rows, 4096), wave = by_wave<T>(C, a.rows);
   const int64_t teams = narrow ? 16 : wave ? 4 : 1;
   const int64_t most = 1 << 20;
   const int64_t blocks = (a.rows + teams - 1) / teams;
@@ -302,7 +315,7 @@ hipError_t layer_norm_t(const seq_layer_norm_args_t& a, hipStream_t stream) {
 // Lanes of a row's team in the gradient.
 template <typename T>
 int grad_team(const seq_layer_norm_grad_args_t& a) {
-  return by_sixteen<T>(a.channels, a.rows, 32768) ? 16 : by_wave<T>(a.channels, a.rows, 512) ? 64 : 256;
+  return by_sixteen<T>(a.channels, a.rows, 32768) ? 16 : by_wave<T>(a.channels, a.rows) ? 64 : 256;
 }
 
 template <typename T, bool WHOLE>
@@ -354,15 +367,14 @@ hipError_t launch_layer_norm(const seq_layer_norm_args_t& a, hipStream_t stream)
 }
 
 // Workgroups of the gradient, each with its own partial dw and db: up to 256 as many as the rows need, then at least four
-// rows a team (1024 rows of 4096 channels in bf16: 18.2 us with 256 workgroups against 30.5 with 1024, whose sums take
-// longer to add than the rows), up to 512, or 1024 where the lanes' registers let more than two share a CU (16384 rows of
-// 1537 channels in fp32 82.3 against 87.9 us with 512; of 4096 in bf16 93.0 against 87.8).
+// rows a team (1024 rows of 4096 channels in bf16: 15.5 us with 256 workgroups against 23.9 with 1024, whose sums take
+// longer to add than the rows), up to 512 (against 1024 and 256: 16384 rows of 4096 channels in bf16 86.8 against 89.0 and
+// 120.5 us, 65536 of 2048 in fp32 295 against 337 and 370, 200704 of 384 in bf16 forward and gradient 156 against 166 and 170).
 int layer_norm_grad_parts(const seq_layer_norm_grad_args_t& a) {
   const int teams = 256 / (a.dtype == CONV_WGRAD_F32 ? grad_team<float>(a) : grad_team<Bf16>(a));
   const int64_t need = (a.rows + teams - 1) / teams, some = (need + 3) / 4;
-  const int64_t most = teams == 1 && a.channels <= 2048 ? 1024 : 512;
   const int64_t parts = need <= 256 ? need : some < 256 ? 256 : some;
-  return (int)(parts < 1 ? 1 : parts < most ? parts : most);
+  return (int)(parts < 1 ? 1 : parts < 512 ? parts : 512);
 }
 
 hipError_t launch_layer_norm_grad(const seq_layer_norm_grad_args_t& a, float* ws, hipStream_t stream) {
