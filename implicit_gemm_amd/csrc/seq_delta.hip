@@ -7,8 +7,8 @@ namespace cw {
 namespace {
 
 // ---- the chunks' systems ----------------------------------------------------------------------------------------------
-// Bound by HBM and the write path where there are many chunks (8192 tokens of 32 heads of 128 in bf16: 144 MB read and 122
-// written in 61 us, 4.4 TB/s; what is written are the systems, which the walk's slices of columns, eight there, then share).
+// Bound by HBM and the write path where there are many chunks (8192 tokens of 32 heads of 128 in bf16: 151 MB read and 153
+// written in 62 us, 4.9 TB/s; what is written are the systems, which the walk's slices of columns, eight there, then share).
 // One workgroup a chunk and head.  Wave r multiplies rows 16 r .. of K and Q with K of the tiles before it; (1 + M)^-1
 // comes from its 16 x 16 diagonal blocks, each solved row by row by one wave, doubled twice: the block below the diagonal
 // of [[A, 0], [C, B]]^-1 is -B^-1 C A^-1, in 32-bit matrix products.
@@ -42,8 +42,8 @@ union ChunkLds {
   } squares;
 };
 
-// EIGHTS: Dk is a multiple of 8, so that no load has a branch (the long prompt, with the walk's WHOLE for Dk = KP: 312 us
-// against 375 without both).
+// EIGHTS: Dk is a multiple of 8, so that no load has a branch (the long prompt, with the walk's WHOLE for Dk = KP: 302 us
+// in a captured graph against 344 without both).
 template <typename T, bool GRAD, bool EIGHTS>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void delta_chunk_kernel(DeltaArgs k) {
   constexpr int N = ElemPieces<T>::n;
@@ -211,11 +211,13 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 3 : 2) void delta_chunk_kerne
 
 // ---- the chunks of a sequence in order ------------------------------------------------------------------------------
 // Bound by the chain's latency: a chunk is three products that wait for each other, each behind an exchange through LDS.
-// 8192 tokens of 32 heads of 128 x 128 in bf16 are 128 chunks in 247 us (1.9 us a chunk; the chain alone 1.4, with its loads
-// 1.65), with one workgroup a CU, the vector ALU 26 %, LDS 30 % and the matrix units 18 % busy.  So the chain has waves of its own, nothing that waits for memory between two exchanges, and operands
-// in LDS in the order that a wave reads them.  Measured and slower: the state only in registers with partial sums of K S
-// exchanged (315 against 262 us then), 32 columns a workgroup (spills).  4 x 2048 tokens of
-// 16 heads, two workgroups a CU: 97 us, and 167 with the 240 MB that the gradient needs (kept by columns in 16-byte stores:
+// 8192 tokens of 32 heads of 128 x 128 in bf16 are 128 chunks in 265 us (2.1 us a chunk; the chain alone 1.4, with its loads
+// 1.65), with one workgroup a CU, the vector ALU 26 %, LDS 29 % and the matrix units 19 % busy.  So the chain has waves of
+// its own, nothing that waits for memory between two exchanges, and operands in LDS in the order that a wave reads them.
+// Outputs take all three pieces of S, P and Z (two, 16 bits, took 246 us and left 0.3 % of bf16 and 1.9 % of fp16 outputs a
+// step off).  Measured and slower: the state only in registers with partial sums of K S exchanged (315 against 262 us then),
+// 32 columns a workgroup (spills), Q S after the first exchange (half of it 275 us against 274, all 288).  4 x 2048 tokens of
+// 16 heads, two workgroups a CU: 120 us, and 172 with the 240 MB that the gradient needs (kept by columns in 16-byte stores:
 // no change).
 //
 // A workgroup has 16 NT columns of one sequence's and head's state.  Waves 0 .. 3 walk the chain: wave r has the
@@ -531,8 +533,9 @@ __device__ __forceinline__ void walk_outputs(const DeltaArgs& k, const Walk& w, 
 }
 
 // Four waves a SIMD, that is two workgroups a CU, wherever they fit without spills: fp16 keys of 65 .. 127 dimensions would
-// take 129 registers when they save (8192 tokens of 16 heads of 100 x 100: 220 us against 288; the others have at most 128
-// by themselves, or, fp32 over 64 and all over 128 dimensions, far more).
+// take 129 registers when they save (4 x 2048 tokens of 16 heads of 100 x 100, a saving call in a captured graph: 242 us
+// against 307; of one sequence of 8192, which leaves CUs empty, 552 against 526; the others have at most 128 by themselves,
+// or, fp32 over 64 and all over 128 dimensions, far more).
 template <class Lds, int KP>
 constexpr int walk_waves() { return KP <= 128 && KP * Lds::N <= 256 ? 4 : 2; }
 

@@ -377,7 +377,7 @@ __device__ __forceinline__ void back_beside(const DeltaArgs& k, const Walk& w, B
 }
 
 // Two workgroups a CU where they fit without spills, as in the forward: fp16 keys of 65 .. 128 dimensions would take up to
-// 139 registers (8192 tokens of 16 heads of 100 x 100, the whole gradient: 520 us against 603; of 128 x 128 448 against 480).
+// 139 registers (4 x 2048 tokens of 16 heads of 100 x 100, the whole gradient: 520 us against 603; of 128 x 128 448 against 480).
 template <class Lds, int KP>
 constexpr int back_waves() { return KP <= 128 && KP * Lds::N <= 256 ? 4 : 2; }
 

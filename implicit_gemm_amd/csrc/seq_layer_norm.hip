@@ -5,8 +5,8 @@
 //   with n = (h - m) r and g = dy w:  dx = r (g - mean(g) - n mean(g n)) + dh,  dw = sum dy n,  db = sum dy over rows
 //
 // Both are bound by HBM: a row is read once, kept in registers between its reductions and its outputs, and written once
-// (bf16, 16384 rows of 2048 with a residual: 49.5 us for 268 MB, 5.4 TB/s, the gradient 46.3 + 4.7 for its partial sums;
-// 200704 rows of 384: 55.2 us for 308 MB, the gradient 97.3 + 4.8 for 462; calls on 16384 rows of 8192: 118 us for 537 MB,
+// (bf16, 16384 rows of 2048 with a residual: 48.6 us for 268 MB, 5.5 TB/s, the gradient 46.1 + 4.7 for its partial sums;
+// 200704 rows of 384: 54.7 us for 308 MB, the gradient 97.6 + 4.8 for 462; calls on 16384 rows of 8192: 118 us for 537 MB,
 // the gradient 162 for 805; on 8192 of 16384: 111 and 178; fp32, 8192 of 8192: 102 and 164).  Not so fp32 rows of more than
 // 8192 channels forward, whose 64 elements a lane leave registers for one wave a SIMD: 4096 of 16384 153 us for 537 MB, of
 // 16383 205.

@@ -14,9 +14,10 @@ tokens.
     o = gated_delta_step(q, k, v, g, beta, state)
 
 Tokens are rows and channels the contiguous last axis (of a head, where there are heads).  Sequences of one length come
-as [S, L, channels]; sequences of uneven lengths as [T, channels] with `offsets` (int32 [S + 1] on the GPU, offsets[0] = 0, not decreasing; rows from
-offsets[S] on are padding, whose outputs are zero).  float32, bfloat16 or float16 elements, float32 parameters (w, A,
-biases) and gates (g, beta), float32 states; arithmetic and sums in float32.  Rows may be strided (a part of a wider projection).
+as [S, L, channels]; sequences of uneven lengths as [T, channels] with `offsets` (int32 [S + 1] on the GPU, offsets[0] =
+0, not decreasing; rows from offsets[S] on are padding, whose outputs are zero).  float32, bfloat16 or float16 elements,
+float32 parameters (w, A, biases) and gates (g, beta), float32 states; arithmetic and sums in float32.  Rows may be strided
+(a part of a wider projection).
 
 States live in pools: `state` [P, ...] with `slots` (int32 [S] on the GPU) naming each sequence's place; without slots
 sequence s has place s.  A slot outside the pool stands for no state: it reads as zeros and is not written, as the rows
@@ -833,7 +834,9 @@ def gated_delta_step(q, k, v, g, beta, state, scale=None, slots=None, state_out=
 def gated_delta_grad(do, q, k, v, g, beta, saved, scale=None, offsets=None, slots=None, state=None, dstate_out=None,
                      stream=None):
     """Gradients of gated_delta, from do, its inputs and its `saved`: a DeltaGrads tuple.  dstate_out float32 [S, H, Dk,
-    Dv]: the gradient of the final states; dstate is that of the first ones, in the order of the sequences."""
+    Dv]: the gradient of the final states; dstate is that of the first ones, in the order of the sequences.  dg is a sum in
+    which what a token writes itself cancels: it is good to 32 bits of those terms (|do| |o| and |dv| |v| of its chunk), so that
+    a dg of zero, as of a first token without a state, comes out as their rounding."""
     on = _here(v, stream)
     if on is None:
         return _there(v, stream, gated_delta_grad, do, q, k, v, g, beta, saved, scale, offsets, slots, state, dstate_out)
