@@ -783,10 +783,11 @@ def gated_delta(q, k, v, g, beta, scale=None, offsets=None, slots=None, state=No
 
         S = e^g S;  S = S + beta k (v - S^T k)^T;  o = scale S^T q        (scale: Dk ** -0.5 by default)
 
-    per token and head with a state S [Dk, Dv].  g is the logarithm of a decay (<= 0 as a rule), keys have unit length
-    as a rule.  Dk <= 256, Dv <= 1024.  An element that is not finite reaches its token's output (q), its column of the
-    head's outputs from its token on (v), all of them (k, beta, and g but for -inf), or its column of all outputs of the
-    sequence (state); v, k, beta and g possibly also the up to 63 tokens before theirs.
+    per token and head with a state S [Dk, Dv].  g is the logarithm of a decay (<= 0 as a rule; else results have 32 bits of
+    what 64 tokens would grow to by their g alone), keys have unit length as a rule.  Dk <= 256, Dv <= 1024.  An element
+    that is not finite reaches its token's output (q), its column of the head's outputs from its token on (v), all of them
+    (k, beta, and g but for -inf), or its column of all outputs of the sequence (state); v, k, beta and g possibly also the
+    up to 63 tokens before theirs.
 
     Returns (o, state_out, saved).  `state` float32 [P, H, Dk, Dv] is where the sequences begin (None: zeros) and
     state_out where their final states go: a new tensor by default or, with slots, `state` itself; the two may be the

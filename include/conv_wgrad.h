@@ -672,7 +672,9 @@ conv_wgrad_status_t seq_selective_scan_grad(const seq_scan_grad_args_t* args, vo
  * the same and do not overlap otherwise, nor do outputs and inputs.  save: NULL, or what seq_gated_delta_grad needs,
  * seq_gated_delta_save bytes, 16-byte aligned.
  * 1 <= key_dim <= 256, 1 <= value_dim <= 1024, heads a multiple of key_heads and at most 65536.
- * States, products and sums keep 32-bit accuracy for every element type.  What an infinite or NaN element reaches: of q its
+ * States, products and sums keep 32-bit accuracy for every element type; where g > 0, of what a chunk of 64 tokens would grow
+ * to by its g alone (a growth that beta k k^T takes back in every direction, as with key_dim 1, leaves e^(sum of g) 2^-24 of
+ * it).  What an infinite or NaN element reaches: of q its
  * own token's output; of v its column of the head's outputs from its token on, and of the state; of k, beta and g (-inf is
  * none, it forgets) all of the head's outputs from its token on, and the state; of the state its column of all the
  * sequence's outputs.  As a chunk of 64 tokens of a sequence is one system, those of v, k, beta and g may reach the up to

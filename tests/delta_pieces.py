@@ -96,7 +96,7 @@ CASES = [
     ((130, 130), 1, 4, 128, 64, "usual"), ((65, 0, 130), 2, 4, 64, 64, "usual"), ((129, 1, 66), 1, 2, 128, 32, "usual"),
     ((129,), 1, 4, 256, 64, "usual"), ((70,), 1, 1, 200, 130, "usual"), ((130, 130), 2, 4, 72, 41, "usual"),
     ((300,), 1, 2, 64, 32, "alike"), ((257,), 1, 1, 128, 64, "alike"), ((4096,), 1, 1, 16, 16, "slow"),
-    ((2500,), 1, 2, 64, 32, "slow")]
+    ((2500,), 1, 2, 64, 32, "slow"), ((130, 65), 1, 2, 64, 32, "growing")]
 
 
 def unit(t):
@@ -105,7 +105,8 @@ def unit(t):
 
 def inputs(case, dt):
     """Packed rows q, k, v, g, beta, state, do, dlast on the CPU in their types.  alike: keys a tenth apart and beta next to
-    one, so that each token's correction takes back most of the last one's.  slow: a memory of thousands of tokens."""
+    one, so that each token's correction takes back most of the last one's.  slow: a memory of thousands of tokens.  growing: states
+    that grow tenfold in some thirty tokens."""
     lens, Hk, H, Dk, Dv, kind = case
     rand = torch.Generator().manual_seed(sum(lens) * 31 + Dk * 7 + Dv)
     r = lambda *s: torch.randn(*s, generator=rand)  # noqa: E731
@@ -117,6 +118,8 @@ def inputs(case, dt):
     beta = torch.sigmoid(b + 4) if kind == "alike" else torch.sigmoid(b)
     if kind == "slow":
         g, beta = g * 1e-3, beta * 0.01
+    if kind == "growing":
+        g = 0.05 - 0.05 * g.clamp(min=-1)
     return ([unit(q).to(dt), unit(k).to(dt), v.to(dt), g, beta, 0.3 * r(S, H, Dk, Dv)], r(T, H, Dv).to(dt),
             0.3 * r(S, H, Dk, Dv))
 
